@@ -1,0 +1,381 @@
+// gq_norm.cu -- layer norm over the rows of a matrix: forward (optionally writing the 8-bit checkpoint
+// of its input in the same pass) and backward (from the input or from its checkpoint), with the
+// reduction of the weight's and bias's gradients over the rows.
+//
+//   forward   mean = sum x / C;  var = sum (x - mean)^2 / C;  rstd = 1 / sqrt(var + eps);
+//             y = (x - mean) rstd gamma + beta.
+//   backward  xh = (x - mean) rstd, g = dy gamma;
+//             dx = rstd (g - sum g / C - xh sum(g xh) / C);
+//             dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy.
+// Sums are binary32.  The squares are summed around the mean, not as sum x^2 - (sum x)^2 / C, which
+// cancels for rows whose mean is large against their spread.
+#include "gq_act.cuh"
+#include "gq_act.h"
+#include "gq_internal.h"
+
+namespace gq {
+namespace {
+
+constexpr unsigned kFullMask = 0xffffffffu;
+
+struct Params {
+    int64_t rows;
+    int cols;
+    const void *x, *dy;
+    void *y;             // y or dx
+    int64_t sx, sdy, sy;
+    Ckpt k;              // codes NULL: none
+    const void *gamma, *beta;
+    int params_f32;      // gamma and beta are float32, else the tensors' type
+    float *mean, *rstd;
+    float eps;
+    float *part_g, *part_b;
+    int parts;
+};
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+// A lane's 8 values of gamma or beta (fill where there is none).
+template <typename T, bool VEC>
+__device__ __forceinline__ void param_load(float (&v)[8], const void *p, int f32, float fill, int base, int lane, int cols)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = chunk_col<VEC>(base, lane, j);
+        v[j] = fill;
+        if (p && c < cols) v[j] = f32 ? __ldg(static_cast<const float *>(p) + c) : to_f(static_cast<const T *>(p)[c]);
+    }
+}
+
+// Sum over the G warps that share a row; `buf` holds one float per warp.  One barrier: the caller
+// alternates buffers, so a buffer is written again only after a later barrier.
+__device__ __forceinline__ float row_sum(float v, float *buf, int G, int warp, int lane)
+{
+    v = warp_sum(v);
+    if (G == 1) return v;
+    if (lane == 0) buf[warp] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int i = 0; i < G; ++i) s += buf[i];
+    return s;
+}
+
+// One block per row at a time, any number of columns; the row is read three times (twice from cache).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Params p)
+{
+    __shared__ float buf[2][16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = blockDim.x >> 5;
+    const float inv_c = 1.0f / (float)p.cols;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T *x = static_cast<const T *>(p.x) + row * p.sx;
+        T *y = static_cast<T *>(p.y) + row * p.sy;
+        float s = 0.0f;
+        for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
+            Raw<T> r;
+            float v[8];
+            chunk_load<T, VEC>(r, x, base, lane, p.cols);
+            to_floats(r, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[j];
+        }
+        const float mean = row_sum(s, buf[0], G, warp, lane) * inv_c;
+        float ss = 0.0f;
+        for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
+            Raw<T> r;
+            float v[8];
+            chunk_load<T, VEC>(r, x, base, lane, p.cols);
+            to_floats(r, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = chunk_col<VEC>(base, lane, j) < p.cols ? v[j] - mean : 0.0f;
+                ss = __fmaf_rn(d, d, ss);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum(ss, buf[1], G, warp, lane) * inv_c + p.eps);
+        for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
+            Raw<T> r;
+            float v[8], g[8], b[8];
+            chunk_load<T, VEC>(r, x, base, lane, p.cols);
+            to_floats(r, v);
+            if (p.k.codes) ckpt_store<VEC>(v, p.k, row, base, lane);
+            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            param_load<T, VEC>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn((v[j] - mean) * rstd, g[j], b[j]);
+            from_floats(r, v);
+            chunk_store<T, VEC>(r, y, base, lane, p.cols);
+        }
+        if (threadIdx.x == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+    }
+}
+
+// A lane's 8 values of the input, from the input or its checkpoint.
+template <typename T, bool VEC>
+__device__ __forceinline__ void input_load(float (&v)[8], const Params &p, int64_t row, int base, int lane)
+{
+    if (p.x) {
+        Raw<T> r;
+        chunk_load<T, VEC>(r, static_cast<const T *>(p.x) + row * p.sx, base, lane, p.cols);
+        to_floats(r, v);
+    } else {
+        RawCkpt<VEC> r;
+        ckpt_load<VEC>(r, p.k, row, base, lane);
+        ckpt_floats<VEC>(r, v);
+    }
+}
+
+// dx for any number of columns, one block per row.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(512) k_backward_rows_any(const __grid_constant__ Params p)
+{
+    __shared__ float buf[2][16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = blockDim.x >> 5;
+    const float inv_c = 1.0f / (float)p.cols;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T *dy = static_cast<const T *>(p.dy) + row * p.sdy;
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
+            Raw<T> r;
+            float x[8], d[8], g[8];
+            chunk_load<T, VEC>(r, dy, base, lane, p.cols);
+            to_floats(r, d);
+            input_load<T, VEC>(x, p, row, base, lane);
+            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (chunk_col<VEC>(base, lane, j) >= p.cols) continue;
+                const float gd = g[j] * d[j];
+                s0 += gd;
+                s1 = __fmaf_rn(gd, (x[j] - mean) * rstd, s1);
+            }
+        }
+        const float c0 = row_sum(s0, buf[0], G, warp, lane) * inv_c;
+        const float c1 = row_sum(s1, buf[1], G, warp, lane) * inv_c;
+        for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
+            Raw<T> r;
+            float x[8], d[8], g[8];
+            chunk_load<T, VEC>(r, dy, base, lane, p.cols);
+            to_floats(r, d);
+            input_load<T, VEC>(x, p, row, base, lane);
+            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                d[j] = rstd * __fmaf_rn(-(x[j] - mean) * rstd, c1, __fmaf_rn(g[j], d[j], -c0));
+            from_floats(r, d);
+            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
+        }
+    }
+}
+
+// Partial sums over the rows: warp (chunk c, part q) walks rows q, q + parts, ...
+template <typename T, bool VEC, bool NORM>
+__global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int base = ((int)blockIdx.x * 4 + warp) * kChunk;
+    if (base >= p.cols) return;
+    float sg[8], sb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sg[j] = sb[j] = 0.0f;
+    for (int64_t row = blockIdx.y; row < p.rows; row += p.parts) {
+        Raw<T> r;
+        float d[8];
+        chunk_load<T, VEC>(r, static_cast<const T *>(p.dy) + row * p.sdy, base, lane, p.cols);
+        to_floats(r, d);
+        if constexpr (NORM) {
+            float x[8];
+            input_load<T, VEC>(x, p, row, base, lane);
+            const float mean = p.mean[row], rstd = p.rstd[row];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sg[j] = __fmaf_rn(d[j], (x[j] - mean) * rstd, sg[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sb[j] += d[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = chunk_col<VEC>(base, lane, j);
+        if (c >= p.cols) continue;
+        const int64_t o = (int64_t)blockIdx.y * p.cols + c;
+        if (NORM) p.part_g[o] = sg[j];
+        p.part_b[o] = sb[j];
+    }
+}
+
+// Column sums of the partial rows, in a fixed order: 8 warps take 8 interleaved sets of rows of 32
+// columns, and their sums are added in warp order.
+__global__ void __launch_bounds__(256) k_parts_reduce(const float *part0, const float *part1, int64_t parts, int cols,
+                                                      float *out0, float *out1, int accumulate)
+{
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float *part = blockIdx.y ? part1 : part0;
+    float *out = blockIdx.y ? out1 : out0;
+    if (!out) return;
+    const int c = (int)blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (c < cols)
+        for (int64_t q = warp; q < parts; q += 8) v += part[q * cols + c];
+    s[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += s[i][lane];
+        out[c] = accumulate ? out[c] + v : v;
+    }
+}
+
+Params params(const NormArgs &a)
+{
+    Params p;
+    p.rows = a.rows;
+    p.cols = (int)a.cols;
+    p.x = a.x.p;
+    p.sx = a.x.stride;
+    p.dy = a.dy.p;
+    p.sdy = a.dy.stride;
+    p.y = const_cast<void *>(a.y.p);
+    p.sy = a.y.stride;
+    const CkptLayout l = ckpt_layout(a.rows, a.cols);
+    p.k = Ckpt{static_cast<uint8_t *>(a.ckpt), a.ckpt ? static_cast<uint8_t *>(a.ckpt) + l.exps_off : nullptr,
+               (int)l.code_pitch, (int)l.exp_pitch};
+    p.gamma = a.gamma;
+    p.beta = a.beta;
+    p.params_f32 = a.param_dtype == GQ_FLOAT32;
+    p.mean = a.mean;
+    p.rstd = a.rstd;
+    p.eps = a.eps;
+    p.part_g = a.parts;
+    p.parts = (int)norm_parts(a.rows, a.cols);
+    p.part_b = a.parts ? a.parts + (int64_t)p.parts * a.cols : nullptr;
+    return p;
+}
+
+bool rows_aligned(int64_t rows, const Mat &m, int per16) { return !m.p || rows == 1 || m.stride % per16 == 0; }
+
+template <typename T>
+cudaError_t forward(const NormArgs &a, cudaStream_t s)
+{
+    const int per16 = 16 / (int)sizeof(T);
+    const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16);
+    const Params p = params(a);
+    const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
+    const int warps = chunks < 16 ? (int)chunks : 16;
+    auto kern = vec ? k_forward_any<T, true> : k_forward_any<T, false>;
+    int per_sm = 0, sms = 0;
+    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = a.rows < (int64_t)per_sm * sms ? a.rows : (int64_t)per_sm * sms;
+    kern<<<(unsigned)grid, warps * 32, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward(const NormArgs &a, cudaStream_t s)
+{
+    const int per16 = 16 / (int)sizeof(T);
+    const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16) && rows_aligned(a.rows, a.dy, per16);
+    const Params p = params(a);
+    if (a.rows > 0) {
+        const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
+        const int warps = chunks < 16 ? (int)chunks : 16;
+        auto kern = vec ? k_backward_rows_any<T, true> : k_backward_rows_any<T, false>;
+        int per_sm = 0, sms = 0;
+        cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
+        if (e != cudaSuccess) return e;
+        const int64_t grid = a.rows < (int64_t)per_sm * sms ? a.rows : (int64_t)per_sm * sms;
+        kern<<<(unsigned)grid, warps * 32, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        if (a.dgamma || a.dbeta) {
+            auto ck = vec ? k_cols<T, true, true> : k_cols<T, false, true>;
+            ck<<<dim3((unsigned)((chunks + 3) / 4), (unsigned)p.parts), 128, 0, s>>>(p);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
+    }
+    if (!a.dgamma && !a.dbeta) return cudaSuccess;
+    return launch_parts_reduce(p.part_g, p.part_b, p.parts, a.cols, a.dgamma, a.dbeta, a.accumulate, s);
+}
+
+template <typename T>
+cudaError_t colsum(int64_t rows, int64_t cols, Mat dy, float *parts, cudaStream_t s)
+{
+    Params p = {};
+    p.rows = rows;
+    p.cols = (int)cols;
+    p.dy = dy.p;
+    p.sdy = dy.stride;
+    p.part_b = parts;
+    p.parts = (int)colsum_parts(rows, cols);
+    const int64_t chunks = (cols + kChunk - 1) / kChunk;
+    auto ck = rows_aligned(rows, dy, 16 / (int)sizeof(T)) ? k_cols<T, true, false> : k_cols<T, false, false>;
+    ck<<<dim3((unsigned)((chunks + 3) / 4), (unsigned)p.parts), 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_parts(int64_t rows, int64_t cols)
+{
+    (void)cols;
+    return rows < 296 ? rows : 296;
+}
+
+int64_t colsum_parts(int64_t rows, int64_t cols)
+{
+    (void)cols;
+    return rows < 128 ? rows : 128;
+}
+
+cudaError_t launch_norm_forward(const NormArgs &a, cudaStream_t stream)
+{
+    if (a.dtype == GQ_FLOAT32) return forward<float>(a, stream);
+    if (a.dtype == GQ_BFLOAT16) return forward<__nv_bfloat16>(a, stream);
+    return forward<__half>(a, stream);
+}
+
+cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t stream)
+{
+    if (a.dtype == GQ_FLOAT32) return backward<float>(a, stream);
+    if (a.dtype == GQ_BFLOAT16) return backward<__nv_bfloat16>(a, stream);
+    return backward<__half>(a, stream);
+}
+
+cudaError_t launch_colsum(int dtype, int64_t rows, int64_t cols, Mat dy, float *parts, float *out, int accumulate,
+                          cudaStream_t stream)
+{
+    if (rows > 0) {
+        const cudaError_t e = dtype == GQ_FLOAT32    ? colsum<float>(rows, cols, dy, parts, stream)
+                              : dtype == GQ_BFLOAT16 ? colsum<__nv_bfloat16>(rows, cols, dy, parts, stream)
+                                                     : colsum<__half>(rows, cols, dy, parts, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_parts_reduce(parts, nullptr, rows > 0 ? colsum_parts(rows, cols) : 0, cols, out, nullptr, accumulate,
+                               stream);
+}
+
+cudaError_t launch_parts_reduce(const float *part0, const float *part1, int64_t parts, int64_t cols, float *out0,
+                                float *out1, int accumulate, cudaStream_t stream)
+{
+    k_parts_reduce<<<dim3((unsigned)((cols + 31) / 32), out1 ? 2u : 1u), 256, 0, stream>>>(part0, part1, parts, (int)cols,
+                                                                                        out0, out1, accumulate);
+    return cudaGetLastError();
+}
+
+}  // namespace gq

@@ -19,6 +19,11 @@ SCHEMES = {"qsgd": GQ_QSGD, "terngrad": GQ_TERNGRAD, "bingrad_b": GQ_BINGRAD_B,
            "qsgd_l2": GQ_QSGD_L2, "terngrad_layer": GQ_TERNGRAD_LAYER}
 
 
+GQ_FLOAT32, GQ_BFLOAT16, GQ_FLOAT16 = range(3)
+GQ_FN_GELU, GQ_FN_GELU_TANH, GQ_FN_SILU = range(3)
+FUNCTIONS = {"gelu": GQ_FN_GELU, "gelu_tanh": GQ_FN_GELU_TANH, "silu": GQ_FN_SILU}
+
+
 class gq_config_t(ctypes.Structure):
     _fields_ = [("scheme", ctypes.c_int32), ("levels", ctypes.c_int32), ("bucket", ctypes.c_int32),
                 ("workers", ctypes.c_int32), ("error_feedback", ctypes.c_int32),
@@ -67,6 +72,18 @@ def lib():
         L.gq_elias_used_bytes.argtypes = [cfgp, ctypes.c_uint64, ctypes.POINTER(sz)]
         L.gq_elias_pack.argtypes = [cfgp, vp, vp, vp]
         L.gq_elias_unpack.argtypes = [cfgp, vp, vp, vp]
+        i64, ci = ctypes.c_int64, ctypes.c_int
+        L.gq_act_layout.argtypes = [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.gq_act_pack.argtypes = [ci, i64, i64, vp, i64, vp, vp]
+        L.gq_act_unpack.argtypes = [ci, i64, i64, vp, vp, i64, vp]
+        L.gq_act_fn_forward.argtypes = [ci, ci, i64, i64, vp, i64, vp, i64, vp, vp]
+        L.gq_act_fn_backward.argtypes = [ci, ci, i64, i64, vp, vp, i64, vp, i64, vp]
+        L.gq_act_weight_grad_workspace.argtypes = [ci, i64, i64, i64, i64, ci, ctypes.POINTER(sz)]
+        L.gq_act_weight_grad.argtypes = [ci, i64, i64, i64, vp, vp, i64, vp, i64, vp, ci, vp, sz, vp]
+        L.gq_layer_norm_forward.argtypes = [ci, ci, i64, i64, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, vp, vp]
+        L.gq_layer_norm_workspace.argtypes = [i64, i64, ctypes.POINTER(sz)]
+        L.gq_layer_norm_backward.argtypes = [ci, ci, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, ci, vp,
+                                             sz, vp]
         L.gq_status_string.argtypes = [ctypes.c_int]
         L.gq_status_string.restype = ctypes.c_char_p
         L.gq_version.restype = ctypes.c_char_p
@@ -75,7 +92,9 @@ def lib():
                   "gq_plan_status", "gq_plan_set_segments", "gq_plan_message_layout", "gq_plan_set_format",
                   "gq_selftest_bounded_wait", "gq_entropy_layout", "gq_entropy_pack",
                   "gq_entropy_unpack", "gq_elias_layout", "gq_elias_used_bytes", "gq_elias_pack",
-                  "gq_elias_unpack"):
+                  "gq_elias_unpack", "gq_act_layout", "gq_act_pack", "gq_act_unpack", "gq_act_fn_forward",
+                  "gq_act_fn_backward", "gq_act_weight_grad_workspace", "gq_act_weight_grad",
+                  "gq_layer_norm_forward", "gq_layer_norm_workspace", "gq_layer_norm_backward"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -224,6 +243,221 @@ def gq_elias_pack(cfg, msg, emsg, stream=None):
 
 def gq_elias_unpack(cfg, emsg, msg, stream=None):
     _check(lib().gq_elias_unpack(ctypes.byref(cfg), _ptr(emsg), _ptr(msg), _stream(stream)), "gq_elias_unpack")
+
+
+# ---------------------------------------------------------------------------------------------
+# activations kept in 8 bits: these take tensors, whose sizes, strides and types are the arguments
+# ---------------------------------------------------------------------------------------------
+_dtypes = None
+
+
+def _dtype(t, what):
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: GQ_FLOAT32, torch.bfloat16: GQ_BFLOAT16, torch.float16: GQ_FLOAT16}
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise TypeError("%s: float32, bfloat16 or float16 expected, got %s" % (what, t.dtype))
+    return d
+
+
+def _matrix(t, what, dtype=None, shape=None):
+    """(pointer, row stride) of a 2-D tensor whose columns are adjacent."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s: a 2-D tensor with adjacent columns expected, got shape %s, strides %s"
+                         % (what, tuple(t.shape), t.stride()))
+    if dtype is not None and _dtype(t, what) != dtype:
+        raise TypeError("%s: its type differs from the other tensors' (%s)" % (what, t.dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s: shape %s expected, got %s" % (what, shape, tuple(t.shape)))
+    return t.data_ptr(), t.stride(0)
+
+
+def _vector(t, what, n, dtype=GQ_FLOAT32):
+    """Pointer of a contiguous vector of n values (None: NULL)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: a contiguous vector of %d values expected, got shape %s, strides %s"
+                         % (what, n, tuple(t.shape), t.stride()))
+    if _dtype(t, what) != dtype:
+        raise TypeError("%s: wrong type %s" % (what, t.dtype))
+    return t.data_ptr()
+
+
+def _ckpt(t, rows, cols):
+    """Pointer of a checkpoint buffer of rows x cols values (None: NULL)."""
+    if t is None:
+        return None
+    cp, ep = (cols + 31) // 32 * 32, (cols + 127) // 128 * 4
+    need = (rows * cp + 15) // 16 * 16 + (rows * ep + 15) // 16 * 16
+    if t.element_size() != 1 or t.dim() != 1 or t.shape[0] < need or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError("ckpt: a contiguous uint8 vector of at least %d bytes expected, got %s of shape %s"
+                         % (need, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _launch(fn, what, stream, tensors, *args):
+    """Call fn(*args, stream) on the tensors' device; the stream defaults to that device's current one."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s: CUDA tensors expected, got one on %s" % (what, t.device))
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError("%s: tensors on different devices" % what)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != GQ_OK:
+        raise GQError(st, what)
+
+
+def _workspace(nbytes, device, stream=None):
+    """nbytes on the device (None for 0), for use on `stream` (default: the current one)."""
+    import torch
+    if not nbytes:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    # from the stream's own pool: nothing else still uses the memory, and what reuses it comes after
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _space(workspace, what):
+    """(pointer, bytes) of a workspace or None."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("%s: a contiguous workspace expected" % what)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gq_act_layout(rows, cols):
+    """(bytes, codes_off, exps_off) of a checkpoint."""
+    b, c, e = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().gq_act_layout(rows, cols, ctypes.byref(b), ctypes.byref(c), ctypes.byref(e)), "gq_act_layout")
+    return b.value, c.value, e.value
+
+
+def gq_act_pack(x, ckpt, stream=None):
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+    _launch(lib().gq_act_pack, "gq_act_pack", stream, (x, ckpt), _dtype(x, "x"), rows, cols, px, sx,
+            _ckpt(ckpt, rows, cols))
+
+
+def gq_act_unpack(ckpt, x, stream=None):
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+    _launch(lib().gq_act_unpack, "gq_act_unpack", stream, (x, ckpt), _dtype(x, "x"), rows, cols,
+            _ckpt(ckpt, rows, cols), px, sx)
+
+
+def gq_act_fn_forward(kind, x, y, ckpt=None, stream=None):
+    """kind: "gelu", "gelu_tanh", "silu" or the C constant."""
+    dt = _dtype(x, "x")
+    rows, cols = x.shape
+    px, sx = _matrix(x, "x")
+    py, sy = _matrix(y, "y", dt, (rows, cols))
+    _launch(lib().gq_act_fn_forward, "gq_act_fn_forward", stream, (x, y, ckpt), FUNCTIONS.get(kind, kind), dt, rows, cols,
+            px, sx, py, sy, _ckpt(ckpt, rows, cols))
+
+
+def gq_act_fn_backward(kind, ckpt, dy, dx, stream=None):
+    dt = _dtype(dy, "dy")
+    rows, cols = dy.shape
+    pdy, sdy = _matrix(dy, "dy")
+    pdx, sdx = _matrix(dx, "dx", dt, (rows, cols))
+    _launch(lib().gq_act_fn_backward, "gq_act_fn_backward", stream, (dy, dx, ckpt), FUNCTIONS.get(kind, kind), dt, rows,
+            cols, _ckpt(ckpt, rows, cols), pdy, sdy, pdx, sdx)
+
+
+def _weight_grad_bytes(dt, tokens, cin, cout, dy_stride, bias):
+    b = ctypes.c_size_t()
+    _check(lib().gq_act_weight_grad_workspace(dt, tokens, cin, cout, dy_stride, int(bias), ctypes.byref(b)),
+           "gq_act_weight_grad_workspace")
+    return b.value
+
+
+def gq_act_weight_grad_workspace(ckpt, dy, dw, db=None):
+    """A workspace tensor for gq_act_weight_grad on tensors of these sizes (None if it needs none)."""
+    return _workspace(_weight_grad_bytes(_dtype(dy, "dy"), dy.shape[0], dw.shape[1], dw.shape[0], dy.stride(0),
+                                         db is not None), dy.device)
+
+
+def gq_act_weight_grad(ckpt, dy, dw, db=None, accumulate=False, workspace=None, stream=None):
+    """dw: (out, in) float32, db: (out,) float32 or None.  Without a workspace one is allocated."""
+    dt = _dtype(dy, "dy")
+    pdy, sdy = _matrix(dy, "dy")
+    pdw, sdw = _matrix(dw, "dw", GQ_FLOAT32)
+    tokens, cout = dy.shape
+    cin = dw.shape[1]
+    if dw.shape[0] != cout:
+        raise ValueError("dw: %d rows expected, got %d" % (cout, dw.shape[0]))
+    if workspace is None:
+        workspace = _workspace(_weight_grad_bytes(dt, tokens, cin, cout, sdy, db is not None), dy.device, stream)
+    pws, nws = _space(workspace, "gq_act_weight_grad")
+    _launch(lib().gq_act_weight_grad, "gq_act_weight_grad", stream, (dy, ckpt, dw, db, workspace), dt, tokens, cin, cout,
+            _ckpt(ckpt, tokens, cin), pdy, sdy, pdw, sdw, _vector(db, "db", cout), int(bool(accumulate)), pws, nws)
+
+
+def gq_layer_norm_forward(x, gamma, beta, eps, y, mean, rstd, ckpt=None, stream=None):
+    """gamma, beta: vectors of x's type or float32 (both the same), or None."""
+    dt = _dtype(x, "x")
+    rows, cols = x.shape
+    px, sx = _matrix(x, "x")
+    py, sy = _matrix(y, "y", dt, (rows, cols))
+    pdt = dt if gamma is None and beta is None else _dtype(gamma if gamma is not None else beta, "gamma")
+    _launch(lib().gq_layer_norm_forward, "gq_layer_norm_forward", stream, (x, gamma, beta, y, mean, rstd, ckpt), dt, pdt,
+            rows, cols, px, sx, _vector(gamma, "gamma", cols, pdt), _vector(beta, "beta", cols, pdt), eps, py, sy,
+            _vector(mean, "mean", rows), _vector(rstd, "rstd", rows), _ckpt(ckpt, rows, cols))
+
+
+def _layer_norm_bytes(rows, cols):
+    b = ctypes.c_size_t()
+    _check(lib().gq_layer_norm_workspace(rows, cols, ctypes.byref(b)), "gq_layer_norm_workspace")
+    return b.value
+
+
+def gq_layer_norm_workspace(dy):
+    """A workspace tensor for gq_layer_norm_backward on a gradient of dy's size."""
+    return _workspace(_layer_norm_bytes(dy.shape[0], dy.shape[1]), dy.device)
+
+
+def gq_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate=False, workspace=None, stream=None):
+    """x: the forward pass's input (2-D) or its checkpoint (a uint8 vector).  dgamma, dbeta: float32
+    vectors or None.  Without a workspace one is allocated."""
+    dt = _dtype(dy, "dy")
+    rows, cols = dy.shape
+    pdy, sdy = _matrix(dy, "dy")
+    pdx, sdx = _matrix(dx, "dx", dt, (rows, cols))
+    if x.dim() == 1:
+        px, sx, pk = None, 0, _ckpt(x, rows, cols)
+    else:
+        (px, sx), pk = _matrix(x, "x", dt, (rows, cols)), None
+    pdt = dt if gamma is None else _dtype(gamma, "gamma")
+    if workspace is None and (dgamma is not None or dbeta is not None):
+        workspace = _workspace(_layer_norm_bytes(rows, cols), dy.device, stream)
+    pws, nws = _space(workspace, "gq_layer_norm_backward")
+    _launch(lib().gq_layer_norm_backward, "gq_layer_norm_backward", stream,
+            (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace), dt, pdt, rows, cols, pdy, sdy, px, sx, pk, _vector(gamma, "gamma", cols, pdt), _vector(mean, "mean", rows),
+            _vector(rstd, "rstd", rows), pdx, sdx, _vector(dgamma, "dgamma", cols), _vector(dbeta, "dbeta", cols),
+            int(bool(accumulate)), pws, nws)
 
 
 def gq_status_string(status):

@@ -344,6 +344,114 @@ GQ_API gq_status_t gq_plan_status(gq_plan_t plan, void *stream);
  * usable.  Returns GQ_ERR_INVALID for a NULL plan, GQ_ERR_CUDA if the launch fails. */
 GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, void *stream);
 
+/*
+ * Activations kept in 8 bits, and the backward pass that reads them.
+ *
+ * The gradient that gq_encode takes is made by a backward pass, which needs every layer's input of
+ * the forward pass.  These calls keep such an input in 8 bits (a "checkpoint", 33/32 bytes per
+ * element) and compute from it the slices of the flat float32 gradient vector: a linear layer's
+ * weight and bias gradient, a layer norm's, and the gradients passed on through activation
+ * functions and norms.  There is no counterpart in the pages; the bucketed codes and the table of
+ * scales are the message's idea (gq_message_layout) on groups of 32.
+ *
+ * Conventions, besides those above:
+ *   - Stateless: no plan, no status word, no allocation.  Calls that may overlap on the GPU (other
+ *     streams, other captured graphs) need outputs and workspaces of their own.
+ *   - A matrix is rows of cols elements of type `dtype`, its rows `stride` elements apart; a column
+ *     step other than 1 is not supported.  Rows of an input may repeat (stride 0) or overlap; those
+ *     of an output may not (stride >= cols).  With one row the stride is not used.  Rows that start
+ *     on 16 bytes take the faster loads.
+ *   - 0 <= rows < 2^31, 1 <= cols <= GQ_ACT_MAX_COLS.  With rows = 0 nothing is read; gradients that
+ *     sum over the rows are then written as 0 (or left as they are when accumulating).
+ *   - float32 outputs (gradients, mean, rstd) and mean/rstd inputs need 4-byte alignment only, so
+ *     that they may be any slice of a flat vector; gamma and beta their type's.
+ *   - No output may share memory with an input or another output (GQ_ERR_INVALID); columns of one
+ *     wider buffer with the same stride do not share any.
+ *   - Non-finite values pass through as in the formulas; a group with one in a checkpoint reads as
+ *     NaN throughout.  Sums are binary32 and their order is fixed: equal calls give equal bits.
+ */
+#define GQ_ACT_MAX_COLS (1 << 24)
+
+typedef enum { GQ_FLOAT32 = 0, GQ_BFLOAT16 = 1, GQ_FLOAT16 = 2 } gq_dtype_t;
+
+/*
+ * Layout of the checkpoint of rows x cols values (host computation; outputs may be NULL).
+ * codes_off = 0: rows of int8 codes, each row padded with 0 to a whole number of groups of 32
+ * columns (pitch 32 * ceil(cols / 32) bytes).  exps_off (16-byte aligned): rows of exponent bytes,
+ * one per group, each row padded with 0 to a multiple of four (pitch 4 * ceil(cols / 128) bytes).
+ * Value of code q under exponent E: q * 2^(E - 133); E = 255: NaN.
+ * E is chosen per group from m = max |x|: the smallest for which every code rint(x * 2^(133 - E)),
+ * ties to even, stays within +-127, at least 0 and at most 254 (where codes saturate at +-127).
+ * Every value is exact in bfloat16 and float32.
+ */
+GQ_API gq_status_t gq_act_layout(int64_t rows, int64_t cols, size_t *bytes, size_t *codes_off, size_t *exps_off);
+
+/* x -> checkpoint (device, gq_act_layout bytes, 16-byte aligned; the up to 15 bytes that round a
+ * region up to 16 are left as they were). */
+GQ_API gq_status_t gq_act_pack(int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride, void *ckpt,
+                               void *stream);
+/* Checkpoint -> x.  In float16 values are rounded and saturate at +-65504 (the largest value of a
+ * group may round up to 65536).  The type need not be the one packed. */
+GQ_API gq_status_t gq_act_unpack(int dtype, int64_t rows, int64_t cols, const void *ckpt, void *x, int64_t x_stride,
+                                 void *stream);
+
+/*
+ * Activation functions.  forward: y = f(x), and, unless ckpt is NULL, the checkpoint of x in the
+ * same pass.  backward: dx = dy * f'(xh), xh the checkpoint's values.
+ *   GQ_FN_GELU       x Phi(x), Phi the normal distribution function;
+ *   GQ_FN_GELU_TANH  x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2;
+ *   GQ_FN_SILU       x / (1 + exp(-x)).
+ */
+typedef enum { GQ_FN_GELU = 0, GQ_FN_GELU_TANH = 1, GQ_FN_SILU = 2 } gq_fn_t;
+GQ_API gq_status_t gq_act_fn_forward(int kind, int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                                     void *y, int64_t y_stride, void *ckpt, void *stream);
+GQ_API gq_status_t gq_act_fn_backward(int kind, int dtype, int64_t rows, int64_t cols, const void *ckpt, const void *dy,
+                                      int64_t dy_stride, void *dx, int64_t dx_stride, void *stream);
+
+/*
+ * A linear layer's gradients (y = x W^T + b, W of out x in) from the checkpoint of its input:
+ *   dw[n][k] = sum over t of dy[t][n] * xh[t][k]    (out x in float32, rows dw_stride apart)
+ *   db[n]    = sum over t of dy[t][n]               (NULL: not wanted)
+ * accumulate = 1 adds to dw and db (micro-batches), 0 overwrites them.
+ *   ckpt       checkpoint of tokens x in values; xh is decoded to dy's type, as by gq_act_unpack:
+ *              exact for bfloat16 and float32.
+ *   dy         tokens x out values of type dtype.
+ *   workspace  device, at least gq_act_weight_grad_workspace bytes (given the same arguments; bias
+ *              is db != NULL), 16-byte aligned; NULL if that is 0.  Its contents do not outlive the call.
+ */
+GQ_API gq_status_t gq_act_weight_grad_workspace(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_stride,
+                                                int bias, size_t *bytes);
+GQ_API gq_status_t gq_act_weight_grad(int dtype, int64_t tokens, int64_t in, int64_t out, const void *ckpt, const void *dy,
+                                      int64_t dy_stride, float *dw, int64_t dw_stride, float *db, int accumulate,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm over each row: y = (x - mean) * rstd * gamma + beta, rstd = 1 / sqrt(var + eps), var the
+ * population variance around the mean.
+ *   gamma, beta  cols values of type param_dtype (dtype or GQ_FLOAT32); NULL: 1 and 0.
+ *   mean, rstd   device, rows float32, written for the backward pass.
+ *   ckpt         receives the checkpoint of x, in the same pass (NULL: none).
+ */
+GQ_API gq_status_t gq_layer_norm_forward(int dtype, int param_dtype, int64_t rows, int64_t cols, const void *x,
+                                         int64_t x_stride, const void *gamma, const void *beta, float eps, void *y,
+                                         int64_t y_stride, float *mean, float *rstd, void *ckpt, void *stream);
+
+/*
+ * Its backward pass, with xh = (x - mean) * rstd and g = dy * gamma:
+ *   dx     = rstd * (g - sum(g) / cols - xh * sum(g xh) / cols)
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy   (cols float32 each; NULL: not
+ *            wanted).  accumulate = 1 adds to them, 0 overwrites them.
+ *   x, ckpt    the input, or its checkpoint: exactly one of the two.
+ *   workspace  device, at least gq_layer_norm_workspace bytes, 16-byte aligned (may be NULL if neither
+ *              dgamma nor dbeta is wanted).  Its contents do not outlive the call.
+ */
+GQ_API gq_status_t gq_layer_norm_workspace(int64_t rows, int64_t cols, size_t *bytes);
+GQ_API gq_status_t gq_layer_norm_backward(int dtype, int param_dtype, int64_t rows, int64_t cols, const void *dy,
+                                          int64_t dy_stride, const void *x, int64_t x_stride, const void *ckpt,
+                                          const void *gamma, const float *mean, const float *rstd, void *dx,
+                                          int64_t dx_stride, float *dgamma, float *dbeta, int accumulate, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. */
 GQ_API const char *gq_status_string(gq_status_t status);
 
