@@ -71,8 +71,8 @@ struct WgradArgs {
     int accumulate;
     unsigned char *ws;
 };
-// Workspace of a weight gradient; *parts_off: the offset of the bias's partial rows in it.
-size_t wgrad_workspace(int dtype, int64_t tokens, int64_t out, int64_t dy_stride, bool bias);
+// Workspace of a weight gradient: the staged gradient, cut tiles and the partial rows of the bias.
+size_t wgrad_workspace(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_stride, bool bias);
 cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream);
 
 // Sums over rows: part[p][c] = sum over the rows of part p of dy[row][c], then

@@ -68,7 +68,7 @@ bool shape_ok(int64_t rows, int64_t cols) { return rows >= 0 && rows <= kMaxRows
 // A matrix read (rows may repeat: stride 0) or written (rows may not share elements).
 bool in_ok(const void *p, int64_t rows, int64_t stride)
 {
-    return p && aligned(p, 16) && (rows <= 1 || (stride >= 0 && stride <= (int64_t(1) << 40)));
+    return p && aligned(p, 16) && (rows <= 1 || (stride >= 0 && stride <= (int64_t(1) << 36)));
 }
 bool out_ok(const void *p, int64_t rows, int64_t cols, int64_t stride)
 {
@@ -162,7 +162,7 @@ gq_status_t gq_act_weight_grad_workspace(int dtype, int64_t tokens, int64_t in, 
                                          size_t *bytes)
 {
     if (!elem_size(dtype) || !shape_ok(tokens, in) || !shape_ok(tokens, out) || !bytes) return GQ_ERR_INVALID;
-    *bytes = gq::wgrad_workspace(dtype, tokens, out, dy_stride, bias != 0);
+    *bytes = gq::wgrad_workspace(dtype, tokens, in, out, dy_stride, bias != 0);
     return GQ_OK;
 }
 
@@ -176,7 +176,7 @@ gq_status_t gq_act_weight_grad(int dtype, int64_t tokens, int64_t in, int64_t ou
     if (!dw || !aligned(dw, 4) || !aligned(db, 4) || (out > 1 && (dw_stride < in || dw_stride > (int64_t(1) << 40))))
         return GQ_ERR_INVALID;
     if (tokens > 0 && (!in_ok(dy, tokens, dy_stride) || !ckpt || !aligned(ckpt, 16))) return GQ_ERR_INVALID;
-    const size_t need = gq::wgrad_workspace(dtype, tokens, out, dy_stride, db != nullptr);
+    const size_t need = gq::wgrad_workspace(dtype, tokens, in, out, dy_stride, db != nullptr);
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return GQ_ERR_INVALID;
     const Region w[] = {region(dw, out, in, dw_stride, 4), region(db, (size_t)out * 4), region(workspace, need)};
     const Region r[] = {region(dy, tokens, out, dy_stride, elem_size(dtype)),

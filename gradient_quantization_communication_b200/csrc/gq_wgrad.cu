@@ -1,108 +1,783 @@
 // gq_wgrad.cu -- a linear layer's weight gradient from its input's 8-bit checkpoint:
 //   dw[n][k] = sum over tokens t of dy[t][n] * xh[t][k],  xh the decoded input,
-// and its bias gradient db[n] = sum over t of dy[t][n].  Sums are binary32.
+// and its bias gradient db[n] = sum over t of dy[t][n].
+//
+// The contraction runs over the tokens, which is the outer axis of both operands, so both are fed to the
+// tensor cores "MN-major": 64 columns (128 bytes) by 8 tokens form one swizzled block of shared memory,
+// and no operand is transposed on the way.  One tcgen05.mma (kind::f16, cta_group::2) makes a 256 x 256
+// tile of dw^T over 16 tokens, binary32 sums in TMEM:
+//   A  256 k: decoded from int8 in shared memory, 128 k by each CTA of the pair;
+//   B  256 n: dy as it is, 128 n in each CTA.
+// Decoding is exact (q * 2^e has 7 significant bits), so the products are too, and rounding happens in
+// the binary32 sums only.  A is the decoded operand because the M side holds 128 columns a CTA however
+// wide the tile is: a stage's 64 x 128 codes cost about 180 issue slots of each scheduler, under the
+// 512 cycles or so that its four MMAs take.
+//
+// Bounded by the tensor pipe for long batches, by the bytes of dw for few tokens.
+//
+// float32 gradients are cut into three bf16 planes without loss (8 significant bits each, by
+// truncation) by a pass before, and the contraction runs over 3 x tokens; so are rows that TMA cannot
+// fetch (a stride that is no multiple of 16 bytes, or rows that overlap) copied to aligned ones.
+#include <cuda.h>
+
 #include "gq_act.cuh"
 #include "gq_act.h"
+#include "gq_device.cuh"
 #include "gq_internal.h"
 
 namespace gq {
 namespace {
 
+constexpr int kTile = 256;               // tile of k and of n, per CTA pair
+constexpr int kHalf = 128;               // k rows, and n columns, of one CTA
+constexpr int kTok = 64;                 // tokens of a stage
+constexpr int kStages = 5;
+constexpr int kABytes = kHalf * kTok * 2;
+constexpr int kBBytes = kHalf * kTok * 2;
+constexpr int kCodeBytes = kHalf * kTok;
+constexpr int kExpBytes = kTok * 4;      // four groups' exponents of every token
+constexpr int kStageBytes = kABytes + kBBytes + kCodeBytes;
+constexpr int kBlockBytes = kTok * 128;  // 64 columns x 64 tokens of a 16-bit operand
+constexpr int kSmemBytes = kStages * (kStageBytes + kExpBytes) + 1024;
+// Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums round
+// toward zero, 16 products at a time: over 8192 tokens they came out 7e-6 small (relative), over 16384
+// 1.6e-5, where a chain rounded to nearest is off by 1e-6.  512 tokens lose 4e-7, and sums of such runs,
+// rounded to nearest, keep that.
+constexpr int kRun = 8;
+// Warps: 4 of control (copies, MMA, exponents, one idle), 8 of epilogue, 8 that decode.  The epilogue holds
+// 128 sums in each thread's registers, more than an even split gives: see kRegs*.
+constexpr int kCtlWarps = 4, kEpiWarps = 8, kConvWarps = 8;
+constexpr int kThreads = (kCtlWarps + kEpiWarps + kConvWarps) * 32;
+constexpr int kRegsLaunch = 96, kRegsCtl = 32, kRegsEpi = 168, kRegsConv = 56;
+static_assert(kCtlWarps * kRegsCtl + kEpiWarps * kRegsEpi + kConvWarps * kRegsConv <= kThreads / 32 * kRegsLaunch,
+              "setmaxnreg: the shares come from the block's own registers at launch");
+constexpr int kPairs = 74;               // CTA pairs of the 148 SMs: the schedule is made for these
+
+// How the tiles are spread over the pairs: whole rounds first, and the tiles of the last, partial round
+// each cut into `split` runs of tokens, whose partial sums meet in the workspace.
+struct Schedule {
+    int tiles_k, tiles_n;
+    int64_t whole, cut;  // tiles done by one pair; tiles cut
+    int split;
+    int64_t blocks;      // stages of a whole tile: planes x ceil(tokens / 64)
+    int64_t tok_blocks;  // ceil(tokens / 64)
+};
+
 struct Params {
+    CUtensorMap codes, dy;
+    Schedule s;
     int64_t tokens;
     int in, out;
-    Ckpt k;
-    const void *dy;
-    int64_t sdy;
+    const uint8_t *exps;
+    int exp_pitch;
     float *dw;
     int64_t sdw;
     int accumulate;
+    float *parts;
+    unsigned long long limit_ns;
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-
-// 64 x 64 outputs per block, 4 x 4 per thread, 16 tokens at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) k_wgrad_simple(const __grid_constant__ Params p)
+Schedule schedule(int dtype, int64_t tokens, int64_t in, int64_t out)
 {
-    __shared__ float sx[16][64], sd[16][64];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int k0 = (int)blockIdx.x * 64, n0 = (int)blockIdx.y * 64;
-    float acc[4][4] = {};
-    for (int64_t t0 = 0; t0 < p.tokens; t0 += 16) {
-        for (int i = threadIdx.x; i < 16 * 64; i += 256) {
-            const int64_t t = t0 + (i >> 6);
-            const int k = k0 + (i & 63), n = n0 + (i & 63);
-            float x = 0.0f, d = 0.0f;
-            if (t < p.tokens && k < p.in) {
-                const float q = (float)(int8_t)p.k.codes[t * p.k.code_pitch + k];
-                x = q * group_scale(p.k.exps[t * p.k.exp_pitch + (k >> 5)]);
-                if (sizeof(T) == 2 && __is_same(T, __half)) {
-                    x = x > 65504.0f ? 65504.0f : x < -65504.0f ? -65504.0f : x;
-                    x = __half2float(__float2half_rn(x));
-                }
-            }
-            if (t < p.tokens && n < p.out) d = to_f(static_cast<const T *>(p.dy)[t * p.sdy + n]);
-            sx[i >> 6][i & 63] = x;
-            sd[i >> 6][i & 63] = d;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < 16; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(sd[t][ty * 4 + i], sx[t][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+    Schedule s;
+    s.tiles_k = (int)((in + kTile - 1) / kTile);
+    s.tiles_n = (int)((out + kTile - 1) / kTile);
+    s.tok_blocks = (tokens + kTok - 1) / kTok;
+    s.blocks = s.tok_blocks * (dtype == GQ_FLOAT32 ? 3 : 1);
+    const int64_t tiles = (int64_t)s.tiles_k * s.tiles_n;
+    s.cut = tiles % kPairs;
+    s.split = 1;
+    if (s.cut) {
+        int64_t most = kPairs / s.cut;
+        const int64_t by_len = s.blocks / 8;
+        if (most > by_len) most = by_len;
+        s.split = most < 1 ? 1 : (int)most;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + ty * 4 + i, k = k0 + tx + 16 * j;
-            if (n >= p.out || k >= p.in) continue;
-            float *o = p.dw + n * p.sdw + k;
-            *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
-        }
+    if (s.split == 1) s.cut = 0;
+    s.whole = tiles - s.cut;
+    return s;
 }
 
-template <typename T>
-cudaError_t launch(const Params &p, cudaStream_t s)
+// ---------------------------------------------------------------------------------------------
+// PTX
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
 {
-    k_wgrad_simple<T><<<dim3((unsigned)((p.in + 63) / 64), (unsigned)((p.out + 63) / 64)), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait of one thread; false if it gave up.
+__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity, unsigned long long limit_ns)
+{
+    if (try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (try_wait_cluster(bar, parity)) return true;
+        if (global_ns() - t0 > limit_ns) return false;
+    }
+}
+// The same, of a warp: every lane acquires, and all agree on the outcome.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned long long limit_ns)
+{
+    return __all_sync(kFull, wait_thread(bar, parity, limit_ns));
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Shared-memory operand, MN-major with the 128-byte swizzle: blocks of 64 columns `kBlockBytes` apart,
+// groups of 8 tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(kBlockBytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, D binary32, both operands MN-major, M = N = 256.
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16)
+{
+    return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | 1u << 15 | 1u << 16 | (uint32_t)(kTile >> 3) << 17 |
+           (uint32_t)(kTile >> 4) << 24;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Arrives on the barrier at this offset of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Decoding 16 codes of one group under exponent byte E.
+// ---------------------------------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ void decode16(const uint4 &codes, uint32_t E, uint4 &lo, uint4 &hi)
+{
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t o[8];
+    if constexpr (BF16) {
+        // bf16 0x4300 | m is 128 + m for 7 bits m; q is its low 7 bits less 128 times its sign bit:
+        // (128 + low) - (128 or 256), exact, then times the scale, exact down to bf16's subnormals
+        uint32_t sb = E > 6u ? (E - 6u) << 7 : 0x40u >> (6u - E);
+        if (E == 255u) sb = 0x7fffu;
+        const uint32_t s2 = sb | sb << 16;
+        const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162 *>(&s2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t p = __byte_perm(w[i >> 1], 0u, (i & 1) ? 0x4342 : 0x4140);
+            const uint32_t a = (p & 0x007f007fu) | 0x43004300u, b = (p & 0x00800080u) | 0x43004300u;
+            const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+            const __nv_bfloat162 r = __hmul2(q, s);
+            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+    } else if (E - 109u <= 32u) {
+        // 2^-24 <= scale <= 2^8: fp16 0x6400 | m is 1024 + m; (1024 + q + 128) - 1152 is exact, the
+        // product with the scale rounds once at most and stays below 65504
+        const int e = (int)E - 133;
+        const uint32_t sb = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+        const uint32_t s2 = sb | sb << 16, off = 0x64806480u;
+        const __half2 s = *reinterpret_cast<const __half2 *>(&s2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t p = __byte_perm(w[i >> 1] ^ 0x80808080u, 0x64u, (i & 1) ? 0x4342 : 0x4140);
+            const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&p), *reinterpret_cast<const __half2 *>(&off));
+            const __half2 r = __hmul2(q, s);
+            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+    } else {
+        // groups beyond fp16's range: below half its smallest step, or saturated, or NaN
+        const float s = group_scale(E);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = (int)(int8_t)(w[i >> 1] >> (16 * (i & 1) + 8 * h));
+                const float f = (float)q * s;
+                v[h] = f > 65504.0f ? 65504.0f : f < -65504.0f ? -65504.0f : f;
+            }
+            const __half2 r = __floats2half2_rn(v[0], v[1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// ---------------------------------------------------------------------------------------------
+// The kernel: one CTA pair per SM pair, walking work items (whole tiles, then runs of cut tiles).
+// ---------------------------------------------------------------------------------------------
+struct Item {
+    int tk, tn;              // tile
+    int64_t first, last;     // its stages
+    int64_t part;            // partial tile in the workspace, -1: the whole tile
+};
+
+__device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
+{
+    int64_t tile;
+    if (i < s.whole) {
+        tile = i;
+        it.first = 0;
+        it.last = s.blocks;
+        it.part = -1;
+    } else {
+        const int64_t c = i - s.whole;
+        if (c >= s.cut * s.split) return false;
+        // run r of cut tile c % cut
+        const int64_t r = c / s.cut;
+        tile = s.whole + (c - r * s.cut);
+        it.first = s.blocks * r / s.split;
+        it.last = s.blocks * (r + 1) / s.split;
+        it.part = (tile - s.whole) * s.split + r;
+    }
+    // bands of 8 k tiles, walked along n: pairs that run together share their operands in L2
+    const int64_t band = (int64_t)8 * s.tiles_n;
+    const int64_t g = tile / band;
+    const int rest = (int)(tile - g * band);
+    const int wide = min(8, s.tiles_k - (int)g * 8);
+    it.tn = rest / wide;
+    it.tk = (int)g * 8 + rest - it.tn * wide;
+    return true;
+}
+
+struct Shared {
+    unsigned long long full[kStages];   // codes, exponents and B have arrived (this CTA)
+    unsigned long long ready[kStages];  // both CTAs have decoded A (the leader's is used)
+    unsigned long long empty[kStages];  // the MMAs have read A and B
+    unsigned long long acc_full[2];     // a run's sums are complete
+    unsigned long long acc_empty[2];    // both CTAs have read them (the leader's is used)
+    uint32_t tmem;
+};
+
+// Position in the ring of stages.
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ Params p)
+{
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ Shared sh;
+    const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t exps = stages + kStages * kStageBytes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t rank = cluster_rank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1 + 32);
+            mbar_init(&sh.ready[i], kConvWarps);  // half of the warps, of two CTAs
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = sh.tmem;
+
+    if (warp < kCtlWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        if (warp == 0 && lane == 0) {
+            // TMA: codes and B of every stage
+            Ring r;
+            int64_t done = 0;
+            bool ok = true;
+            Item it;
+            for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
+                const int k0 = it.tk * kTile + (int)rank * kHalf, n0 = it.tn * kTile + (int)rank * kHalf;
+                int plane = (int)(it.first / p.s.tok_blocks);
+                int64_t tb = it.first - plane * p.s.tok_blocks;
+                for (int64_t b = it.first; b < it.last; ++b) {
+                    if (done >= kStages && !wait_thread(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const int t0 = (int)tb * kTok;
+                    const uint32_t base = stages + r.st * kStageBytes, bar = smem_u32(&sh.full[r.st]);
+                    mbar_arrive_expect_tx(&sh.full[r.st], kBBytes + kCodeBytes);
+                    tma_load_2d(base + kABytes + kBBytes, &p.codes, k0, t0, bar);
+                    tma_load_3d(base + kABytes, &p.dy, n0, t0, plane, bar);
+                    tma_load_3d(base + kABytes + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
+                    ++done;
+                    r.next();
+                    if (++tb == p.s.tok_blocks) {
+                        tb = 0;
+                        ++plane;
+                    }
+                }
+            }
+            // what is still under way into this CTA's shared memory arrives before the CTA may leave: the
+            // MMAs' signals (after which the copies have been read), or, where a wait gave up, the copies
+            const int left = done < kStages ? (int)done : kStages;
+            for (int i = 0; i < left; ++i) {
+                if (--r.st < 0) {
+                    r.st = kStages - 1;
+                    r.ph ^= 1u;
+                }
+                wait_thread(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit_ns);
+            }
+        } else if (warp == 1 && rank == 0 && lane == 0) {
+            // MMA: one thread of the leader CTA
+            const uint32_t idesc = instr_desc(BF16);
+            Ring r;
+            int64_t runs = 0;
+            bool ok = true;
+            Item it;
+            for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
+                for (int64_t b = it.first; ok && b < it.last; ++runs) {
+                    const int buf = (int)(runs & 1);
+                    if (runs >= 2 && !wait_thread(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t d = tmem + buf * kTile;
+                    const int64_t first = b, last = b + kRun < it.last ? b + kRun : it.last;
+                    for (; b < last; ++b) {
+                        if (!wait_thread(smem_u32(&sh.ready[r.st]), r.ph, p.limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint32_t base = stages + r.st * kStageBytes;
+                        const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
+#pragma unroll
+                        for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of 8, 2048 bytes
+                            mma(d, da + (uint64_t)(k * 2048 >> 4), db + (uint64_t)(k * 2048 >> 4), idesc, b > first || k > 0);
+                        commit_pair(smem_u32(&sh.empty[r.st]));
+                        r.next();
+                    }
+                    if (ok) commit_pair(smem_u32(&sh.acc_full[buf]));
+                }
+            }
+        } else if (warp == 2) {
+            // Exponents: one word a token, two tokens a lane.  Loaded here and not by the warps that decode:
+            // their release of A would wait for loads of their own.
+            Ring r;
+            int64_t done = 0;
+            bool ok = true;
+            Item it;
+            for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
+                const int k0 = it.tk * kTile + (int)rank * kHalf;
+                const bool any = k0 < p.in;
+                int64_t t = it.first % p.s.tok_blocks * kTok + lane;
+                const uint8_t *src = p.exps + (any ? k0 >> 5 : 0);
+                for (int64_t b = it.first; b < it.last; ++b) {
+                    if (done >= kStages && !wait_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // tokens past the last, and columns past the last, read as 0 (their codes are 0)
+                        const bool in = any && t + 32 * h < p.tokens;
+                        const uint8_t *g = in ? src + (t + 32 * h) * p.exp_pitch : p.exps;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(exps + r.st * kExpBytes + (lane + 32 * h) * 4),
+                                     "l"(g), "r"(in ? 4 : 0)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[r.st])) : "memory");
+                    ++done;
+                    r.next();
+                    t += kTok;
+                    if (t >= p.s.tok_blocks * kTok) t = lane;  // the next plane
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else if (warp < kCtlWarps + kEpiWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // Epilogue: TMEM lane = k, column = n; four warps take 128 n each.  A warp's 32 lanes store 32
+        // adjacent k of one n.
+        const int quarter = warp & 3;  // the TMEM lanes this warp may read
+        const int n_off = (warp - kCtlWarps >= 4) ? kTile / 2 : 0;
+        const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), 0);
+        const uint32_t cols = tmem + ((uint32_t)(quarter * 32) << 16) + n_off;
+        int64_t runs = 0;
+        bool ok = true;
+        Item it;
+        for (int64_t i = pair; item_of(p.s, i, it); i += pairs) {
+            float acc[kTile / 2];
+#pragma unroll
+            for (int j = 0; j < kTile / 2; ++j) acc[j] = 0.0f;
+            for (int64_t b = it.first; b < it.last; b += kRun, ++runs) {
+                const int buf = (int)(runs & 1);
+                ok = ok && wait_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit_ns);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < kTile / 2; c += 16) {
+                    float v[16];
+                    tmem_load16(cols + buf * kTile + c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_cluster(acc_empty + buf * 8);
+            }
+            if (!ok) {  // a wait gave up: the tile's sums are not known
+#pragma unroll
+                for (int j = 0; j < kTile / 2; ++j) acc[j] = __uint_as_float(0x7fffffffu);
+            }
+            const int kl = (int)rank * kHalf + quarter * 32 + lane;
+            const int64_t k = (int64_t)it.tk * kTile + kl;
+            const int n0 = it.tn * kTile + n_off;
+            if (it.part >= 0) {
+                float *o = p.parts + (it.part * kTile + n_off) * kTile + kl;
+#pragma unroll
+                for (int j = 0; j < kTile / 2; ++j) o[j * kTile] = acc[j];
+            } else if (k < p.in) {
+                float *o = p.dw + (int64_t)n0 * p.sdw + k;
+                const int n = p.out - n0;
+                if (p.accumulate) {
+#pragma unroll
+                    for (int j = 0; j < kTile / 2; ++j)
+                        if (j < n) o[j * p.sdw] += acc[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kTile / 2; ++j)
+                        if (j < n) o[j * p.sdw] = acc[j];
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        // Decode: four warps take the even stages, four the odd ones; a warp 16 tokens, 8 lanes a token and
+        // 16 codes a lane at a time
+        const int w = warp - kCtlWarps - kEpiWarps;
+        const int j = lane & 7, tr = (w & 3) * 16 + (lane >> 3);
+        const uint32_t ready = in_cta(smem_u32(&sh.ready[0]), 0);
+        Ring r;
+        int64_t stage = 0;
+        bool ok = true;
+        Item it;
+        for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
+            for (int64_t b = it.first; b < it.last; ++b, ++stage, r.next()) {
+                if (((int)stage & 1) != (w >> 2)) continue;
+                if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = stages + r.st * kStageBytes;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int ts = tr + 4 * h;
+                    uint4 c, v[2];
+                    uint32_t E;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
+                                 : "r"(base + kABytes + kBBytes + ts * 128 + j * 16));
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(E) : "r"(exps + r.st * kExpBytes + ts * 4 + (j >> 1)));
+                    decode16<BF16>(c, E, v[0], v[1]);
+                    // 16-byte pieces (j & 3) * 2 and + 1 of block j >> 2, swizzled by the token; lanes of the
+                    // two blocks store their pieces in opposite order, so that 8 lanes cover all banks
+                    const uint32_t row = base + (j >> 2) * kBlockBytes + ts * 128;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int hi = x ^ (j >> 2);
+                        const uint4 s = hi ? v[1] : v[0];
+                        const uint32_t at = row + ((((j & 3) * 2 + hi) ^ (ts & 7)) << 4);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(s.x), "r"(s.y), "r"(s.z), "r"(s.w)
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(ready + r.st * 8);
+            }
+        }
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// The cut tiles' sums, run by run in order, into dw.
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
+{
+    Item it;
+    const int64_t cut = blockIdx.x / (kTile / 4);
+    const int n = (int)(blockIdx.x % (kTile / 4)) * 4;
+    item_of(p.s, p.s.whole + cut, it);
+    const int64_t k = (int64_t)it.tk * kTile + threadIdx.x;
+    if (k >= p.in) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = (int64_t)it.tn * kTile + n + j;
+        if (row >= p.out) return;
+        const float *s = p.parts + (cut * p.s.split * kTile + n + j) * kTile + threadIdx.x;
+        float v = 0.0f;
+        for (int r = 0; r < p.s.split; ++r) v += s[(int64_t)r * kTile * kTile];
+        float *o = p.dw + row * p.sdw + k;
+        *o = p.accumulate ? *o + v : v;
+    }
+}
+
+__global__ void __launch_bounds__(256) k_zero(float *dw, int64_t sdw, int in, int out)
+{
+    for (int64_t n = blockIdx.x; n < out; n += gridDim.x)
+        for (int k = threadIdx.x; k < in; k += 256) dw[n * sdw + k] = 0.0f;
+}
+
+// dy into rows of `pitch` 16-bit values: float32 as three bf16 planes that add up to it exactly (smallest
+// first), 16-bit types as they are.
+template <typename T>
+__global__ void __launch_bounds__(256) k_stage(const T *dy, int64_t sdy, int64_t tokens, int out, int64_t pitch, uint16_t *dst)
+{
+    const int per_row = (out + 255) / 256;
+    const int64_t n = tokens * per_row;
+    for (int64_t id = blockIdx.x; id < n; id += gridDim.x) {
+        const int64_t t = id / per_row;
+        const int c = (int)(id - t * per_row) * 256 + threadIdx.x;
+        if (c >= out) continue;
+        if constexpr (sizeof(T) == 2) {
+            dst[t * pitch + c] = (uint16_t)elem_bits(dy[t * sdy + c]);
+        } else {
+            const float v = dy[t * sdy + c];
+            const uint32_t bits = __float_as_uint(v);
+            uint32_t hi = bits >> 16, mid = 0, lo = 0;
+            if ((bits & 0x7f800000u) == 0x7f800000u) {
+                if (bits & 0x007fffffu) hi |= 0x40u;  // a NaN stays one
+            } else {
+                const float r = v - __uint_as_float(bits & 0xffff0000u);
+                const uint32_t m = __float_as_uint(r);
+                mid = m >> 16;
+                lo = __float_as_uint(r - __uint_as_float(m & 0xffff0000u)) >> 16;
+            }
+            const int64_t plane = tokens * pitch, at = t * pitch + c;
+            dst[at] = (uint16_t)lo;
+            dst[plane + at] = (uint16_t)mid;
+            dst[2 * plane + at] = (uint16_t)hi;
+        }
+    }
+}
+
+bool staged(int dtype, int64_t tokens, int64_t out, int64_t dy_stride)
+{
+    return dtype == GQ_FLOAT32 || (tokens > 1 && (dy_stride % 8 != 0 || dy_stride < out));
+}
+int64_t staged_pitch(int64_t out) { return (out + 7) / 8 * 8; }
+
+struct Spaces {
+    size_t staged, parts, cols, bytes;  // offsets of the staged gradient, the cut tiles, the bias's partial rows
+};
+Spaces spaces(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_stride, bool bias)
+{
+    const Schedule s = schedule(dtype, tokens, in, out);
+    Spaces w;
+    w.staged = 0;
+    w.parts = staged(dtype, tokens, out, dy_stride)
+                  ? (size_t)(tokens * staged_pitch(out)) * (dtype == GQ_FLOAT32 ? 6 : 2) : 0;
+    w.cols = w.parts + (size_t)(s.cut * s.split) * kTile * kTile * sizeof(float);
+    w.bytes = w.cols + (bias ? (size_t)(colsum_parts(tokens, out) * out) * sizeof(float) : 0);
+    return w;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Registers a thread of a kernel is launched with (0: unknown).
+template <typename K>
+int num_regs(K kern)
+{
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
 }
 
 }  // namespace
 
-size_t wgrad_workspace(int dtype, int64_t tokens, int64_t out, int64_t dy_stride, bool bias)
+size_t wgrad_workspace(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_stride, bool bias)
 {
-    (void)dtype;
-    (void)dy_stride;
-    return bias ? (size_t)colsum_parts(tokens, out) * (size_t)out * sizeof(float) : 0;
+    return spaces(dtype, tokens, in, out, dy_stride, bias).bytes;
 }
 
 cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
 {
+    if (a.tokens == 0) {
+        if (a.accumulate) return cudaSuccess;
+        k_zero<<<(unsigned)(a.out < 1024 ? a.out : 1024), 256, 0, stream>>>(a.dw, a.dw_stride, (int)a.in, (int)a.out);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess && a.db ? cudaMemsetAsync(a.db, 0, (size_t)a.out * sizeof(float), stream) : e;
+    }
     const CkptLayout l = ckpt_layout(a.tokens, a.in);
-    uint8_t *ck = static_cast<uint8_t *>(const_cast<void *>(a.ckpt));
+    const Spaces w = spaces(a.dtype, a.tokens, a.in, a.out, a.dy.stride, a.db != nullptr);
+    int per_sm = 0, sms = 0;
+    cudaError_t e = cudaSuccess;
+
     Params p;
+    p.s = schedule(a.dtype, a.tokens, a.in, a.out);
     p.tokens = a.tokens;
     p.in = (int)a.in;
     p.out = (int)a.out;
-    p.k = Ckpt{ck, ck + l.exps_off, (int)l.code_pitch, (int)l.exp_pitch};
-    p.dy = a.dy.p;
-    p.sdy = a.dy.stride;
+    p.exps = static_cast<const uint8_t *>(a.ckpt) + l.exps_off;
+    p.exp_pitch = (int)l.exp_pitch;
     p.dw = a.dw;
     p.sdw = a.dw_stride;
     p.accumulate = a.accumulate;
-    const cudaError_t e = a.dtype == GQ_FLOAT32    ? launch<float>(p, stream)
-                          : a.dtype == GQ_BFLOAT16 ? launch<__nv_bfloat16>(p, stream)
-                                                   : launch<__half>(p, stream);
-    if (e != cudaSuccess || !a.db) return e;
-    return launch_colsum(a.dtype, a.tokens, a.out, a.dy, reinterpret_cast<float *>(a.ws), a.db, a.accumulate, stream);
+    p.parts = reinterpret_cast<float *>(a.ws + w.parts);
+    // a tile's sums take about 0.3 us a stage; 20 us a stage and two seconds are never reached but by a fault
+    p.limit_ns = 2000000000ull + 20000ull * (unsigned long long)p.s.blocks;
+
+    const void *dy = a.dy.p;
+    int64_t pitch = a.tokens > 1 ? a.dy.stride : staged_pitch(a.out);
+    const int planes = a.dtype == GQ_FLOAT32 ? 3 : 1;
+    if (staged(a.dtype, a.tokens, a.out, a.dy.stride)) {
+        pitch = staged_pitch(a.out);
+        const int64_t need = a.tokens * ((a.out + 255) / 256);
+        const unsigned grid = (unsigned)(need < 148 * 8 ? need : 148 * 8);
+        if (a.dtype == GQ_FLOAT32)
+            k_stage<float><<<grid, 256, 0, stream>>>(static_cast<const float *>(dy), a.dy.stride, a.tokens, (int)a.out, pitch,
+                                                    reinterpret_cast<uint16_t *>(a.ws));
+        else
+            k_stage<__half><<<grid, 256, 0, stream>>>(static_cast<const __half *>(dy), a.dy.stride, a.tokens, (int)a.out,
+                                                     pitch, reinterpret_cast<uint16_t *>(a.ws));
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        dy = a.ws;
+    }
+    const EncodeFn encode = encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint32_t ones[3] = {1, 1, 1};
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)l.code_pitch, (cuuint64_t)a.tokens};
+        const cuuint64_t strides[1] = {(cuuint64_t)l.code_pitch};
+        const cuuint32_t box[2] = {kHalf, kTok};
+        if (encode(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(a.ckpt), dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)a.out, (cuuint64_t)a.tokens, (cuuint64_t)planes};
+        const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)(planes > 1 ? a.tokens : 1)};
+        const cuuint32_t box[3] = {64, kTok, 1};
+        if (encode(&p.dy, a.dtype == GQ_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void *>(dy), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+
+    auto kern = a.dtype == GQ_FLOAT16 ? k_wgrad<false> : k_wgrad<true>;
+    e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, kSmemBytes, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    static const int regs[2] = {num_regs(k_wgrad<false>), num_regs(k_wgrad<true>)};
+    if (regs[0] < kRegsLaunch || regs[1] < kRegsLaunch) return cudaErrorInvalidKernelImage;  // setmaxnreg would wait
+    const int64_t items = p.s.whole + p.s.cut * p.s.split;
+    const int64_t pairs = items < kPairs ? items : kPairs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return e;
+    if (p.s.cut) {
+        k_join<<<(unsigned)(p.s.cut * (kTile / 4)), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (!a.db) return cudaSuccess;
+    return launch_colsum(a.dtype, a.tokens, a.out, a.dy, reinterpret_cast<float *>(a.ws + w.cols), a.db, a.accumulate, stream);
 }
 
 }  // namespace gq

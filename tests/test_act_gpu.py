@@ -249,6 +249,21 @@ def test_weight_grad(dtype, tokens, cin, cout, pad):
     assert flat[0] == 5.0 and (flat[-2:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,cin,cout", [(700, 2600, 2500), (5000, 700, 650), (9001, 256, 256), (70, 5000, 4999)])
+def test_weight_grad_many_tiles(dtype, tokens, cin, cout):
+    """More tiles than CTA pairs, tiles cut along the tokens, long sums; the 64-bit product on the GPU."""
+    x, dy = _values(tokens, cin, dtype, 1), _values(tokens, cout, dtype, 2, 0.01)
+    ck, codes, exps = _ckpt(x)
+    xh = A.as_type(A.decode(codes, exps, cin), torch.float16 if dtype == torch.float16 else torch.float32).double().cuda()
+    d = dy.double().cuda()
+    dw = torch.empty(cout, cin, device="cuda")
+    G.gq_act_weight_grad(ck, dy.cuda(), dw)
+    # runs of 512 tokens lose at most two steps every 16 tokens, their sums one rounding each
+    steps = min(tokens, 512) / 16 * 2 + 3 * tokens / 512 + 16
+    assert ((dw.double() - d.t() @ xh).abs() <= steps * 2.0 ** -23 * (d.abs().t() @ xh.abs())).all()
+
+
 def test_weight_grad_strided_output_and_no_bias():
     x, dy = _values(70, 72, torch.bfloat16, 1), _values(70, 40, torch.bfloat16, 2)
     ck, dw, size, _, _ = _wgrad_want(x, dy)
