@@ -31,14 +31,16 @@ namespace {
 constexpr int kTile = 256;               // tile of k and of n, per CTA pair
 constexpr int kHalf = 128;               // k rows, and n columns, of one CTA
 constexpr int kTok = 64;                 // tokens of a stage
-constexpr int kStages = 5;
 constexpr int kABytes = kHalf * kTok * 2;
 constexpr int kBBytes = kHalf * kTok * 2;
 constexpr int kCodeBytes = kHalf * kTok;
 constexpr int kExpBytes = kTok * 4;      // four groups' exponents of every token
-constexpr int kStageBytes = kABytes + kBBytes + kCodeBytes;
 constexpr int kBlockBytes = kTok * 128;  // 64 columns x 64 tokens of a 16-bit operand
-constexpr int kSmemBytes = kStages * (kStageBytes + kExpBytes) + 1024;
+// Two rings.  What is fetched (B, codes, exponents) lives from the start of its copy to the end of its MMA,
+// some 3000 cycles of which the copy takes half; the decoded A lives for its decoding and its MMA.
+constexpr int kLoads = 6, kDecoded = 5;
+constexpr int kLoadBytes = kBBytes + kCodeBytes;
+constexpr int kSmemBytes = kLoads * (kLoadBytes + kExpBytes) + kDecoded * kABytes + 1024;
 // Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums round
 // toward zero, 16 products at a time: over 8192 tokens they came out 7e-6 small (relative), over 16384
 // 1.6e-5, where a chain rounded to nearest is off by 1e-6.  512 tokens lose 4e-7, and sums of such runs,
@@ -48,7 +50,7 @@ constexpr int kRun = 8;
 // 128 sums in each thread's registers, more than an even split gives: see kRegs*.
 constexpr int kCtlWarps = 4, kEpiWarps = 8, kConvWarps = 8;
 constexpr int kThreads = (kCtlWarps + kEpiWarps + kConvWarps) * 32;
-constexpr int kRegsLaunch = 96, kRegsCtl = 32, kRegsEpi = 168, kRegsConv = 56;
+constexpr int kRegsLaunch = 96, kRegsCtl = 64, kRegsEpi = 168, kRegsConv = 40;
 static_assert(kCtlWarps * kRegsCtl + kEpiWarps * kRegsEpi + kConvWarps * kRegsConv <= kThreads / 32 * kRegsLaunch,
               "setmaxnreg: the shares come from the block's own registers at launch");
 constexpr int kPairs = 74;               // CTA pairs of the 148 SMs: the schedule is made for these
@@ -74,7 +76,7 @@ struct Params {
     int64_t sdw;
     int accumulate;
     float *parts;
-    unsigned long long limit_ns;
+    long long limit;          // cycles after which a wait gives up
 };
 
 Schedule schedule(int dtype, int64_t tokens, int64_t in, int64_t out)
@@ -101,33 +103,34 @@ Schedule schedule(int dtype, int64_t tokens, int64_t in, int64_t out)
 // ---------------------------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
-// Bounded wait of one thread; false if it gave up.
-__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity, unsigned long long limit_ns)
+// Bounded wait of one thread; false if it gave up.  By the SM's clock: reading the global timer takes
+// longer than most waits here.
+__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity, long long limit)
 {
-    if (try_wait_cluster(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
+    if (try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (try_wait_cluster(bar, parity)) return true;
-        if (global_ns() - t0 > limit_ns) return false;
+            if (try_wait(bar, parity)) return true;
+        if (clock64() - t0 > limit) return false;
     }
 }
 // The same, of a warp: every lane acquires, and all agree on the outcome.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, unsigned long long limit_ns)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit)
 {
-    return __all_sync(kFull, wait_thread(bar, parity, limit_ns));
+    return __all_sync(kFull, wait_thread(bar, parity, limit));
 }
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 {
@@ -137,7 +140,14 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -203,60 +213,68 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
 }
 
 // ---------------------------------------------------------------------------------------------
-// Decoding 16 codes of one group under exponent byte E.
+// Decoding 16 codes of one group.  Of four codes in a word, the even and the odd ones make a pair each
+// (a mask instead of a byte permutation), so columns 1 and 2 of every four change places in A; the
+// epilogue's threads store them back in order.
 // ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t bits2(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+__device__ __forceinline__ uint32_t bits2(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// 16-bit lanes holding the codes' bytes, even (i = 0) or odd (i = 1) ones of a word.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) { return (i ? w >> 8 : w) & 0x00ff00ffu; }
+
 template <bool BF16>
-__device__ __forceinline__ void decode16(const uint4 &codes, uint32_t E, uint4 &lo, uint4 &hi)
+__device__ __forceinline__ void decode16(const uint4 &codes, uint32_t E, uint32_t (&o)[8])
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t o[8];
     if constexpr (BF16) {
-        // bf16 0x4300 | m is 128 + m for 7 bits m; q is its low 7 bits less 128 times its sign bit:
-        // (128 + low) - (128 or 256), exact, then times the scale, exact down to bf16's subnormals
-        uint32_t sb = E > 6u ? (E - 6u) << 7 : 0x40u >> (6u - E);
-        if (E == 255u) sb = 0x7fffu;
-        const uint32_t s2 = sb | sb << 16;
-        const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162 *>(&s2);
+        if (E - 7u <= 245u) {
+            // 2^-126 <= s <= 2^119.  bf16 0x4300 | (q + 128) is 256 + q for q < 0 and 256 + 2 q for q >= 0
+            // (its step doubles at 256).  y = that less 256, times s, is q s or 2 q s; half of y where it is
+            // positive, taken off, leaves q s.  Every step is exact.
+            const __nv_bfloat162 s = bf2(E * 0x00800080u - 6u * 0x00800080u);
+            const __nv_bfloat162 half = __hmul2(s, bf2(0x3f003f00u)), c = __hmul2(s, bf2(0xc380c380u)),
+                                 hc = __hmul2(s, bf2(0xc300c300u));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t p = __byte_perm(w[i >> 1], 0u, (i & 1) ? 0x4342 : 0x4140);
-            const uint32_t a = (p & 0x007f007fu) | 0x43004300u, b = (p & 0x00800080u) | 0x43004300u;
-            const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-            const __nv_bfloat162 r = __hmul2(q, s);
-            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+            for (int i = 0; i < 8; ++i) {
+                const __nv_bfloat162 v = bf2(code_pair(w[i >> 1], i & 1) ^ 0x43804380u);
+                o[i] = bits2(__hsub2(__hfma2(v, s, c), __hfma2_relu(v, half, hc)));
+            }
+        } else {
+            // the ends of the range, NaN, and E = 0 (groups of zeros): 0x4300 | m is 128 + m for 7 bits m, and
+            // q its low 7 bits less 128 times its sign bit, exact, times the scale
+            const uint32_t b = E == 255u ? 0x7fffu : E > 6u ? (E - 6u) << 7 : 0x40u >> (6u - E);
+            const __nv_bfloat162 s = bf2(b | b << 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t p = code_pair(w[i >> 1], i & 1);
+                o[i] = bits2(__hmul2(__hsub2(bf2((p & 0x007f007fu) | 0x43004300u), bf2((p & 0x00800080u) | 0x43004300u)), s));
+            }
         }
     } else if (E - 109u <= 32u) {
-        // 2^-24 <= scale <= 2^8: fp16 0x6400 | m is 1024 + m; (1024 + q + 128) - 1152 is exact, the
-        // product with the scale rounds once at most and stays below 65504
-        const int e = (int)E - 133;
-        const uint32_t sb = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
-        const uint32_t s2 = sb | sb << 16, off = 0x64806480u;
-        const __half2 s = *reinterpret_cast<const __half2 *>(&s2);
+        // 2^-24 <= s <= 2^8.  fp16 0x6400 | m is 1024 + m; (1024 + q + 128) - 1152 is exact, the product with
+        // the scale rounds once at most and stays below 65504
+        const uint32_t b = E >= 119u ? (E - 118u) << 10 : 1u << (E - 109u);
+        const __half2 s = h2(b | b << 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t p = __byte_perm(w[i >> 1] ^ 0x80808080u, 0x64u, (i & 1) ? 0x4342 : 0x4140);
-            const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&p), *reinterpret_cast<const __half2 *>(&off));
-            const __half2 r = __hmul2(q, s);
-            o[i] = *reinterpret_cast<const uint32_t *>(&r);
-        }
+        for (int i = 0; i < 8; ++i)
+            o[i] = bits2(__hmul2(__hsub2(h2(code_pair(w[i >> 1], i & 1) ^ 0x64806480u), h2(0x64806480u)), s));
     } else {
         // groups beyond fp16's range: below half its smallest step, or saturated, or NaN
         const float s = group_scale(E);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            const uint32_t p = code_pair(w[i >> 1], i & 1);
             float v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int q = (int)(int8_t)(w[i >> 1] >> (16 * (i & 1) + 8 * h));
-                const float f = (float)q * s;
+                const float f = (float)(int)(int8_t)(p >> (16 * h)) * s;
                 v[h] = f > 65504.0f ? 65504.0f : f < -65504.0f ? -65504.0f : f;
             }
-            const __half2 r = __floats2half2_rn(v[0], v[1]);
-            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+            o[i] = bits2(__floats2half2_rn(v[0], v[1]));
         }
     }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -297,22 +315,34 @@ __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
 }
 
 struct Shared {
-    unsigned long long full[kStages];   // codes, exponents and B have arrived (this CTA)
-    unsigned long long ready[kStages];  // both CTAs have decoded A (the leader's is used)
-    unsigned long long empty[kStages];  // the MMAs have read A and B
-    unsigned long long acc_full[2];     // a run's sums are complete
-    unsigned long long acc_empty[2];    // both CTAs have read them (the leader's is used)
+    unsigned long long full[kLoads];       // codes, exponents and B have arrived (this CTA)
+    unsigned long long empty[kLoads];      // the MMAs have read B (and A, so the codes have been read)
+    unsigned long long ready[kDecoded];    // both CTAs have decoded A (the leader's is used)
+    unsigned long long a_empty[kDecoded];  // the MMAs have read A
+    unsigned long long acc_full[2];        // a run's sums are complete
+    unsigned long long acc_empty[2];       // both CTAs have read them (the leader's is used)
     uint32_t tmem;
 };
 
-// Position in the ring of stages.
+// Position in a ring of N stages; wrapped: every stage has been used before.
+template <int N>
 struct Ring {
     int st = 0;
     uint32_t ph = 0;
-    __device__ __forceinline__ void next()
+    bool wrapped = false;
+    __device__ __forceinline__ void next(int by = 1)
     {
-        if (++st == kStages) {
-            st = 0;
+        st += by;
+        if (st >= N) {
+            st -= N;
+            ph ^= 1u;
+            wrapped = true;
+        }
+    }
+    __device__ __forceinline__ void back()
+    {
+        if (--st < 0) {
+            st = N - 1;
             ph ^= 1u;
         }
     }
@@ -324,16 +354,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     extern __shared__ unsigned char raw_smem[];
     __shared__ Shared sh;
     const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t exps = stages + kStages * kStageBytes;
+    const uint32_t decoded = stages + kLoads * kLoadBytes, exps = decoded + kDecoded * kABytes;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             mbar_init(&sh.full[i], 1 + 32);
-            mbar_init(&sh.ready[i], kConvWarps);  // half of the warps, of two CTAs
             mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < kDecoded; ++i) {
+            mbar_init(&sh.ready[i], kConvWarps);  // half of the warps, of two CTAs
+            mbar_init(&sh.a_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -355,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
             // TMA: codes and B of every stage
-            Ring r;
-            int64_t done = 0;
+            Ring<kLoads> r;
+            Ring<kDecoded> ra;
             bool ok = true;
             Item it;
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
@@ -364,18 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 int plane = (int)(it.first / p.s.tok_blocks);
                 int64_t tb = it.first - plane * p.s.tok_blocks;
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (done >= kStages && !wait_thread(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit_ns)) {
+                    if (r.wrapped && !wait_thread(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
                         ok = false;
                         break;
                     }
                     const int t0 = (int)tb * kTok;
-                    const uint32_t base = stages + r.st * kStageBytes, bar = smem_u32(&sh.full[r.st]);
+                    const uint32_t base = stages + r.st * kLoadBytes, bar = smem_u32(&sh.full[r.st]);
                     mbar_arrive_expect_tx(&sh.full[r.st], kBBytes + kCodeBytes);
-                    tma_load_2d(base + kABytes + kBBytes, &p.codes, k0, t0, bar);
-                    tma_load_3d(base + kABytes, &p.dy, n0, t0, plane, bar);
-                    tma_load_3d(base + kABytes + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
-                    ++done;
+                    tma_load_2d(base + kBBytes, &p.codes, k0, t0, bar);
+                    tma_load_3d(base, &p.dy, n0, t0, plane, bar);
+                    tma_load_3d(base + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
                     r.next();
+                    ra.next();
                     if (++tb == p.s.tok_blocks) {
                         tb = 0;
                         ++plane;
@@ -384,87 +417,99 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             }
             // what is still under way into this CTA's shared memory arrives before the CTA may leave: the
             // MMAs' signals (after which the copies have been read), or, where a wait gave up, the copies
-            const int left = done < kStages ? (int)done : kStages;
-            for (int i = 0; i < left; ++i) {
-                if (--r.st < 0) {
-                    r.st = kStages - 1;
-                    r.ph ^= 1u;
-                }
-                wait_thread(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit_ns);
+            const int left = r.wrapped ? kLoads : r.st, left_a = ok ? ra.wrapped ? kDecoded : ra.st : 0;
+            for (int i = 0; i < left_a; ++i) {
+                ra.back();
+                wait_thread(smem_u32(&sh.a_empty[ra.st]), ra.ph, p.limit);
             }
-        } else if (warp == 1 && rank == 0 && lane == 0) {
-            // MMA: one thread of the leader CTA
+            for (int i = 0; i < left; ++i) {
+                r.back();
+                wait_thread(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit);
+            }
+        } else if (warp == 1 && rank == 0) {
+            // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one
+            // lane issues
+            const bool one = elect_one();
             const uint32_t idesc = instr_desc(BF16);
-            Ring r;
+            Ring<kLoads> r;
+            Ring<kDecoded> ra;
             int64_t runs = 0;
             bool ok = true;
             Item it;
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
                 for (int64_t b = it.first; ok && b < it.last; ++runs) {
                     const int buf = (int)(runs & 1);
-                    if (runs >= 2 && !wait_thread(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit_ns)) {
+                    if (runs >= 2 && !wait_warp(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit)) {
                         ok = false;
                         break;
                     }
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t d = tmem + buf * kTile;
-                    const int64_t first = b, last = b + kRun < it.last ? b + kRun : it.last;
-                    for (; b < last; ++b) {
-                        if (!wait_thread(smem_u32(&sh.ready[r.st]), r.ph, p.limit_ns)) {
+                    const int n = (int)(it.last - b < kRun ? it.last - b : kRun);
+                    b += n;
+                    for (int j = 0; j < n; ++j) {
+                        if (!wait_warp(smem_u32(&sh.ready[ra.st]), ra.ph, p.limit)) {
                             ok = false;
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t base = stages + r.st * kStageBytes;
-                        const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
+                        const uint64_t da = operand_desc(decoded + ra.st * kABytes), db = operand_desc(stages + r.st * kLoadBytes);
+                        if (one) {
 #pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of 8, 2048 bytes
-                            mma(d, da + (uint64_t)(k * 2048 >> 4), db + (uint64_t)(k * 2048 >> 4), idesc, b > first || k > 0);
-                        commit_pair(smem_u32(&sh.empty[r.st]));
+                            for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of 8, 2048 bytes
+                                mma(d, da + (uint64_t)(k * 2048 >> 4), db + (uint64_t)(k * 2048 >> 4), idesc, j > 0 || k > 0);
+                            commit_pair(smem_u32(&sh.a_empty[ra.st]));
+                            commit_pair(smem_u32(&sh.empty[r.st]));
+                        }
+                        __syncwarp();
                         r.next();
+                        ra.next();
                     }
-                    if (ok) commit_pair(smem_u32(&sh.acc_full[buf]));
+                    if (ok && one) commit_pair(smem_u32(&sh.acc_full[buf]));
+                    __syncwarp();
                 }
             }
         } else if (warp == 2) {
-            // Exponents: one word a token, two tokens a lane.  Loaded here and not by the warps that decode:
-            // their release of A would wait for loads of their own.
-            Ring r;
-            int64_t done = 0;
+            // Exponents of every stage: one word a token, two tokens a lane.  Loaded here and not by the warps
+            // that decode: their signals would wait for loads of their own.
+            Ring<kLoads> r;
             bool ok = true;
             Item it;
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
                 const int k0 = it.tk * kTile + (int)rank * kHalf;
                 const bool any = k0 < p.in;
+                const int64_t end = p.s.tok_blocks * kTok;
                 int64_t t = it.first % p.s.tok_blocks * kTok + lane;
-                const uint8_t *src = p.exps + (any ? k0 >> 5 : 0);
+                const uint8_t *src = p.exps + (any ? t * p.exp_pitch + (k0 >> 5) : 0);
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (done >= kStages && !wait_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit_ns)) {
+                    if (r.wrapped && !wait_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
                         ok = false;
                         break;
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // tokens past the last, and columns past the last, read as 0 (their codes are 0)
-                        const bool in = any && t + 32 * h < p.tokens;
-                        const uint8_t *g = in ? src + (t + 32 * h) * p.exp_pitch : p.exps;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(exps + r.st * kExpBytes + (lane + 32 * h) * 4),
-                                     "l"(g), "r"(in ? 4 : 0)
-                                     : "memory");
-                    }
+                    const uint32_t dst = exps + r.st * kExpBytes + lane * 4;
+                    // tokens past the last, and columns past the last, read as 0 (their codes are 0)
+                    const bool in0 = any && t < p.tokens, in1 = any && t + 32 < p.tokens;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in0 ? src : p.exps), "r"(in0 ? 4 : 0)
+                                 : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 128),
+                                 "l"(in1 ? src + 32 * p.exp_pitch : p.exps), "r"(in1 ? 4 : 0)
+                                 : "memory");
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[r.st])) : "memory");
-                    ++done;
                     r.next();
                     t += kTok;
-                    if (t >= p.s.tok_blocks * kTok) t = lane;  // the next plane
+                    if (any) src += kTok * p.exp_pitch;
+                    if (t >= end) {  // the next plane
+                        if (any) src -= end * p.exp_pitch;
+                        t -= end;
+                    }
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp < kCtlWarps + kEpiWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-        // Epilogue: TMEM lane = k, column = n; four warps take 128 n each.  A warp's 32 lanes store 32
-        // adjacent k of one n.
+        // Epilogue: TMEM lane = k (1 and 2 of every four exchanged), column = n; four warps take 128 n each.
+        // A warp's 32 lanes store 32 adjacent k of one n.
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
         const int n_off = (warp - kCtlWarps >= 4) ? kTile / 2 : 0;
         const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), 0);
@@ -478,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             for (int j = 0; j < kTile / 2; ++j) acc[j] = 0.0f;
             for (int64_t b = it.first; b < it.last; b += kRun, ++runs) {
                 const int buf = (int)(runs & 1);
-                ok = ok && wait_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit_ns);
+                ok = ok && wait_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < kTile / 2; c += 16) {
@@ -495,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
 #pragma unroll
                 for (int j = 0; j < kTile / 2; ++j) acc[j] = __uint_as_float(0x7fffffffu);
             }
-            const int kl = (int)rank * kHalf + quarter * 32 + lane;
+            const int kl = (int)rank * kHalf + quarter * 32 + (lane & 28) + ((lane & 1) << 1) + (lane >> 1 & 1);
             const int64_t k = (int64_t)it.tk * kTile + kl;
             const int n0 = it.tn * kTile + n_off;
             if (it.part >= 0) {
@@ -518,49 +563,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        // Decode: four warps take the even stages, four the odd ones; a warp 16 tokens, 8 lanes a token and
-        // 16 codes a lane at a time
+        // Decode: four warps take the even stages, four the odd ones; a warp 16 tokens, a lane 16 codes at a
+        // time.  Eight lanes read 64 bytes of codes of tokens t and t ^ 5 and store 8 pieces of 16 bytes: with
+        // the 128-byte swizzle of both (piece ^ (token & 7)) either access covers all banks.
         const int w = warp - kCtlWarps - kEpiWarps;
-        const int j = lane & 7, tr = (w & 3) * 16 + (lane >> 3);
         const uint32_t ready = in_cta(smem_u32(&sh.ready[0]), 0);
-        Ring r;
-        int64_t stage = 0;
-        bool ok = true;
+        int64_t total = 0;
         Item it;
-        for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
-            for (int64_t b = it.first; b < it.last; ++b, ++stage, r.next()) {
-                if (((int)stage & 1) != (w >> 2)) continue;
-                if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t base = stages + r.st * kStageBytes;
+        for (int64_t i = pair; item_of(p.s, i, it); i += pairs) total += it.last - it.first;
+        const int c = lane & 3, block = lane >> 3 & 1;
+        const int pr = lane >> 4, x = (lane & 4) ? pr ^ 5 : pr;      // token & 7 of the first of four
+        const int t = (w & 3) * 16 + x;
+        const uint32_t from = stages + kBBytes + t * 128 + (((block * 4 + c) ^ x) << 4);
+        const uint32_t to = decoded + block * kBlockBytes + t * 128 + (((2 * c) ^ x) << 4);  // and the piece beside it
+        const uint32_t ex = exps + t * 4 + block * 2 + (c >> 1);
+        Ring<kLoads> r;
+        Ring<kDecoded> ra;
+        r.next(w >> 2);
+        ra.next(w >> 2);
+        for (int64_t i = w >> 2; i < total; i += 2, r.next(2), ra.next(2)) {
+            if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit) ||
+                (ra.wrapped && !wait_warp(smem_u32(&sh.a_empty[ra.st]), ra.ph ^ 1u, p.limit)))
+                break;
+            const uint32_t off = r.st * kLoadBytes, off_a = ra.st * kABytes;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int ts = tr + 4 * h;
-                    uint4 c, v[2];
-                    uint32_t E;
+            for (int g = 0; g < 2; ++g) {  // tokens t, t + 2 (its swizzle differs in bit 1), and 8 on
+                uint4 q[2];
+                uint32_t E[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w)
-                                 : "r"(base + kABytes + kBBytes + ts * 128 + j * 16));
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(E) : "r"(exps + r.st * kExpBytes + ts * 4 + (j >> 1)));
-                    decode16<BF16>(c, E, v[0], v[1]);
-                    // 16-byte pieces (j & 3) * 2 and + 1 of block j >> 2, swizzled by the token; lanes of the
-                    // two blocks store their pieces in opposite order, so that 8 lanes cover all banks
-                    const uint32_t row = base + (j >> 2) * kBlockBytes + ts * 128;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int hi = x ^ (j >> 2);
-                        const uint4 s = hi ? v[1] : v[0];
-                        const uint32_t at = row + ((((j & 3) * 2 + hi) ^ (ts & 7)) << 4);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(s.x), "r"(s.y), "r"(s.z), "r"(s.w)
-                                     : "memory");
-                    }
+                                 : "=r"(q[h].x), "=r"(q[h].y), "=r"(q[h].z), "=r"(q[h].w)
+                                 : "r"((from ^ (h * 32)) + h * 256 + g * 1024 + off));
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(E[h]) : "r"(ex + h * 8 + g * 32 + r.st * kExpBytes));
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) arrive_cluster(ready + r.st * 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[8];
+                    decode16<BF16>(q[h], E[h], o);
+                    const uint32_t at = (to ^ (h * 32)) + h * 256 + g * 1024 + off_a;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                 : "memory");
+                }
             }
+            // A is in this CTA's shared memory, whose stores the fence has made visible to its tensor cores: the
+            // signal carries no more than that, and a release to the cluster would take some 1300 cycles
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(ready + ra.st * 8);
         }
     }
     __syncwarp();
@@ -707,8 +759,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     p.sdw = a.dw_stride;
     p.accumulate = a.accumulate;
     p.parts = reinterpret_cast<float *>(a.ws + w.parts);
-    // a tile's sums take about 0.3 us a stage; 20 us a stage and two seconds are never reached but by a fault
-    p.limit_ns = 2000000000ull + 20000ull * (unsigned long long)p.s.blocks;
+    p.limit = 4000000000ll;  // two seconds; the longest wait, for a run of stages, is some microseconds
 
     const void *dy = a.dy.p;
     int64_t pitch = a.tokens > 1 ? a.dy.stride : staged_pitch(a.out);
@@ -735,7 +786,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
         const cuuint64_t strides[1] = {(cuuint64_t)l.code_pitch};
         const cuuint32_t box[2] = {kHalf, kTok};
         if (encode(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(a.ckpt), dims, strides, box, ones,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
