@@ -50,7 +50,7 @@ constexpr int kRun = 8;
 // 128 sums in each thread's registers, more than an even split gives: see kRegs*.
 constexpr int kCtlWarps = 4, kEpiWarps = 8, kConvWarps = 8;
 constexpr int kThreads = (kCtlWarps + kEpiWarps + kConvWarps) * 32;
-constexpr int kRegsLaunch = 96, kRegsCtl = 64, kRegsEpi = 168, kRegsConv = 40;
+constexpr int kRegsLaunch = 96, kRegsCtl = 48, kRegsEpi = 168, kRegsConv = 48;
 static_assert(kCtlWarps * kRegsCtl + kEpiWarps * kRegsEpi + kConvWarps * kRegsConv <= kThreads / 32 * kRegsLaunch,
               "setmaxnreg: the shares come from the block's own registers at launch");
 constexpr int kPairs = 74;               // CTA pairs of the 148 SMs: the schedule is made for these
@@ -224,35 +224,30 @@ __device__ __forceinline__ uint32_t bits2(__half2 x) { return *reinterpret_cast<
 // 16-bit lanes holding the codes' bytes, even (i = 0) or odd (i = 1) ones of a word.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) { return (i ? w >> 8 : w) & 0x00ff00ffu; }
 
+// Exponents whose codes decode16 takes; decode16_any takes all.
+template <bool BF16>
+__device__ __forceinline__ bool usual(uint32_t E)
+{
+    return BF16 ? E - 7u <= 245u : E - 109u <= 32u;
+}
+
 template <bool BF16>
 __device__ __forceinline__ void decode16(const uint4 &codes, uint32_t E, uint32_t (&o)[8])
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     if constexpr (BF16) {
-        if (E - 7u <= 245u) {
-            // 2^-126 <= s <= 2^119.  bf16 0x4300 | (q + 128) is 256 + q for q < 0 and 256 + 2 q for q >= 0
-            // (its step doubles at 256).  y = that less 256, times s, is q s or 2 q s; half of y where it is
-            // positive, taken off, leaves q s.  Every step is exact.
-            const __nv_bfloat162 s = bf2(E * 0x00800080u - 6u * 0x00800080u);
-            const __nv_bfloat162 half = __hmul2(s, bf2(0x3f003f00u)), c = __hmul2(s, bf2(0xc380c380u)),
-                                 hc = __hmul2(s, bf2(0xc300c300u));
+        // 2^-126 <= s <= 2^119.  bf16 0x4300 | (q + 128) is 256 + q for q < 0 and 256 + 2 q for q >= 0 (its
+        // step doubles at 256).  y = that less 256, times s, is q s or 2 q s; half of y where it is positive,
+        // taken off, leaves q s.  Every step is exact.
+        const __nv_bfloat162 s = bf2(E * 0x00800080u - 6u * 0x00800080u);
+        const __nv_bfloat162 half = __hmul2(s, bf2(0x3f003f00u)), c = __hmul2(s, bf2(0xc380c380u)),
+                             hc = __hmul2(s, bf2(0xc300c300u));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const __nv_bfloat162 v = bf2(code_pair(w[i >> 1], i & 1) ^ 0x43804380u);
-                o[i] = bits2(__hsub2(__hfma2(v, s, c), __hfma2_relu(v, half, hc)));
-            }
-        } else {
-            // the ends of the range, NaN, and E = 0 (groups of zeros): 0x4300 | m is 128 + m for 7 bits m, and
-            // q its low 7 bits less 128 times its sign bit, exact, times the scale
-            const uint32_t b = E == 255u ? 0x7fffu : E > 6u ? (E - 6u) << 7 : 0x40u >> (6u - E);
-            const __nv_bfloat162 s = bf2(b | b << 16);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t p = code_pair(w[i >> 1], i & 1);
-                o[i] = bits2(__hmul2(__hsub2(bf2((p & 0x007f007fu) | 0x43004300u), bf2((p & 0x00800080u) | 0x43004300u)), s));
-            }
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = bf2(code_pair(w[i >> 1], i & 1) ^ 0x43804380u);
+            o[i] = bits2(__hsub2(__hfma2(v, s, c), __hfma2_relu(v, half, hc)));
         }
-    } else if (E - 109u <= 32u) {
+    } else {
         // 2^-24 <= s <= 2^8.  fp16 0x6400 | m is 1024 + m; (1024 + q + 128) - 1152 is exact, the product with
         // the scale rounds once at most and stays below 65504
         const uint32_t b = E >= 119u ? (E - 118u) << 10 : 1u << (E - 109u);
@@ -260,8 +255,25 @@ __device__ __forceinline__ void decode16(const uint4 &codes, uint32_t E, uint32_
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             o[i] = bits2(__hmul2(__hsub2(h2(code_pair(w[i >> 1], i & 1) ^ 0x64806480u), h2(0x64806480u)), s));
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void decode16_any(const uint4 &codes, uint32_t E, uint32_t (&o)[8])
+{
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    if constexpr (BF16) {
+        // 0x4300 | m is 128 + m for 7 bits m, and q its low 7 bits less 128 times its sign bit: exact, and so
+        // is the product with the scale, down to bf16's smallest subnormal
+        const uint32_t b = E == 255u ? 0x7fffu : E > 6u ? (E - 6u) << 7 : 0x40u >> (6u - E);
+        const __nv_bfloat162 s = bf2(b | b << 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t p = code_pair(w[i >> 1], i & 1);
+            o[i] = bits2(__hmul2(__hsub2(bf2((p & 0x007f007fu) | 0x43004300u), bf2((p & 0x00800080u) | 0x43004300u)), s));
+        }
     } else {
-        // groups beyond fp16's range: below half its smallest step, or saturated, or NaN
+        // also groups beyond fp16's range: below half its smallest step, or saturated, or NaN
         const float s = group_scale(E);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -586,28 +598,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 (ra.wrapped && !wait_warp(smem_u32(&sh.a_empty[ra.st]), ra.ph ^ 1u, p.limit)))
                 break;
             const uint32_t off = r.st * kLoadBytes, off_a = ra.st * kABytes;
+            uint4 q[4];
+            uint32_t E[4];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // tokens t, t + 2 (its swizzle differs in bit 1), and 8 on
-                uint4 q[2];
-                uint32_t E[2];
+            for (int h = 0; h < 4; ++h) {  // tokens t, t + 2 (its swizzle differs in bit 1), and 8 on
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(q[h].x), "=r"(q[h].y), "=r"(q[h].z), "=r"(q[h].w)
+                             : "r"((from ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off));
+                asm volatile("ld.shared.u8 %0, [%1];"
+                             : "=r"(E[h])
+                             : "r"(ex + (h & 1) * 8 + (h >> 1) * 32 + r.st * kExpBytes));
+            }
+            auto put = [&](int h, const uint32_t (&o)[8]) {
+                const uint32_t at = (to ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off_a;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                             : "memory");
+            };
+            if (usual<BF16>(E[0]) && usual<BF16>(E[1]) && usual<BF16>(E[2]) && usual<BF16>(E[3])) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(q[h].x), "=r"(q[h].y), "=r"(q[h].z), "=r"(q[h].w)
-                                 : "r"((from ^ (h * 32)) + h * 256 + g * 1024 + off));
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(E[h]) : "r"(ex + h * 8 + g * 32 + r.st * kExpBytes));
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     uint32_t o[8];
                     decode16<BF16>(q[h], E[h], o);
-                    const uint32_t at = (to ^ (h * 32)) + h * 256 + g * 1024 + off_a;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                 : "memory");
+                    put(h, o);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t o[8];
+                    decode16_any<BF16>(q[h], E[h], o);
+                    put(h, o);
                 }
             }
+            __syncwarp();
             // A is in this CTA's shared memory, whose stores the fence has made visible to its tensor cores: the
             // signal carries no more than that, and a release to the cluster would take some 1300 cycles
             fence_proxy_async();
