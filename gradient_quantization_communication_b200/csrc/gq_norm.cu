@@ -31,6 +31,7 @@ struct Params {
     float eps;
     float *part_g, *part_b;
     int parts;
+    int G, slots;        // rows in registers: warps a row, rows a block
 };
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -44,10 +45,23 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-// A lane's 8 values of gamma or beta (fill where there is none).
+// A lane's 8 values of gamma or beta (fill where there is none).  They are read again for every row: from
+// L1, which costs less than the registers that would hold them.
 template <typename T, bool VEC>
 __device__ __forceinline__ void param_load(float (&v)[8], const void *p, int f32, float fill, int base, int lane, int cols)
 {
+    if (p && f32 && VEC && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        Raw<float> r;
+        chunk_load<float, true>(r, static_cast<const float *>(p), base, lane, cols);
+        to_floats(r, v);
+        return;
+    }
+    if (p && !f32 && VEC && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        Raw<T> r;
+        chunk_load<T, true>(r, static_cast<const T *>(p), base, lane, cols);
+        to_floats(r, v);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = chunk_col<VEC>(base, lane, j);
@@ -69,7 +83,217 @@ __device__ __forceinline__ float row_sum(float v, float *buf, int G, int warp, i
     return s;
 }
 
-// One block per row at a time, any number of columns; the row is read three times (twice from cache).
+// ---------------------------------------------------------------------------------------------
+// Rows kept in registers: up to kRegCols columns.  G warps take a row, NC chunks of 256 columns each; a block
+// holds `slots` such groups and walks the rows, and loads its next row before it works on the present one.
+// ---------------------------------------------------------------------------------------------
+constexpr int kRegCols = 8192;
+
+struct Shape {
+    int G, nc, slots;
+};
+// Two chunks a warp (one where a row has no more): 16 values a lane leave room for the next row's in 128
+// registers, and the fewest warps share a row's sums.  Blocks of about 8 warps.
+inline Shape shape_of(int64_t cols)
+{
+    const int n = (int)((cols + kChunk - 1) / kChunk);
+    Shape s;
+    s.nc = n > 1 ? 2 : 1;
+    s.G = (n + s.nc - 1) / s.nc;
+    s.slots = s.G >= 8 ? 1 : 8 / s.G;
+    return s;
+}
+
+// Sums of N values over the G warps of a slot.  `buf` must not be written again before another barrier of the
+// slot has passed: callers alternate between two.
+template <int N>
+__device__ __forceinline__ void slot_sum(float (&v)[N], float (*buf)[N], int G, int slot, int wslot, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (G == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) buf[slot * G + wslot][i] = v[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += buf[slot * G + g][i];
+    }
+}
+
+template <typename T, bool VEC, int NC, bool KEEP>
+__global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params p)
+{
+    __shared__ float buf[2][16][1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
+    const int slot = warp / G, wslot = warp - slot * G;
+    const float inv_c = 1.0f / (float)p.cols;
+    const int64_t step = (int64_t)gridDim.x * p.slots;
+    int64_t row = (int64_t)blockIdx.x * p.slots + slot;
+    Raw<T> next[NC];
+    if (row < p.rows) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            chunk_load<T, VEC>(next[c], static_cast<const T *>(p.x) + row * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
+    }
+    for (; row < p.rows; row += step) {
+        float v[NC][8];
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            to_floats(next[c], v[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] += v[c][j];
+        }
+        if (row + step < p.rows) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                chunk_load<T, VEC>(next[c], static_cast<const T *>(p.x) + (row + step) * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
+        }
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) ckpt_store<VEC>(v[c], p.k, row, (wslot + c * G) * kChunk, lane);
+        }
+        slot_sum<1>(s, buf[0], G, slot, wslot, lane);
+        const float mean = s[0] * inv_c;
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = chunk_col<VEC>((wslot + c * G) * kChunk, lane, j) < p.cols ? v[c][j] - mean : 0.0f;
+                v[c][j] = d;
+                ss[0] = __fmaf_rn(d, d, ss[0]);
+            }
+        slot_sum<1>(ss, buf[1], G, slot, wslot, lane);
+        const float rstd = 1.0f / sqrtf(ss[0] * inv_c + p.eps);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int base = (wslot + c * G) * kChunk;
+            float g[8], b[8];
+            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            param_load<T, VEC>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn(v[c][j] * rstd, g[j], b[j]);
+            Raw<T> r;
+            from_floats(r, v[c]);
+            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
+        }
+        if (wslot == 0 && lane == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+    }
+}
+
+// dx, and the block's partial sums of dgamma and dbeta (part_g, part_b: one row a block).
+template <typename T, bool VEC, int NC, bool FROM_CKPT>
+__global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params p)
+{
+    extern __shared__ float fold[];  // slots > 1: the block's sums, cols of dgamma and cols of dbeta
+    __shared__ float buf[2][16][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
+    const int slot = warp / G, wslot = warp - slot * G;
+    const float inv_c = 1.0f / (float)p.cols;
+    const int64_t step = (int64_t)gridDim.x * p.slots;
+    int64_t row = (int64_t)blockIdx.x * p.slots + slot;
+    Raw<T> ndy[NC], nx[FROM_CKPT ? 1 : NC];
+    RawCkpt<VEC> nk[FROM_CKPT ? NC : 1];
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t r) {
+        nmean = __ldg(p.mean + r);
+        nrstd = __ldg(p.rstd + r);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int base = (wslot + c * G) * kChunk;
+            chunk_load<T, VEC>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
+            if constexpr (FROM_CKPT) ckpt_load<VEC>(nk[c], p.k, r, base, lane);
+            else chunk_load<T, VEC>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
+        }
+    };
+    float sg[NC][8], sb[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sg[c][j] = sb[c][j] = 0.0f;
+    if (row < p.rows) fetch(row);
+    int turn = 0;
+    for (; row < p.rows; row += step, turn ^= 1) {
+        float x[NC][8], d[NC][8];
+        const float mean = nmean, rstd = nrstd;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            to_floats(ndy[c], d[c]);
+            if constexpr (FROM_CKPT) ckpt_floats<VEC>(nk[c], x[c]);
+            else to_floats(nx[c], x[c]);
+        }
+        if (row + step < p.rows) fetch(row + step);
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int base = (wslot + c * G) * kChunk;
+            float g[8];
+            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // past the last column dy reads as 0, and xh is made 0 so that no infinity meets it
+                const float xh = chunk_col<VEC>(base, lane, j) < p.cols ? (x[c][j] - mean) * rstd : 0.0f;
+                sg[c][j] = __fmaf_rn(d[c][j], xh, sg[c][j]);
+                sb[c][j] += d[c][j];
+                const float gd = chunk_col<VEC>(base, lane, j) < p.cols ? g[j] * d[c][j] : 0.0f;
+                x[c][j] = xh;
+                d[c][j] = gd;
+                s[0] += gd;
+                s[1] = __fmaf_rn(gd, xh, s[1]);
+            }
+        }
+        slot_sum<2>(s, buf[turn], G, slot, wslot, lane);
+        const float c0 = s[0] * inv_c, c1 = s[1] * inv_c;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[c][j] = rstd * __fmaf_rn(-x[c][j], c1, d[c][j] - c0);
+            Raw<T> r;
+            from_floats(r, d[c]);
+            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, (wslot + c * G) * kChunk, lane, p.cols);
+        }
+    }
+    if (!p.part_b) return;
+    // the slots' sums, slot by slot in order
+    for (int t = 0; t < p.slots; ++t) {
+        if (slot == t) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int col = chunk_col<VEC>((wslot + c * G) * kChunk, lane, j);
+                    if (col >= p.cols) continue;
+                    float a = sg[c][j], b = sb[c][j];
+                    if (t > 0) {
+                        a += fold[col];
+                        b += fold[p.cols + col];
+                    }
+                    if (t + 1 < p.slots) {
+                        fold[col] = a;
+                        fold[p.cols + col] = b;
+                    } else {
+                        p.part_g[(int64_t)blockIdx.x * p.cols + col] = a;
+                        p.part_b[(int64_t)blockIdx.x * p.cols + col] = b;
+                    }
+                }
+        }
+        if (p.slots > 1) __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Wider rows: one block per row at a time, any number of columns; the row is read three times (twice from
+// cache).
+// ---------------------------------------------------------------------------------------------
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Params p)
 {
@@ -268,14 +492,33 @@ Params params(const NormArgs &a)
 
 bool rows_aligned(int64_t rows, const Mat &m, int per16) { return !m.p || rows == 1 || m.stride % per16 == 0; }
 
+template <typename T, int NC>
+cudaError_t forward_reg(const Params &p, bool vec, cudaStream_t s)
+{
+    auto kern = vec ? (p.k.codes ? k_forward<T, true, NC, true> : k_forward<T, true, NC, false>)
+                    : (p.k.codes ? k_forward<T, false, NC, true> : k_forward<T, false, NC, false>);
+    const int threads = p.G * p.slots * 32;
+    int per_sm = 0, sms = 0;
+    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), threads, 0, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    const int64_t need = (p.rows + p.slots - 1) / p.slots, most = (int64_t)per_sm * sms;
+    kern<<<(unsigned)(need < most ? need : most), threads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t forward(const NormArgs &a, cudaStream_t s)
 {
     const int per16 = 16 / (int)sizeof(T);
     const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16);
-    const Params p = params(a);
-    const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
-    const int warps = chunks < 16 ? (int)chunks : 16;
+    Params p = params(a);
+    if (a.cols <= kRegCols) {
+        const Shape sh = shape_of(a.cols);
+        p.G = sh.G;
+        p.slots = sh.slots;
+        return sh.nc == 1 ? forward_reg<T, 1>(p, vec, s) : forward_reg<T, 2>(p, vec, s);
+    }
+    const int warps = 16;
     auto kern = vec ? k_forward_any<T, true> : k_forward_any<T, false>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
@@ -285,15 +528,31 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <typename T, int NC>
+cudaError_t backward_reg(const Params &p, bool vec, cudaStream_t s)
+{
+    auto kern = vec ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
+                    : (p.x ? k_backward<T, false, NC, false> : k_backward<T, false, NC, true>);
+    const size_t smem = p.slots > 1 ? (size_t)p.cols * 2 * sizeof(float) : 0;
+    kern<<<(unsigned)p.parts, p.G * p.slots * 32, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t backward(const NormArgs &a, cudaStream_t s)
 {
     const int per16 = 16 / (int)sizeof(T);
     const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16) && rows_aligned(a.rows, a.dy, per16);
-    const Params p = params(a);
-    if (a.rows > 0) {
+    Params p = params(a);
+    if (a.rows > 0 && a.cols <= kRegCols) {
+        const Shape sh = shape_of(a.cols);
+        p.G = sh.G;
+        p.slots = sh.slots;
+        const cudaError_t e = sh.nc == 1 ? backward_reg<T, 1>(p, vec, s) : backward_reg<T, 2>(p, vec, s);
+        if (e != cudaSuccess) return e;
+    } else if (a.rows > 0) {
         const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
-        const int warps = chunks < 16 ? (int)chunks : 16;
+        const int warps = 16;
         auto kern = vec ? k_backward_rows_any<T, true> : k_backward_rows_any<T, false>;
         int per_sm = 0, sms = 0;
         cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
@@ -333,8 +592,13 @@ cudaError_t colsum(int64_t rows, int64_t cols, Mat dy, float *parts, cudaStream_
 
 int64_t norm_parts(int64_t rows, int64_t cols)
 {
-    (void)cols;
-    return rows < 296 ? rows : 296;
+    if (rows <= 0) return 0;
+    if (cols > kRegCols) return rows < 296 ? rows : 296;
+    // blocks of the backward pass: two an SM, and at least two rows to each of a block's slots, so that the
+    // partial sums stay fewer bytes than the rows
+    const int64_t rows_a_block = 2 * shape_of(cols).slots;
+    const int64_t n = (rows + rows_a_block - 1) / rows_a_block;
+    return n < 296 ? n : 296;
 }
 
 int64_t colsum_parts(int64_t rows, int64_t cols)
