@@ -1,7 +1,8 @@
 // gq_act.cu -- pack and unpack of the 8-bit activation checkpoint, and activation functions whose
 // forward pass writes the checkpoint of its input and whose backward pass reads it.
 //
-// All are one pass over their tensors: a warp takes chunks of 256 columns of a row, two at a time.
+// All are one pass over their tensors: a warp takes chunks of 256 columns of a row, two at a time.  Bounded by
+// the bytes; the arithmetic leaves some 27 instruction slots an element at full bandwidth in 16-bit types.
 #include "gq_act.cuh"
 #include "gq_act.h"
 #include "gq_internal.h"
@@ -16,28 +17,70 @@ constexpr int kThreads = 256;
 //              tail's digits, where 1 + erf would cancel.
 //   GELU tanh  x s(2u), u = sqrt(2/pi) (x + 0.044715 x^3)  [= x (1 + tanh u) / 2], s the logistic function;
 //   SiLU       x s(x);  s (1 + x (1 - s)).
-template <int KIND>
-struct Fn;
+// In 16-bit types, whose own step hides it, the exponential is the hardware's (2^-21 or so), and Phi's tail
+// comes from a polynomial; binary32 calls expf and erfcf.
+template <bool FAST>
+__device__ __forceinline__ float exp_neg(float t)
+{
+    return FAST ? __expf(t) : expf(t);
+}
 
 // s(t) = 1 / (1 + exp(-t)) and 1 - s, through exp(-|t|) <= 1: neither overflows nor cancels.
+template <bool FAST>
 __device__ __forceinline__ void logistic(float t, float &s, float &one_minus)
 {
-    const float e = expf(-fabsf(t));
+    const float e = exp_neg<FAST>(-fabsf(t));
     const float a = __fdividef(1.0f, 1.0f + e), b = e * a;
     s = t >= 0.0f ? a : b;
     one_minus = t >= 0.0f ? b : a;
 }
 
-template <>
-struct Fn<GQ_FN_GELU> {
-    static __device__ __forceinline__ float f(float x) { return 0.5f * x * erfcf(-x * 0.70710678f); }
+// Phi(x) and exp(-x^2 / 2).
+template <bool FAST>
+__device__ __forceinline__ void normal(float x, float &Phi, float &e)
+{
+    e = exp_neg<FAST>(-0.5f * x * x);
+    if constexpr (FAST) {
+        // Phi(-z) exp(z^2 / 2) = t P(t) with t = 1 / (1 + 0.31 z), z = |x|: the smoothest of such maps of
+        // [0, inf) to (0, 1].  P has degree 7, fitted on z <= 14.5 (beyond, the tail is below binary32's
+        // range) by Lawson's weighted least squares to the smallest largest relative error, 1.6e-7; 5e-7 in
+        // binary32 arithmetic.
+        const float t = __fdividef(1.0f, __fmaf_rn(0.31f, fabsf(x), 1.0f));
+        float h = 0.035870399326086044f;
+        h = __fmaf_rn(h, t, -0.1417304277420044f);
+        h = __fmaf_rn(h, t, 0.15529736876487732f);
+        h = __fmaf_rn(h, t, -0.015128081664443016f);
+        h = __fmaf_rn(h, t, 0.11023717373609543f);
+        h = __fmaf_rn(h, t, 0.10772977769374847f);
+        h = __fmaf_rn(h, t, 0.12406746298074722f);
+        h = __fmaf_rn(h, t, 0.12365640699863434f);
+        const float tail = h * t * e;
+        Phi = x >= 0.0f ? 1.0f - tail : tail;
+    } else {
+        Phi = 0.5f * erfcf(-x * 0.70710678f);
+    }
+}
+
+template <int KIND, bool FAST>
+struct Fn;
+
+template <bool FAST>
+struct Fn<GQ_FN_GELU, FAST> {
+    static __device__ __forceinline__ float f(float x)
+    {
+        float P, e;
+        normal<FAST>(x, P, e);
+        return x * P;
+    }
     static __device__ __forceinline__ float df(float x)
     {
-        return __fmaf_rn(x * 0.39894228f, expf(-0.5f * x * x), 0.5f * erfcf(-x * 0.70710678f));
+        float P, e;
+        normal<FAST>(x, P, e);
+        return __fmaf_rn(x * 0.39894228f, e, P);
     }
 };
-template <>
-struct Fn<GQ_FN_GELU_TANH> {
+template <bool FAST>
+struct Fn<GQ_FN_GELU_TANH, FAST> {
     static constexpr float c = 1.5957691f;  // 2 sqrt(2/pi)
     // s is 0 or 1 in binary32 beyond |x| = 30; there x^3 need not be formed, which could overflow
     static __device__ __forceinline__ float bounded(float x) { return max_nan(min_nan(x, 30.0f), -30.0f); }
@@ -45,29 +88,29 @@ struct Fn<GQ_FN_GELU_TANH> {
     {
         const float b = bounded(x);
         float s, r;
-        logistic(c * __fmaf_rn(0.044715f * b, b * b, b), s, r);
+        logistic<FAST>(c * __fmaf_rn(0.044715f * b, b * b, b), s, r);
         return x * s;
     }
     static __device__ __forceinline__ float df(float x)
     {
         const float b = bounded(x);
         float s, r;
-        logistic(c * __fmaf_rn(0.044715f * b, b * b, b), s, r);
+        logistic<FAST>(c * __fmaf_rn(0.044715f * b, b * b, b), s, r);
         return __fmaf_rn(b * s * r, c * __fmaf_rn(0.134145f * b, b, 1.0f), s);
     }
 };
-template <>
-struct Fn<GQ_FN_SILU> {
+template <bool FAST>
+struct Fn<GQ_FN_SILU, FAST> {
     static __device__ __forceinline__ float f(float x)
     {
         float s, r;
-        logistic(x, s, r);
+        logistic<FAST>(x, s, r);
         return x * s;
     }
     static __device__ __forceinline__ float df(float x)
     {
         float s, r;
-        logistic(x, s, r);
+        logistic<FAST>(x, s, r);
         return s * __fmaf_rn(x, r, 1.0f);
     }
 };
@@ -75,58 +118,65 @@ struct Fn<GQ_FN_SILU> {
 struct Params {
     int64_t rows, chunks;  // chunks: rows * chunks per row
     int cols, per_row;
+    int64_t drow;          // warps of the grid = drow rows of chunks and dchunk chunks
+    int dchunk;
     const void *a;
     void *b;
     int64_t sa, sb;
     Ckpt k;
 };
 
-template <typename T, int OP, int KIND, bool VEC>
+template <typename T, int OP, int KIND, bool AL>
 __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params p)
 {
     constexpr int U = 2;
+    constexpr bool READS = OP != kUnpack, WRITES = OP != kPack, DECODES = OP == kUnpack || OP == kBackward;
+    using F = Fn<KIND, sizeof(T) == 2>;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t id0 = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); id0 < p.chunks; id0 += U * warps) {
-        Raw<T> raw[U];
-        RawCkpt<VEC> rk[U];
-        int64_t row[U];
+    int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    // (row, chunk of the row) of chunk id; a step of `warps` chunks is (drow, dchunk), without divisions
+    int64_t row = id / p.per_row;
+    int chunk = (int)(id - row * p.per_row);
+    for (; id < p.chunks; id += U * warps) {
+        Raw<T, AL> raw[U];
+        RawCkpt rk[U];
+        int64_t rows[U];
         int base[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t id = id0 + u * warps;
-            if (id >= p.chunks) break;
-            row[u] = id / p.per_row;
-            base[u] = (int)(id - row[u] * p.per_row) * kChunk;
-            if constexpr (OP != kUnpack)
-                chunk_load<T, VEC>(raw[u], static_cast<const T *>(p.a) + row[u] * p.sa, base[u], lane, p.cols);
-            if constexpr (OP == kUnpack || OP == kBackward) ckpt_load<VEC>(rk[u], p.k, row[u], base[u], lane);
+            rows[u] = row;
+            base[u] = chunk * kChunk;
+            row += p.drow;
+            chunk += p.dchunk;
+            if (chunk >= p.per_row) {
+                chunk -= p.per_row;
+                ++row;
+            }
+            if (id + u * warps < p.chunks) {
+                if constexpr (READS)
+                    chunk_load<T, AL>(raw[u], static_cast<const T *>(p.a) + rows[u] * p.sa, base[u], lane, p.cols);
+                if constexpr (DECODES) ckpt_load(rk[u], p.k, rows[u], base[u], lane);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (id0 + u * warps >= p.chunks) break;
-            float v[8], o[8];
-            if constexpr (OP == kPack || OP == kForward || OP == kForwardKeep) to_floats(raw[u], v);
-            else ckpt_floats<VEC>(rk[u], v);
-            if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store<VEC>(v, p.k, row[u], base[u], lane);
-            if constexpr (OP == kPack) continue;
-            if constexpr (OP == kUnpack) {
-                saturate<T>(v);
+            if (id + u * warps >= p.chunks) break;
+            float in[8], v[8], o[8];
+            if constexpr (READS) to_floats(in_place<T, AL>(raw[u], static_cast<const T *>(p.a) + rows[u] * p.sa), in);
+            if constexpr (DECODES) ckpt_floats(rk[u], v);
+            if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store(in, p.k, rows[u], base[u], lane);
+            if constexpr (OP == kUnpack) saturate<T>(v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = v[j];
-            } else if constexpr (OP == kBackward) {
-                float d[8];
-                to_floats(raw[u], d);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = d[j] * Fn<KIND>::df(v[j]);
-            } else if constexpr (OP != kPack) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = Fn<KIND>::f(v[j]);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (OP == kUnpack) o[j] = v[j];
+                else if constexpr (OP == kBackward) o[j] = in[j] * F::df(v[j]);
+                else if constexpr (WRITES) o[j] = F::f(in[j]);
             }
-            if constexpr (OP != kPack) {
-                Raw<T> out;
+            if constexpr (WRITES) {
+                Words<T> out;
                 from_floats(out, o);
-                chunk_store<T, VEC>(out, static_cast<T *>(p.b) + row[u] * p.sb, base[u], lane, p.cols);
+                chunk_store<T, AL>(out, static_cast<T *>(p.b) + rows[u] * p.sb, base[u], lane, p.cols);
             }
         }
     }
@@ -147,15 +197,18 @@ cudaError_t launch(const ActArgs &a, cudaStream_t stream)
     p.sb = a.b.stride;
     p.k = Ckpt{static_cast<uint8_t *>(a.ckpt), static_cast<uint8_t *>(a.ckpt) + l.exps_off, (int)l.code_pitch,
                (int)l.exp_pitch};
-    // 16-byte accesses need every row to start on 16 bytes (the bases do)
+    // whether every row starts on 16 bytes (the bases do)
     const int per16 = 16 / (int)sizeof(T);
-    const bool vec = (OP == kUnpack || a.rows == 1 || p.sa % per16 == 0) && (OP == kPack || a.rows == 1 || p.sb % per16 == 0);
-    auto kern = vec ? k_act<T, OP, KIND, true> : k_act<T, OP, KIND, false>;
+    const bool al = (OP == kUnpack || a.rows == 1 || p.sa % per16 == 0) && (OP == kPack || a.rows == 1 || p.sb % per16 == 0);
+    auto kern = al ? k_act<T, OP, KIND, true> : k_act<T, OP, KIND, false>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     const int64_t need = (p.chunks + kThreads / 32 - 1) / (kThreads / 32);
     const int64_t grid = need < (int64_t)per_sm * sms ? need : (int64_t)per_sm * sms;
+    const int64_t warps = grid * (kThreads / 32);
+    p.drow = warps / p.per_row;
+    p.dchunk = (int)(warps - p.drow * p.per_row);
     kern<<<(unsigned)grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

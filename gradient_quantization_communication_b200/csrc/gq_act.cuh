@@ -22,35 +22,80 @@ namespace gq {
 constexpr int kChunk = 256;  // columns of a row that one warp handles at a time: 8 per lane
 
 // ---------------------------------------------------------------------------------------------
-// A lane's 8 elements, as loaded.
-// VEC: columns base + 8 * lane + j, 16-byte accesses (row starts 16-byte aligned).
-// else: columns base + 32 * j + lane, one element per access (any row start).
+// A lane's 8 elements, columns base + 8 * lane + j of a row, as loaded.
+// AL: every row starts on 16 bytes, and the 8 elements are one or two 16-byte accesses.
+// else: rows start anywhere (on their element size).  A lane loads the aligned 16-byte pieces its elements
+// lie in and shifts them into place when it uses them; a store shifts its elements, with the next lane's
+// first ones behind them, onto aligned pieces.  Loading element by element took 2 to 3 times as long.
 // ---------------------------------------------------------------------------------------------
 template <typename T>
+struct Words {
+    uint32_t w[2 * sizeof(T)];  // the 8 elements
+};
+template <typename T, bool AL>
 struct Raw {
-    uint32_t w[2 * sizeof(T)];
+    uint32_t w[2 * sizeof(T) + (AL ? 0 : 4)];
 };
 
 __device__ __forceinline__ uint32_t elem_bits(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ uint32_t elem_bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 __device__ __forceinline__ uint32_t elem_bits(__half x) { return __half_as_ushort(x); }
 
+// Element j of an array of words.
 template <typename T>
-__device__ __forceinline__ void raw_set(Raw<T> &r, int j, uint32_t bits)
+__device__ __forceinline__ void elem_set(uint32_t *w, int j, uint32_t bits)
 {
     if constexpr (sizeof(T) == 4) {
-        r.w[j] = bits;
+        w[j] = bits;
     } else {
-        if (j & 1) r.w[j >> 1] |= bits << 16;
-        else r.w[j >> 1] = bits;
+        if (j & 1) w[j >> 1] |= bits << 16;
+        else w[j >> 1] = bits;
+    }
+}
+template <typename T>
+__device__ __forceinline__ T elem_get(const uint32_t *w, int j)
+{
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(w[j]);
+    } else {
+        const unsigned short h = (unsigned short)((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
+        if constexpr (__is_same(T, __half)) return __ushort_as_half(h);
+        else return __ushort_as_bfloat16(h);
     }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void chunk_load(Raw<T> &r, const T *row, int base, int lane, int cols)
+// Bytes by which a row's start lies past a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ uint32_t row_shift(const T *row)
 {
-    if constexpr (VEC) {
-        const int c0 = base + lane * 8;
+    return (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+}
+
+// The 16-byte pieces from `from` bytes past the start of w: out[i] = w[i + from / 4], shifted by from % 4.
+template <int N>
+__device__ __forceinline__ void shift_words(const uint32_t (&in)[N + 4], uint32_t from, uint32_t (&out)[N])
+{
+    uint32_t t[N + 4];
+#pragma unroll
+    for (int i = 0; i < N + 4; ++i) t[i] = in[i];
+    if (from & 8u) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) t[i] = t[i + 2];
+    }
+    if (from & 4u) {
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) t[i] = t[i + 1];
+    }
+    const uint32_t bits = (from & 3u) * 8u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], bits);
+}
+
+template <typename T, bool AL>
+__device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base, int lane, int cols)
+{
+    const int c0 = base + lane * 8;
+    if constexpr (AL) {
         if (c0 + 8 <= cols) {
             const uint4 *p = reinterpret_cast<const uint4 *>(row + c0);
             const uint4 a = __ldg(p);
@@ -61,23 +106,47 @@ __device__ __forceinline__ void chunk_load(Raw<T> &r, const T *row, int base, in
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) raw_set(r, j, c0 + j < cols ? elem_bits(row[c0 + j]) : 0u);
+            for (int j = 0; j < 8; ++j) elem_set<T>(r.w, j, c0 + j < cols ? elem_bits(row[c0 + j]) : 0u);
         }
     } else {
+        // only bytes of the row are read: a piece that reaches over its start or end is put together
+        constexpr int P = sizeof(T) == 4 ? 3 : 2, E = 16 / sizeof(T);
+        const int first = c0 - (int)(row_shift(row) / sizeof(T));  // column of the first piece's first element
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = base + j * 32 + lane;
-            raw_set(r, j, c < cols ? elem_bits(row[c]) : 0u);
+        for (int i = 0; i < P; ++i) {
+            const int c = first + i * E;
+            if (c >= 0 && c + E <= cols) {
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + c));
+                r.w[4 * i] = a.x; r.w[4 * i + 1] = a.y; r.w[4 * i + 2] = a.z; r.w[4 * i + 3] = a.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    elem_set<T>(r.w + 4 * i, j, c + j >= 0 && c + j < cols ? elem_bits(row[c + j]) : 0u);
+            }
         }
     }
 }
 
-__device__ __forceinline__ void to_floats(const Raw<float> &r, float (&v)[8])
+// The loaded elements in place.
+template <typename T, bool AL>
+__device__ __forceinline__ Words<T> in_place(const Raw<T, AL> &r, const T *row)
+{
+    Words<T> o;
+    if constexpr (AL) {
+#pragma unroll
+        for (int i = 0; i < (int)(2 * sizeof(T)); ++i) o.w[i] = r.w[i];
+    } else {
+        shift_words<2 * sizeof(T)>(r.w, row_shift(row), o.w);
+    }
+    return o;
+}
+
+__device__ __forceinline__ void to_floats(const Words<float> &r, float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j]);
 }
-__device__ __forceinline__ void to_floats(const Raw<__nv_bfloat16> &r, float (&v)[8])
+__device__ __forceinline__ void to_floats(const Words<__nv_bfloat16> &r, float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -85,7 +154,7 @@ __device__ __forceinline__ void to_floats(const Raw<__nv_bfloat16> &r, float (&v
         v[2 * j + 1] = __uint_as_float(r.w[j] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void to_floats(const Raw<__half> &r, float (&v)[8])
+__device__ __forceinline__ void to_floats(const Words<__half> &r, float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -96,12 +165,12 @@ __device__ __forceinline__ void to_floats(const Raw<__half> &r, float (&v)[8])
     }
 }
 
-__device__ __forceinline__ void from_floats(Raw<float> &r, const float (&v)[8])
+__device__ __forceinline__ void from_floats(Words<float> &r, const float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(v[j]);
 }
-__device__ __forceinline__ void from_floats(Raw<__nv_bfloat16> &r, const float (&v)[8])
+__device__ __forceinline__ void from_floats(Words<__nv_bfloat16> &r, const float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -109,7 +178,7 @@ __device__ __forceinline__ void from_floats(Raw<__nv_bfloat16> &r, const float (
         r.w[j] = *reinterpret_cast<const uint32_t *>(&h);
     }
 }
-__device__ __forceinline__ void from_floats(Raw<__half> &r, const float (&v)[8])
+__device__ __forceinline__ void from_floats(Words<__half> &r, const float (&v)[8])
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -118,23 +187,14 @@ __device__ __forceinline__ void from_floats(Raw<__half> &r, const float (&v)[8])
     }
 }
 
-template <typename T>
-__device__ __forceinline__ T raw_get(const Raw<T> &r, int j)
+// Every lane of the warp calls it.
+template <typename T, bool AL>
+__device__ __forceinline__ void chunk_store(const Words<T> &r, T *row, int base, int lane, int cols)
 {
-    if constexpr (sizeof(T) == 4) {
-        return __uint_as_float(r.w[j]);
-    } else {
-        const unsigned short h = (unsigned short)((j & 1) ? r.w[j >> 1] >> 16 : r.w[j >> 1] & 0xffffu);
-        if constexpr (sizeof(T) == 2 && __is_same(T, __half)) return __ushort_as_half(h);
-        else return __ushort_as_bfloat16(h);
-    }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void chunk_store(const Raw<T> &r, T *row, int base, int lane, int cols)
-{
-    if constexpr (VEC) {
-        const int c0 = base + lane * 8;
+    constexpr int W = 2 * sizeof(T);
+    const int c0 = base + lane * 8;
+    const uint32_t shift = AL ? 0u : row_shift(row);
+    if (AL || shift == 0u) {
         if (c0 + 8 <= cols) {
             uint4 *p = reinterpret_cast<uint4 *>(row + c0);
             p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
@@ -142,22 +202,31 @@ __device__ __forceinline__ void chunk_store(const Raw<T> &r, T *row, int base, i
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (c0 + j < cols) row[c0 + j] = raw_get(r, j);
+                if (c0 + j < cols) row[c0 + j] = elem_get<T>(r.w, j);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = base + j * 32 + lane;
-            if (c < cols) row[c] = raw_get(r, j);
-        }
+        return;
     }
-}
-
-// Column of a lane's element j.
-template <bool VEC>
-__device__ __forceinline__ int chunk_col(int base, int lane, int j)
-{
-    return VEC ? base + lane * 8 + j : base + j * 32 + lane;
+    // a lane's pieces start `head` elements into its own and end `head` elements into the next lane's
+    const int head = (int)((16u - shift) / sizeof(T));
+    uint32_t w[W + 4], o[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = r.w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[W + i] = __shfl_down_sync(0xffffffffu, r.w[i], 1);
+    shift_words<W>(w, 16u - shift, o);
+    const bool whole = lane < 31 && c0 + head + 8 <= cols;
+    if (whole) {
+        uint4 *p = reinterpret_cast<uint4 *>(row + c0 + head);
+        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (sizeof(T) == 4) p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    // elements no piece covers: the first lane's head, and the last lanes' rest
+    const bool own_head = lane == 0 || c0 + head > cols;
+    if (own_head || !whole) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j < cols && (j < head ? own_head : !whole)) row[c0 + j] = elem_get<T>(r.w, j);
+    }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -223,90 +292,59 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
 }
 
 // Encode a lane's 8 values (0 past the last column) of a chunk; every lane of the warp calls it.
-template <bool VEC>
 __device__ __forceinline__ void ckpt_store(const float (&v)[8], const Ckpt &k, int64_t row, int base, int lane)
 {
-    uint8_t *codes = k.codes + row * k.code_pitch;
-    uint8_t *exps = k.exps + row * k.exp_pitch;
-    if constexpr (VEC) {
-        float m = fabsf(v[0]);
+    float m = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-        for (int j = 1; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t E = group_exp(__float_as_uint(m) & 0x7fffffffu);
-        uint32_t q[8];
-        if (!group_is_slow(E)) {
-            const float inv = group_inv(E);
+    for (int j = 2; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t E = group_exp(__float_as_uint(m) & 0x7fffffffu);
+    uint32_t q[8];
+    if (!group_is_slow(E)) {
+        const float inv = group_inv(E);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = group_code(v[j], inv);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = group_code_slow(v[j], E);
-        }
-        const int c0 = base + lane * 8;
-        if (c0 < k.code_pitch)
-            *reinterpret_cast<uint2 *>(codes + c0) =
-                make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
-        if ((lane & 3) == 0 && (c0 >> 5) < k.exp_pitch) exps[c0 >> 5] = (uint8_t)E;
+        for (int j = 0; j < 8; ++j) q[j] = group_code(v[j], inv);
     } else {
-        uint32_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
-            const uint32_t E = group_exp(m);
-            const uint32_t q = group_is_slow(E) ? group_code_slow(v[j], E) : group_code(v[j], group_inv(E));
-            const int c = base + j * 32 + lane;
-            if (c < k.code_pitch) codes[c] = (uint8_t)q;
-            if (lane == j) mine = E;
-        }
-        if (lane < 8 && (base >> 5) + lane < k.exp_pitch) exps[(base >> 5) + lane] = (uint8_t)mine;
+        for (int j = 0; j < 8; ++j) q[j] = group_code_slow(v[j], E);
     }
+    const int c0 = base + lane * 8;
+    if (c0 < k.code_pitch)
+        *reinterpret_cast<uint2 *>(k.codes + row * k.code_pitch + c0) =
+            make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+    if ((lane & 3) == 0 && (c0 >> 5) < k.exp_pitch) k.exps[row * k.exp_pitch + (c0 >> 5)] = (uint8_t)E;
 }
 
-// A lane's codes and exponents of a chunk, as loaded.
-template <bool VEC>
+// A lane's codes and their exponent, as loaded.
 struct RawCkpt {
-    uint32_t q[2];
-    uint32_t e[VEC ? 1 : 8];
+    uint32_t q[2], e;
 };
 
-template <bool VEC>
-__device__ __forceinline__ void ckpt_load(RawCkpt<VEC> &r, const Ckpt &k, int64_t row, int base, int lane)
+__device__ __forceinline__ void ckpt_load(RawCkpt &r, const Ckpt &k, int64_t row, int base, int lane)
 {
-    const uint8_t *codes = k.codes + row * k.code_pitch;
-    const uint8_t *exps = k.exps + row * k.exp_pitch;
-    if constexpr (VEC) {
-        const int c0 = base + lane * 8;
-        r.q[0] = r.q[1] = r.e[0] = 0;
-        if (c0 < k.code_pitch) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2 *>(codes + c0));
-            r.q[0] = a.x;
-            r.q[1] = a.y;
-            r.e[0] = __ldg(exps + (c0 >> 5));
-        }
-    } else {
-        r.q[0] = r.q[1] = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = base + j * 32 + lane;
-            const bool in = c < k.code_pitch;
-            r.q[j >> 2] |= (in ? (uint32_t)__ldg(codes + c) : 0u) << (8 * (j & 3));
-            r.e[j] = in ? __ldg(exps + (c >> 5)) : 0u;
-        }
+    const int c0 = base + lane * 8;
+    r.q[0] = r.q[1] = r.e = 0;
+    if (c0 < k.code_pitch) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2 *>(k.codes + row * k.code_pitch + c0));
+        r.q[0] = a.x;
+        r.q[1] = a.y;
+        r.e = __ldg(k.exps + row * k.exp_pitch + (c0 >> 5));
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void ckpt_floats(const RawCkpt<VEC> &r, float (&v)[8])
+// Code j (0 .. 7) as a binary32 integer.
+__device__ __forceinline__ float code_float(const RawCkpt &r, int j)
 {
-    const uint32_t a = r.q[0] ^ 0x80808080u, b = r.q[1] ^ 0x80808080u;
+    // 2^23 + (q + 128), less 2^23 + 128
+    return __fsub_rn(__uint_as_float(__byte_perm(r.q[j >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 | (j & 3))), 8388736.0f);
+}
+
+__device__ __forceinline__ void ckpt_floats(const RawCkpt &r, float (&v)[8])
+{
+    const float s = group_scale(r.e);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        // 2^23 + (q + 128), then the exact integer q, then its exact product with the scale
-        const float f = __uint_as_float(__byte_perm(j < 4 ? a : b, 0x4B000000u, 0x7440 | (j & 3)));
-        v[j] = __fmul_rn(__fsub_rn(f, 8388736.0f), group_scale(r.e[VEC ? 0 : j]));
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(code_float(r, j), s);
 }
 
 // Largest finite binary16: decoded values saturate there (a group's largest value may round up to 65536).

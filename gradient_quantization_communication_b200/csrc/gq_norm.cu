@@ -47,27 +47,43 @@ __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
 // A lane's 8 values of gamma or beta (fill where there is none).  They are read again for every row: from
 // L1, which costs less than the registers that would hold them.
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ void param_load(float (&v)[8], const void *p, int f32, float fill, int base, int lane, int cols)
 {
-    if (p && f32 && VEC && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        Raw<float> r;
-        chunk_load<float, true>(r, static_cast<const float *>(p), base, lane, cols);
-        to_floats(r, v);
-        return;
-    }
-    if (p && !f32 && VEC && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        Raw<T> r;
-        chunk_load<T, true>(r, static_cast<const T *>(p), base, lane, cols);
-        to_floats(r, v);
+    if (p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        if (f32) {
+            Raw<float, true> r;
+            chunk_load<float, true>(r, static_cast<const float *>(p), base, lane, cols);
+            to_floats(in_place<float, true>(r, nullptr), v);
+        } else {
+            Raw<T, true> r;
+            chunk_load<T, true>(r, static_cast<const T *>(p), base, lane, cols);
+            to_floats(in_place<T, true>(r, nullptr), v);
+        }
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int c = chunk_col<VEC>(base, lane, j);
+        const int c = base + lane * 8 + j;
         v[j] = fill;
         if (p && c < cols) v[j] = f32 ? __ldg(static_cast<const float *>(p) + c) : to_f(static_cast<const T *>(p)[c]);
     }
+}
+
+// A lane's 8 values of a row.
+template <typename T, bool AL>
+__device__ __forceinline__ void row_floats(float (&v)[8], const T *row, int base, int lane, int cols)
+{
+    Raw<T, AL> r;
+    chunk_load<T, AL>(r, row, base, lane, cols);
+    to_floats(in_place<T, AL>(r, row), v);
+}
+template <typename T, bool AL>
+__device__ __forceinline__ void row_store(const float (&v)[8], T *row, int base, int lane, int cols)
+{
+    Words<T> r;
+    from_floats(r, v);
+    chunk_store<T, AL>(r, row, base, lane, cols);
 }
 
 // Sum over the G warps that share a row; `buf` holds one float per warp.  One barrier: the caller
@@ -84,104 +100,118 @@ __device__ __forceinline__ float row_sum(float v, float *buf, int G, int warp, i
 }
 
 // ---------------------------------------------------------------------------------------------
-// Rows kept in registers: up to kRegCols columns.  G warps take a row, NC chunks of 256 columns each; a block
-// holds `slots` such groups and walks the rows, and loads its next row before it works on the present one.
+// Rows kept in registers.  G warps take a row, NC chunks of 256 columns each (chunk c of warp w is w + c G); a
+// block holds `slots` such groups and walks the rows, and loads its next row before it works on the present one.
 // ---------------------------------------------------------------------------------------------
-constexpr int kRegCols = 8192;
+constexpr int kForwardCols = 16384, kBackwardCols = 8192;
 
 struct Shape {
     int G, nc, slots;
 };
-// Two chunks a warp (one where a row has no more): 16 values a lane leave room for the next row's in 128
-// registers, and the fewest warps share a row's sums.  Blocks of about 8 warps.
-inline Shape shape_of(int64_t cols)
+inline Shape shape_of(int64_t cols, int most)
 {
     const int n = (int)((cols + kChunk - 1) / kChunk);
     Shape s;
-    s.nc = n > 1 ? 2 : 1;
+    s.nc = n >= most ? most : n >= 2 ? 2 : 1;
     s.G = (n + s.nc - 1) / s.nc;
-    s.slots = s.G >= 8 ? 1 : 8 / s.G;
+    s.slots = s.G >= 8 ? 1 : 8 / s.G;  // blocks of about 8 warps
     return s;
 }
-
-// Sums of N values over the G warps of a slot.  `buf` must not be written again before another barrier of the
-// slot has passed: callers alternate between two.
-template <int N>
-__device__ __forceinline__ void slot_sum(float (&v)[N], float (*buf)[N], int G, int slot, int wslot, int lane)
+// Forward: four chunks a warp where the rows are enough to fill the device, since the reductions and the
+// barrier are per warp; for fewer rows one, which has the shortest way from load to store.
+inline Shape forward_shape(int64_t rows, int64_t cols)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (G == 1) return;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) buf[slot * G + wslot][i] = v[i];
-    }
+    const int n = (int)((cols + kChunk - 1) / kChunk);
+    return shape_of(cols, rows * n <= 148 * 16 && n <= 16 ? 1 : 4);
+}
+// Backward: two, whose sums and next row still fit 128 registers.
+inline Shape backward_shape(int64_t cols) { return shape_of(cols, 2); }
+
+// Barrier of a slot's G warps.
+__device__ __forceinline__ void slot_sync(int slot, int G)
+{
     asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += buf[slot * G + g][i];
-    }
 }
 
-template <typename T, bool VEC, int NC, bool KEEP>
+template <typename T, bool AL, int NC, bool KEEP>
 __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params p)
 {
-    __shared__ float buf[2][16][1];
+    __shared__ float4 buf[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
     const int slot = warp / G, wslot = warp - slot * G;
     const float inv_c = 1.0f / (float)p.cols;
+    float mine = 0.0f;  // columns of this warp
+#pragma unroll
+    for (int c = 0; c < NC; ++c) mine += (float)min(max(p.cols - (wslot + c * G) * kChunk, 0), kChunk);
+    const float inv_mine = 1.0f / mine;
     const int64_t step = (int64_t)gridDim.x * p.slots;
     int64_t row = (int64_t)blockIdx.x * p.slots + slot;
-    Raw<T> next[NC];
-    if (row < p.rows) {
+    Raw<T, AL> next[NC];
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            chunk_load<T, VEC>(next[c], static_cast<const T *>(p.x) + row * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
-    }
-    for (; row < p.rows; row += step) {
+            chunk_load<T, AL>(next[c], static_cast<const T *>(p.x) + r * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
+    };
+    if (row < p.rows) fetch(row);
+    int turn = 0;
+    for (; row < p.rows; row += step, turn ^= 1) {
         float v[NC][8];
-        float s[1] = {0.0f};
+        float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            to_floats(next[c], v[c]);
+            to_floats(in_place<T, AL>(next[c], static_cast<const T *>(p.x) + row * p.sx), v[c]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += v[c][j];
+            for (int j = 0; j < 8; ++j) s += v[c][j];
         }
-        if (row + step < p.rows) {
+        if (row + step < p.rows) fetch(row + step);
+        // the warp's own mean and squares around it, then all warps' put together with one barrier:
+        // sum (x - mean)^2 = sum over warps of (their squares + their columns (their mean - mean)^2)
+        s = warp_sum(s);
+        const float wmean = s * inv_mine;
+        float ss = 0.0f;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                chunk_load<T, VEC>(next[c], static_cast<const T *>(p.x) + (row + step) * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
-        }
-        if constexpr (KEEP) {
+        for (int c = 0; c < NC; ++c) {
+            const int c0 = (wslot + c * G) * kChunk;
+            if (c0 + kChunk <= p.cols) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) ckpt_store<VEC>(v[c], p.k, row, (wslot + c * G) * kChunk, lane);
-        }
-        slot_sum<1>(s, buf[0], G, slot, wslot, lane);
-        const float mean = s[0] * inv_c;
-        float ss[1] = {0.0f};
+                for (int j = 0; j < 8; ++j) {
+                    const float d = v[c][j] - wmean;
+                    ss = __fmaf_rn(d, d, ss);
+                }
+            } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = chunk_col<VEC>((wslot + c * G) * kChunk, lane, j) < p.cols ? v[c][j] - mean : 0.0f;
-                v[c][j] = d;
-                ss[0] = __fmaf_rn(d, d, ss[0]);
+                for (int j = 0; j < 8; ++j) {
+                    const float d = c0 + lane * 8 + j < p.cols ? v[c][j] - wmean : 0.0f;
+                    ss = __fmaf_rn(d, d, ss);
+                }
             }
-        slot_sum<1>(ss, buf[1], G, slot, wslot, lane);
-        const float rstd = 1.0f / sqrtf(ss[0] * inv_c + p.eps);
+        }
+        ss = warp_sum(ss);
+        float mean = wmean;
+        if (G > 1) {
+            if (lane == 0) buf[turn][warp] = make_float4(mine, s, wmean, ss);
+            slot_sync(slot, G);
+            const float4 *b = buf[turn] + slot * G;
+            s = 0.0f;
+            for (int g = 0; g < G; ++g) s += b[g].y;
+            mean = s * inv_c;
+            ss = 0.0f;
+            for (int g = 0; g < G; ++g) {
+                const float d = b[g].z - mean;
+                ss += __fmaf_rn(b[g].x * d, d, b[g].w);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(ss * inv_c + p.eps);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int base = (wslot + c * G) * kChunk;
+            if constexpr (KEEP) ckpt_store(v[c], p.k, row, base, lane);
             float g[8], b[8];
-            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
-            param_load<T, VEC>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
+            param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            param_load<T>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn(v[c][j] * rstd, g[j], b[j]);
-            Raw<T> r;
-            from_floats(r, v[c]);
-            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
+            for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn((v[c][j] - mean) * rstd, g[j], b[j]);
+            row_store<T, AL>(v[c], static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
         }
         if (wslot == 0 && lane == 0) {
             p.mean[row] = mean;
@@ -191,18 +221,18 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 }
 
 // dx, and the block's partial sums of dgamma and dbeta (part_g, part_b: one row a block).
-template <typename T, bool VEC, int NC, bool FROM_CKPT>
+template <typename T, bool AL, int NC, bool FROM_CKPT>
 __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params p)
 {
     extern __shared__ float fold[];  // slots > 1: the block's sums, cols of dgamma and cols of dbeta
-    __shared__ float buf[2][16][2];
+    __shared__ float2 buf[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
     const int slot = warp / G, wslot = warp - slot * G;
     const float inv_c = 1.0f / (float)p.cols;
     const int64_t step = (int64_t)gridDim.x * p.slots;
     int64_t row = (int64_t)blockIdx.x * p.slots + slot;
-    Raw<T> ndy[NC], nx[FROM_CKPT ? 1 : NC];
-    RawCkpt<VEC> nk[FROM_CKPT ? NC : 1];
+    Raw<T, AL> ndy[NC], nx[FROM_CKPT ? 1 : NC];
+    RawCkpt nk[FROM_CKPT ? NC : 1];
     float nmean = 0.0f, nrstd = 0.0f;
     auto fetch = [&](int64_t r) {
         nmean = __ldg(p.mean + r);
@@ -210,9 +240,9 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int base = (wslot + c * G) * kChunk;
-            chunk_load<T, VEC>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
-            if constexpr (FROM_CKPT) ckpt_load<VEC>(nk[c], p.k, r, base, lane);
-            else chunk_load<T, VEC>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
+            chunk_load<T, AL>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
+            if constexpr (FROM_CKPT) ckpt_load(nk[c], p.k, r, base, lane);
+            else chunk_load<T, AL>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
         }
     };
     float sg[NC][8], sb[NC][8];
@@ -227,39 +257,50 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
         const float mean = nmean, rstd = nrstd;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            to_floats(ndy[c], d[c]);
-            if constexpr (FROM_CKPT) ckpt_floats<VEC>(nk[c], x[c]);
-            else to_floats(nx[c], x[c]);
-        }
-        if (row + step < p.rows) fetch(row + step);
-        float s[2] = {0.0f, 0.0f};
+            to_floats(in_place<T, AL>(ndy[c], static_cast<const T *>(p.dy) + row * p.sdy), d[c]);
+            if constexpr (FROM_CKPT) {
+                const float sc = group_scale(nk[c].e);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int base = (wslot + c * G) * kChunk;
-            float g[8];
-            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+                for (int j = 0; j < 8; ++j) x[c][j] = __fmaf_rn(code_float(nk[c], j), sc, -mean) * rstd;
+            } else {
+                to_floats(in_place<T, AL>(nx[c], static_cast<const T *>(p.x) + row * p.sx), x[c]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // past the last column dy reads as 0, and xh is made 0 so that no infinity meets it
-                const float xh = chunk_col<VEC>(base, lane, j) < p.cols ? (x[c][j] - mean) * rstd : 0.0f;
-                sg[c][j] = __fmaf_rn(d[c][j], xh, sg[c][j]);
-                sb[c][j] += d[c][j];
-                const float gd = chunk_col<VEC>(base, lane, j) < p.cols ? g[j] * d[c][j] : 0.0f;
-                x[c][j] = xh;
-                d[c][j] = gd;
-                s[0] += gd;
-                s[1] = __fmaf_rn(gd, xh, s[1]);
+                for (int j = 0; j < 8; ++j) x[c][j] = (x[c][j] - mean) * rstd;
             }
         }
-        slot_sum<2>(s, buf[turn], G, slot, wslot, lane);
-        const float c0 = s[0] * inv_c, c1 = s[1] * inv_c;
+        if (row + step < p.rows) fetch(row + step);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float g[8];
+            param_load<T>(g, p.gamma, p.params_f32, 1.0f, (wslot + c * G) * kChunk, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // past the last column d is 0
+                sg[c][j] = __fmaf_rn(d[c][j], x[c][j], sg[c][j]);
+                sb[c][j] += d[c][j];
+                d[c][j] *= g[j];
+                s0 += d[c][j];
+                s1 = __fmaf_rn(d[c][j], x[c][j], s1);
+            }
+        }
+        s0 = warp_sum(s0);
+        s1 = warp_sum(s1);
+        if (G > 1) {
+            if (lane == 0) buf[turn][warp] = make_float2(s0, s1);
+            slot_sync(slot, G);
+            s0 = s1 = 0.0f;
+            for (int g = 0; g < G; ++g) {
+                const float2 b = buf[turn][slot * G + g];
+                s0 += b.x;
+                s1 += b.y;
+            }
+        }
+        const float a0 = -(s0 * inv_c) * rstd, a1 = -(s1 * inv_c) * rstd;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[c][j] = rstd * __fmaf_rn(-x[c][j], c1, d[c][j] - c0);
-            Raw<T> r;
-            from_floats(r, d[c]);
-            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, (wslot + c * G) * kChunk, lane, p.cols);
+            for (int j = 0; j < 8; ++j) d[c][j] = __fmaf_rn(x[c][j], a1, __fmaf_rn(d[c][j], rstd, a0));
+            row_store<T, AL>(d[c], static_cast<T *>(p.y) + row * p.sy, (wslot + c * G) * kChunk, lane, p.cols);
         }
     }
     if (!p.part_b) return;
@@ -270,7 +311,7 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int col = chunk_col<VEC>((wslot + c * G) * kChunk, lane, j);
+                    const int col = (wslot + c * G) * kChunk + lane * 8 + j;
                     if (col >= p.cols) continue;
                     float a = sg[c][j], b = sb[c][j];
                     if (t > 0) {
@@ -294,7 +335,7 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
 // Wider rows: one block per row at a time, any number of columns; the row is read three times (twice from
 // cache).
 // ---------------------------------------------------------------------------------------------
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Params p)
 {
     __shared__ float buf[2][16];
@@ -305,39 +346,32 @@ __global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Par
         T *y = static_cast<T *>(p.y) + row * p.sy;
         float s = 0.0f;
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
-            Raw<T> r;
             float v[8];
-            chunk_load<T, VEC>(r, x, base, lane, p.cols);
-            to_floats(r, v);
+            row_floats<T, AL>(v, x, base, lane, p.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[j];
         }
         const float mean = row_sum(s, buf[0], G, warp, lane) * inv_c;
         float ss = 0.0f;
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
-            Raw<T> r;
             float v[8];
-            chunk_load<T, VEC>(r, x, base, lane, p.cols);
-            to_floats(r, v);
+            row_floats<T, AL>(v, x, base, lane, p.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float d = chunk_col<VEC>(base, lane, j) < p.cols ? v[j] - mean : 0.0f;
+                const float d = base + lane * 8 + j < p.cols ? v[j] - mean : 0.0f;
                 ss = __fmaf_rn(d, d, ss);
             }
         }
         const float rstd = 1.0f / sqrtf(row_sum(ss, buf[1], G, warp, lane) * inv_c + p.eps);
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
-            Raw<T> r;
             float v[8], g[8], b[8];
-            chunk_load<T, VEC>(r, x, base, lane, p.cols);
-            to_floats(r, v);
-            if (p.k.codes) ckpt_store<VEC>(v, p.k, row, base, lane);
-            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
-            param_load<T, VEC>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
+            row_floats<T, AL>(v, x, base, lane, p.cols);
+            if (p.k.codes) ckpt_store(v, p.k, row, base, lane);
+            param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            param_load<T>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn((v[j] - mean) * rstd, g[j], b[j]);
-            from_floats(r, v);
-            chunk_store<T, VEC>(r, y, base, lane, p.cols);
+            row_store<T, AL>(v, y, base, lane, p.cols);
         }
         if (threadIdx.x == 0) {
             p.mean[row] = mean;
@@ -347,22 +381,20 @@ __global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Par
 }
 
 // A lane's 8 values of the input, from the input or its checkpoint.
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __device__ __forceinline__ void input_load(float (&v)[8], const Params &p, int64_t row, int base, int lane)
 {
     if (p.x) {
-        Raw<T> r;
-        chunk_load<T, VEC>(r, static_cast<const T *>(p.x) + row * p.sx, base, lane, p.cols);
-        to_floats(r, v);
+        row_floats<T, AL>(v, static_cast<const T *>(p.x) + row * p.sx, base, lane, p.cols);
     } else {
-        RawCkpt<VEC> r;
-        ckpt_load<VEC>(r, p.k, row, base, lane);
-        ckpt_floats<VEC>(r, v);
+        RawCkpt r;
+        ckpt_load(r, p.k, row, base, lane);
+        ckpt_floats(r, v);
     }
 }
 
 // dx for any number of columns, one block per row.
-template <typename T, bool VEC>
+template <typename T, bool AL>
 __global__ void __launch_bounds__(512) k_backward_rows_any(const __grid_constant__ Params p)
 {
     __shared__ float buf[2][16];
@@ -373,15 +405,13 @@ __global__ void __launch_bounds__(512) k_backward_rows_any(const __grid_constant
         const float mean = p.mean[row], rstd = p.rstd[row];
         float s0 = 0.0f, s1 = 0.0f;
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
-            Raw<T> r;
             float x[8], d[8], g[8];
-            chunk_load<T, VEC>(r, dy, base, lane, p.cols);
-            to_floats(r, d);
-            input_load<T, VEC>(x, p, row, base, lane);
-            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            row_floats<T, AL>(d, dy, base, lane, p.cols);
+            input_load<T, AL>(x, p, row, base, lane);
+            param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (chunk_col<VEC>(base, lane, j) >= p.cols) continue;
+                if (base + lane * 8 + j >= p.cols) continue;
                 const float gd = g[j] * d[j];
                 s0 += gd;
                 s1 = __fmaf_rn(gd, (x[j] - mean) * rstd, s1);
@@ -390,23 +420,20 @@ __global__ void __launch_bounds__(512) k_backward_rows_any(const __grid_constant
         const float c0 = row_sum(s0, buf[0], G, warp, lane) * inv_c;
         const float c1 = row_sum(s1, buf[1], G, warp, lane) * inv_c;
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
-            Raw<T> r;
             float x[8], d[8], g[8];
-            chunk_load<T, VEC>(r, dy, base, lane, p.cols);
-            to_floats(r, d);
-            input_load<T, VEC>(x, p, row, base, lane);
-            param_load<T, VEC>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
+            row_floats<T, AL>(d, dy, base, lane, p.cols);
+            input_load<T, AL>(x, p, row, base, lane);
+            param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 d[j] = rstd * __fmaf_rn(-(x[j] - mean) * rstd, c1, __fmaf_rn(g[j], d[j], -c0));
-            from_floats(r, d);
-            chunk_store<T, VEC>(r, static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
+            row_store<T, AL>(d, static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
         }
     }
 }
 
 // Partial sums over the rows: warp (chunk c, part q) walks rows q, q + parts, ...
-template <typename T, bool VEC, bool NORM>
+template <typename T, bool AL, bool NORM>
 __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -416,13 +443,11 @@ __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sg[j] = sb[j] = 0.0f;
     for (int64_t row = blockIdx.y; row < p.rows; row += p.parts) {
-        Raw<T> r;
         float d[8];
-        chunk_load<T, VEC>(r, static_cast<const T *>(p.dy) + row * p.sdy, base, lane, p.cols);
-        to_floats(r, d);
+        row_floats<T, AL>(d, static_cast<const T *>(p.dy) + row * p.sdy, base, lane, p.cols);
         if constexpr (NORM) {
             float x[8];
-            input_load<T, VEC>(x, p, row, base, lane);
+            input_load<T, AL>(x, p, row, base, lane);
             const float mean = p.mean[row], rstd = p.rstd[row];
 #pragma unroll
             for (int j = 0; j < 8; ++j) sg[j] = __fmaf_rn(d[j], (x[j] - mean) * rstd, sg[j]);
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int c = chunk_col<VEC>(base, lane, j);
+        const int c = base + lane * 8 + j;
         if (c >= p.cols) continue;
         const int64_t o = (int64_t)blockIdx.y * p.cols + c;
         if (NORM) p.part_g[o] = sg[j];
@@ -493,9 +518,9 @@ Params params(const NormArgs &a)
 bool rows_aligned(int64_t rows, const Mat &m, int per16) { return !m.p || rows == 1 || m.stride % per16 == 0; }
 
 template <typename T, int NC>
-cudaError_t forward_reg(const Params &p, bool vec, cudaStream_t s)
+cudaError_t forward_reg(const Params &p, bool al, cudaStream_t s)
 {
-    auto kern = vec ? (p.k.codes ? k_forward<T, true, NC, true> : k_forward<T, true, NC, false>)
+    auto kern = al ? (p.k.codes ? k_forward<T, true, NC, true> : k_forward<T, true, NC, false>)
                     : (p.k.codes ? k_forward<T, false, NC, true> : k_forward<T, false, NC, false>);
     const int threads = p.G * p.slots * 32;
     int per_sm = 0, sms = 0;
@@ -510,16 +535,16 @@ template <typename T>
 cudaError_t forward(const NormArgs &a, cudaStream_t s)
 {
     const int per16 = 16 / (int)sizeof(T);
-    const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16);
+    const bool al = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16);
     Params p = params(a);
-    if (a.cols <= kRegCols) {
-        const Shape sh = shape_of(a.cols);
+    if (a.cols <= kForwardCols) {
+        const Shape sh = forward_shape(a.rows, a.cols);
         p.G = sh.G;
         p.slots = sh.slots;
-        return sh.nc == 1 ? forward_reg<T, 1>(p, vec, s) : forward_reg<T, 2>(p, vec, s);
+        return sh.nc == 1 ? forward_reg<T, 1>(p, al, s) : sh.nc == 2 ? forward_reg<T, 2>(p, al, s) : forward_reg<T, 4>(p, al, s);
     }
     const int warps = 16;
-    auto kern = vec ? k_forward_any<T, true> : k_forward_any<T, false>;
+    auto kern = al ? k_forward_any<T, true> : k_forward_any<T, false>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
     if (e != cudaSuccess) return e;
@@ -529,9 +554,9 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s)
 }
 
 template <typename T, int NC>
-cudaError_t backward_reg(const Params &p, bool vec, cudaStream_t s)
+cudaError_t backward_reg(const Params &p, bool al, cudaStream_t s)
 {
-    auto kern = vec ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
+    auto kern = al ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
                     : (p.x ? k_backward<T, false, NC, false> : k_backward<T, false, NC, true>);
     const size_t smem = p.slots > 1 ? (size_t)p.cols * 2 * sizeof(float) : 0;
     kern<<<(unsigned)p.parts, p.G * p.slots * 32, smem, s>>>(p);
@@ -542,18 +567,18 @@ template <typename T>
 cudaError_t backward(const NormArgs &a, cudaStream_t s)
 {
     const int per16 = 16 / (int)sizeof(T);
-    const bool vec = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16) && rows_aligned(a.rows, a.dy, per16);
+    const bool al = rows_aligned(a.rows, a.x, per16) && rows_aligned(a.rows, a.y, per16) && rows_aligned(a.rows, a.dy, per16);
     Params p = params(a);
-    if (a.rows > 0 && a.cols <= kRegCols) {
-        const Shape sh = shape_of(a.cols);
+    if (a.rows > 0 && a.cols <= kBackwardCols) {
+        const Shape sh = backward_shape(a.cols);
         p.G = sh.G;
         p.slots = sh.slots;
-        const cudaError_t e = sh.nc == 1 ? backward_reg<T, 1>(p, vec, s) : backward_reg<T, 2>(p, vec, s);
+        const cudaError_t e = sh.nc == 1 ? backward_reg<T, 1>(p, al, s) : backward_reg<T, 2>(p, al, s);
         if (e != cudaSuccess) return e;
     } else if (a.rows > 0) {
         const int64_t chunks = (a.cols + kChunk - 1) / kChunk;
         const int warps = 16;
-        auto kern = vec ? k_backward_rows_any<T, true> : k_backward_rows_any<T, false>;
+        auto kern = al ? k_backward_rows_any<T, true> : k_backward_rows_any<T, false>;
         int per_sm = 0, sms = 0;
         cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), warps * 32, 0, &per_sm, &sms);
         if (e != cudaSuccess) return e;
@@ -562,7 +587,7 @@ cudaError_t backward(const NormArgs &a, cudaStream_t s)
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         if (a.dgamma || a.dbeta) {
-            auto ck = vec ? k_cols<T, true, true> : k_cols<T, false, true>;
+            auto ck = al ? k_cols<T, true, true> : k_cols<T, false, true>;
             ck<<<dim3((unsigned)((chunks + 3) / 4), (unsigned)p.parts), 128, 0, s>>>(p);
             e = cudaGetLastError();
             if (e != cudaSuccess) return e;
@@ -593,10 +618,10 @@ cudaError_t colsum(int64_t rows, int64_t cols, Mat dy, float *parts, cudaStream_
 int64_t norm_parts(int64_t rows, int64_t cols)
 {
     if (rows <= 0) return 0;
-    if (cols > kRegCols) return rows < 296 ? rows : 296;
+    if (cols > kBackwardCols) return rows < 296 ? rows : 296;
     // blocks of the backward pass: two an SM, and at least two rows to each of a block's slots, so that the
     // partial sums stay fewer bytes than the rows
-    const int64_t rows_a_block = 2 * shape_of(cols).slots;
+    const int64_t rows_a_block = 2 * backward_shape(cols).slots;
     const int64_t n = (rows + rows_a_block - 1) / rows_a_block;
     return n < 296 ? n : 296;
 }
