@@ -1,7 +1,7 @@
 // gq_act.cu -- pack and unpack of the 8-bit activation checkpoint, and activation functions whose
 // forward pass writes the checkpoint of its input and whose backward pass reads it.
 //
-// All are one pass over their tensors: a warp takes chunks of 256 columns of a row, two at a time.  Bounded by
+// All are one pass over their tensors: a warp takes 512 columns of a row at a time.  Bounded by
 // the bytes; the arithmetic leaves some 27 instruction slots an element at full bandwidth in 16-bit types.
 #include "gq_act.cuh"
 #include "gq_act.h"
@@ -11,6 +11,7 @@ namespace gq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kItem = 2 * kChunk;  // columns of a row that a warp takes at a time
 
 // f(x) and f'(x), in binary32.
 //   GELU       x Phi(x);  Phi(x) + x phi(x).  Phi = erfc(-x / sqrt 2) / 2, which keeps the negative
@@ -19,10 +20,23 @@ constexpr int kThreads = 256;
 //   SiLU       x s(x);  s (1 + x (1 - s)).
 // In 16-bit types, whose own step hides it, the exponential is the hardware's (2^-21 or so), and Phi's tail
 // comes from a polynomial; binary32 calls expf and erfcf.
+// exp(t) for t <= 0.
 template <bool FAST>
 __device__ __forceinline__ float exp_neg(float t)
 {
-    return FAST ? __expf(t) : expf(t);
+    if constexpr (!FAST) return expf(t);
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));  // keeps subnormal results: x times them need not be
+    return r;
+}
+// 1 / x for 1 <= x.
+template <bool FAST>
+__device__ __forceinline__ float inverse(float x)
+{
+    if constexpr (!FAST) return __fdividef(1.0f, x);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // s(t) = 1 / (1 + exp(-t)) and 1 - s, through exp(-|t|) <= 1: neither overflows nor cancels.
@@ -30,7 +44,7 @@ template <bool FAST>
 __device__ __forceinline__ void logistic(float t, float &s, float &one_minus)
 {
     const float e = exp_neg<FAST>(-fabsf(t));
-    const float a = __fdividef(1.0f, 1.0f + e), b = e * a;
+    const float a = inverse<FAST>(1.0f + e), b = e * a;
     s = t >= 0.0f ? a : b;
     one_minus = t >= 0.0f ? b : a;
 }
@@ -45,7 +59,7 @@ __device__ __forceinline__ void normal(float x, float &Phi, float &e)
         // [0, inf) to (0, 1].  P has degree 7, fitted on z <= 14.5 (beyond, the tail is below binary32's
         // range) by Lawson's weighted least squares to the smallest largest relative error, 1.6e-7; 5e-7 in
         // binary32 arithmetic.
-        const float t = __fdividef(1.0f, __fmaf_rn(0.31f, fabsf(x), 1.0f));
+        const float t = inverse<true>(__fmaf_rn(0.31f, fabsf(x), 1.0f));
         float h = 0.035870399326086044f;
         h = __fmaf_rn(h, t, -0.1417304277420044f);
         h = __fmaf_rn(h, t, 0.15529736876487732f);
@@ -116,10 +130,10 @@ struct Fn<GQ_FN_SILU, FAST> {
 };
 
 struct Params {
-    int64_t rows, chunks;  // chunks: rows * chunks per row
+    int64_t items;         // rows * items per row
     int cols, per_row;
-    int64_t drow;          // warps of the grid = drow rows of chunks and dchunk chunks
-    int dchunk;
+    int64_t drow;          // warps of the grid = drow rows of items and dplace items
+    int dplace;
     const void *a;
     void *b;
     int64_t sa, sb;
@@ -129,43 +143,35 @@ struct Params {
 template <typename T, int OP, int KIND, bool AL>
 __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params p)
 {
-    constexpr int U = 2;
     constexpr bool READS = OP != kUnpack, WRITES = OP != kPack, DECODES = OP == kUnpack || OP == kBackward;
     using F = Fn<KIND, sizeof(T) == 2>;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
     int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    // (row, chunk of the row) of chunk id; a step of `warps` chunks is (drow, dchunk), without divisions
+    // (row, place in the row) of id; a step of `warps` is (drow, dplace), without divisions
     int64_t row = id / p.per_row;
-    int chunk = (int)(id - row * p.per_row);
-    for (; id < p.chunks; id += U * warps) {
-        Raw<T, AL> raw[U];
-        RawCkpt rk[U];
-        int64_t rows[U];
-        int base[U];
+    int place = (int)(id - row * p.per_row);
+    for (; id < p.items; id += warps) {
+        const int base = place * kItem;
+        const T *a = static_cast<const T *>(p.a) + row * p.sa;
+        Raw<T, AL> raw[kItem / kChunk];
+        RawCkpt rk[kItem / kChunk];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rows[u] = row;
-            base[u] = chunk * kChunk;
-            row += p.drow;
-            chunk += p.dchunk;
-            if (chunk >= p.per_row) {
-                chunk -= p.per_row;
-                ++row;
-            }
-            if (id + u * warps < p.chunks) {
-                if constexpr (READS)
-                    chunk_load<T, AL>(raw[u], static_cast<const T *>(p.a) + rows[u] * p.sa, base[u], lane, p.cols);
-                if constexpr (DECODES) ckpt_load(rk[u], p.k, rows[u], base[u], lane);
-            }
+        for (int u = 0; u < kItem / kChunk; ++u) {
+            if constexpr (READS) chunk_load<T, AL>(raw[u], a, base + u * kChunk, lane, p.cols);
+            if constexpr (DECODES) ckpt_load(rk[u], p.k, row, base + u * kChunk, lane);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (id + u * warps >= p.chunks) break;
+        for (int u = 0; u < kItem / kChunk; ++u) {
+            const int at = base + u * kChunk;
+            if (u > 0 && at >= p.cols) break;
             float in[8], v[8], o[8];
-            if constexpr (READS) to_floats(in_place<T, AL>(raw[u], static_cast<const T *>(p.a) + rows[u] * p.sa), in);
+            if constexpr (READS) {
+                const Words<T> w = in_place<T, AL>(raw[u], a);
+                to_floats(w, in);
+                if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store<T>(w, in, p.k, row, at, lane);
+            }
             if constexpr (DECODES) ckpt_floats(rk[u], v);
-            if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store(in, p.k, rows[u], base[u], lane);
             if constexpr (OP == kUnpack) saturate<T>(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -176,8 +182,14 @@ __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params
             if constexpr (WRITES) {
                 Words<T> out;
                 from_floats(out, o);
-                chunk_store<T, AL>(out, static_cast<T *>(p.b) + rows[u] * p.sb, base[u], lane, p.cols);
+                chunk_store<T, AL>(out, static_cast<T *>(p.b) + row * p.sb, at, lane, p.cols);
             }
+        }
+        row += p.drow;
+        place += p.dplace;
+        if (place >= p.per_row) {
+            place -= p.per_row;
+            ++row;
         }
     }
 }
@@ -187,10 +199,9 @@ cudaError_t launch(const ActArgs &a, cudaStream_t stream)
 {
     const CkptLayout l = ckpt_layout(a.rows, a.cols);
     Params p;
-    p.rows = a.rows;
     p.cols = (int)a.cols;
-    p.per_row = (int)((a.cols + kChunk - 1) / kChunk);
-    p.chunks = a.rows * p.per_row;
+    p.per_row = (int)((a.cols + kItem - 1) / kItem);
+    p.items = a.rows * p.per_row;
     p.a = a.a.p;
     p.sa = a.a.stride;
     p.b = const_cast<void *>(a.b.p);
@@ -204,11 +215,11 @@ cudaError_t launch(const ActArgs &a, cudaStream_t stream)
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);
     if (e != cudaSuccess) return e;
-    const int64_t need = (p.chunks + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t need = (p.items + kThreads / 32 - 1) / (kThreads / 32);
     const int64_t grid = need < (int64_t)per_sm * sms ? need : (int64_t)per_sm * sms;
     const int64_t warps = grid * (kThreads / 32);
     p.drow = warps / p.per_row;
-    p.dchunk = (int)(warps - p.drow * p.per_row);
+    p.dplace = (int)(warps - p.drow * p.per_row);
     kern<<<(unsigned)grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }

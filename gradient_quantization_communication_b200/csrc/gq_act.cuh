@@ -246,24 +246,15 @@ __device__ __forceinline__ uint32_t group_exp(uint32_t abs_bits)
     return abs_bits >= 0x7f800000u ? 255u : e;
 }
 
-// The code of v as a byte in a word's low 8 bits (other bits undefined).  fma(v, 2^-e, 1.5 * 2^23)
-// leaves rint(v * 2^-e), ties to even, in two's complement in the low mantissa bits; v * 2^-e is exact.
-// Outside 6 <= E <= 253 the scale leaves binary32's range or the code may pass 127: see group_code_slow.
+// The code of v as a byte in a word's low 8 bits (other bits undefined): fma(v, 2^-e, 1.5 * 2^23) leaves
+// rint(v * 2^-e), ties to even, in two's complement in the low mantissa bits; v * 2^-e is exact.
 __device__ __forceinline__ uint32_t group_code(float v, float inv)
 {
     return __float_as_uint(__fmaf_rn(v, inv, 12582912.0f));
 }
-__device__ __forceinline__ bool group_is_slow(uint32_t E) { return E - 6u > 247u; }
-__device__ __forceinline__ float group_inv(uint32_t E) { return __uint_as_float((260u - E) << 23); }
-static __device__ __noinline__ uint32_t group_code_slow(float v, uint32_t E)
-{
-    if (E == 255u) return 0u;
-    float t;
-    if (E >= 6u) t = __fmul_rn(v, __uint_as_float((260u - E) << 23));
-    else t = __fmul_rn(__fmul_rn(v, __uint_as_float(254u << 23)), __uint_as_float((133u - E) << 23));
-    t = fminf(fmaxf(t, -127.0f), 127.0f);
-    return __float_as_uint(__fadd_rn(t, 12582912.0f));
-}
+
+// The codes of a lane's 8 values of a group under E, as two words.
+__device__ __forceinline__ uint2 group_codes(const float (&v)[8], uint32_t E);
 
 // 2^(E - 133), NaN for E = 255.
 __device__ __forceinline__ float group_scale(uint32_t E)
@@ -291,28 +282,61 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Encode a lane's 8 values (0 past the last column) of a chunk; every lane of the warp calls it.
-__device__ __forceinline__ void ckpt_store(const float (&v)[8], const Ckpt &k, int64_t row, int base, int lane)
+__device__ __forceinline__ uint2 group_codes(const float (&v)[8], uint32_t E)
 {
-    float m = max_nan(fabsf(v[0]), fabsf(v[1]));
+    float w[8], inv = __uint_as_float((260u - E) << 23);
 #pragma unroll
-    for (int j = 2; j < 8; ++j) m = max_nan(m, fabsf(v[j]));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t E = group_exp(__float_as_uint(m) & 0x7fffffffu);
-    uint32_t q[8];
-    if (!group_is_slow(E)) {
-        const float inv = group_inv(E);
+    for (int j = 0; j < 8; ++j) w[j] = v[j];
+    if (E - 6u > 247u) {
+        // The scale leaves binary32's range (E < 6: in two steps), a code may pass 127 (E = 254), or the group
+        // has no codes (E = 255: all 0; the bounds swallow NaN).
+        const float bound = E < 6u ? __uint_as_float(0x7f800000u) : E == 254u ? 127.0f * 0x1p121f : 0.0f;
+        const float pre = E < 6u ? 0x1p64f : 1.0f;
+        inv = E < 6u ? __uint_as_float((196u - E) << 23) : 0x1p-121f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = group_code(v[j], inv);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = group_code_slow(v[j], E);
+        for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(fminf(fmaxf(v[j], -bound), bound), pre);
     }
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = group_code(w[j], inv);
+    return make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+}
+
+// E of the group that a lane's 8 elements belong to (4 lanes hold it); every lane of the warp calls it.
+__device__ __forceinline__ uint32_t group_of(const Words<float> &r)
+{
+    uint32_t m = r.w[0] & 0x7fffffffu;  // as integers, NaNs and infinities are the largest
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = max(m, r.w[j] & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return group_exp(m);
+}
+template <typename W>
+__device__ __forceinline__ uint32_t max16x2(const W &r)
+{
+    uint32_t m = r.w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int j = 1; j < 4; ++j) m = __vmaxu2(m, r.w[j] & 0x7fff7fffu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ uint32_t group_of(const Words<__nv_bfloat16> &r) { return group_exp(max16x2(r) << 16); }
+__device__ __forceinline__ uint32_t group_of(const Words<__half> &r)
+{
+    return group_exp(__float_as_uint(__half2float(__ushort_as_half((unsigned short)max16x2(r)))));
+}
+
+// Encode a lane's 8 elements (0 past the last column; r and v hold the same) of a chunk; every lane of the
+// warp calls it.
+template <typename T>
+__device__ __forceinline__ void ckpt_store(const Words<T> &r, const float (&v)[8], const Ckpt &k, int64_t row, int base, int lane)
+{
+    const uint32_t E = group_of(r);
+    const uint2 q = group_codes(v, E);
     const int c0 = base + lane * 8;
-    if (c0 < k.code_pitch)
-        *reinterpret_cast<uint2 *>(k.codes + row * k.code_pitch + c0) =
-            make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+    if (c0 < k.code_pitch) *reinterpret_cast<uint2 *>(k.codes + row * k.code_pitch + c0) = q;
     if ((lane & 3) == 0 && (c0 >> 5) < k.exp_pitch) k.exps[row * k.exp_pitch + (c0 >> 5)] = (uint8_t)E;
 }
 

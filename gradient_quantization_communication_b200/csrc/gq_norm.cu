@@ -45,8 +45,7 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-// A lane's 8 values of gamma or beta (fill where there is none).  They are read again for every row: from
-// L1, which costs less than the registers that would hold them.
+// A lane's 8 values of gamma or beta (fill where there is none).
 template <typename T>
 __device__ __forceinline__ void param_load(float (&v)[8], const void *p, int f32, float fill, int base, int lane, int cols)
 {
@@ -127,6 +126,25 @@ inline Shape forward_shape(int64_t rows, int64_t cols)
 // Backward: two, whose sums and next row still fit 128 registers.
 inline Shape backward_shape(int64_t cols) { return shape_of(cols, 2); }
 
+// gamma or beta of all columns in shared memory, binary32, read again for every row: n chunks of 256 columns,
+// of which lane l's first four (columns 8 l ..) lie at words 4 l and its others at 128 + 4 l, so that 8 lanes
+// read all banks.  Columns past the last hold 0.
+template <typename T>
+__device__ __forceinline__ void params_to_shared(float *dst, const void *src, int f32, float fill, int n, int cols)
+{
+    for (int i = threadIdx.x; i < n * kChunk; i += blockDim.x) {
+        const int c = i & (kChunk - 1), at = (i - c) + (c & 4) * 32 + (c >> 3) * 4 + (c & 3);
+        dst[at] = i >= cols ? 0.0f : !src ? fill : f32 ? static_cast<const float *>(src)[i] : to_f(static_cast<const T *>(src)[i]);
+    }
+}
+__device__ __forceinline__ void params_shared(float (&v)[8], const float *src, int base, int lane)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(src + base + lane * 4);
+    const float4 b = *reinterpret_cast<const float4 *>(src + base + 128 + lane * 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
 // Barrier of a slot's G warps.
 __device__ __forceinline__ void slot_sync(int slot, int G)
 {
@@ -136,6 +154,7 @@ __device__ __forceinline__ void slot_sync(int slot, int G)
 template <typename T, bool AL, int NC, bool KEEP>
 __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params p)
 {
+    extern __shared__ float4 shared_params[];
     __shared__ float4 buf[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
     const int slot = warp / G, wslot = warp - slot * G;
@@ -144,6 +163,10 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 #pragma unroll
     for (int c = 0; c < NC; ++c) mine += (float)min(max(p.cols - (wslot + c * G) * kChunk, 0), kChunk);
     const float inv_mine = 1.0f / mine;
+    float *gamma = reinterpret_cast<float *>(shared_params), *beta = gamma + NC * G * kChunk;
+    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols);
+    params_to_shared<T>(beta, p.beta, p.params_f32, 0.0f, NC * G, p.cols);
+    __syncthreads();
     const int64_t step = (int64_t)gridDim.x * p.slots;
     int64_t row = (int64_t)blockIdx.x * p.slots + slot;
     Raw<T, AL> next[NC];
@@ -159,9 +182,11 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
         float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            to_floats(in_place<T, AL>(next[c], static_cast<const T *>(p.x) + row * p.sx), v[c]);
+            const Words<T> w = in_place<T, AL>(next[c], static_cast<const T *>(p.x) + row * p.sx);
+            to_floats(w, v[c]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[c][j];
+            if constexpr (KEEP) ckpt_store<T>(w, v[c], p.k, row, (wslot + c * G) * kChunk, lane);
         }
         if (row + step < p.rows) fetch(row + step);
         // the warp's own mean and squares around it, then all warps' put together with one barrier:
@@ -205,10 +230,9 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int base = (wslot + c * G) * kChunk;
-            if constexpr (KEEP) ckpt_store(v[c], p.k, row, base, lane);
             float g[8], b[8];
-            param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
-            param_load<T>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
+            params_shared(g, gamma, base, lane);
+            params_shared(b, beta, base, lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn((v[c][j] - mean) * rstd, g[j], b[j]);
             row_store<T, AL>(v[c], static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
@@ -224,7 +248,7 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 template <typename T, bool AL, int NC, bool FROM_CKPT>
 __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params p)
 {
-    extern __shared__ float fold[];  // slots > 1: the block's sums, cols of dgamma and cols of dbeta
+    extern __shared__ float4 shared_params[];
     __shared__ float2 buf[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
     const int slot = warp / G, wslot = warp - slot * G;
@@ -251,6 +275,9 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
 #pragma unroll
         for (int j = 0; j < 8; ++j) sg[c][j] = sb[c][j] = 0.0f;
     if (row < p.rows) fetch(row);
+    float *gamma = reinterpret_cast<float *>(shared_params);
+    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols);
+    __syncthreads();
     int turn = 0;
     for (; row < p.rows; row += step, turn ^= 1) {
         float x[NC][8], d[NC][8];
@@ -273,7 +300,7 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float g[8];
-            param_load<T>(g, p.gamma, p.params_f32, 1.0f, (wslot + c * G) * kChunk, lane, p.cols);
+            params_shared(g, gamma, (wslot + c * G) * kChunk, lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {  // past the last column d is 0
                 sg[c][j] = __fmaf_rn(d[c][j], x[c][j], sg[c][j]);
@@ -304,7 +331,8 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
         }
     }
     if (!p.part_b) return;
-    // the slots' sums, slot by slot in order
+    // the slots' sums, slot by slot in order (slots > 1: in shared memory behind gamma)
+    float *fold = gamma + NC * G * kChunk;
     for (int t = 0; t < p.slots; ++t) {
         if (slot == t) {
 #pragma unroll
@@ -365,8 +393,11 @@ __global__ void __launch_bounds__(512) k_forward_any(const __grid_constant__ Par
         const float rstd = 1.0f / sqrtf(row_sum(ss, buf[1], G, warp, lane) * inv_c + p.eps);
         for (int base = warp * kChunk; base < p.cols; base += G * kChunk) {
             float v[8], g[8], b[8];
-            row_floats<T, AL>(v, x, base, lane, p.cols);
-            if (p.k.codes) ckpt_store(v, p.k, row, base, lane);
+            Raw<T, AL> r;
+            chunk_load<T, AL>(r, x, base, lane, p.cols);
+            const Words<T> w = in_place<T, AL>(r, x);
+            to_floats(w, v);
+            if (p.k.codes) ckpt_store<T>(w, v, p.k, row, base, lane);
             param_load<T>(g, p.gamma, p.params_f32, 1.0f, base, lane, p.cols);
             param_load<T>(b, p.beta, p.params_f32, 0.0f, base, lane, p.cols);
 #pragma unroll
@@ -523,11 +554,12 @@ cudaError_t forward_reg(const Params &p, bool al, cudaStream_t s)
     auto kern = al ? (p.k.codes ? k_forward<T, true, NC, true> : k_forward<T, true, NC, false>)
                     : (p.k.codes ? k_forward<T, false, NC, true> : k_forward<T, false, NC, false>);
     const int threads = p.G * p.slots * 32;
+    const size_t smem = (size_t)NC * p.G * kChunk * 2 * sizeof(float);
     int per_sm = 0, sms = 0;
-    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), threads, 0, &per_sm, &sms);
+    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), threads, smem, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     const int64_t need = (p.rows + p.slots - 1) / p.slots, most = (int64_t)per_sm * sms;
-    kern<<<(unsigned)(need < most ? need : most), threads, 0, s>>>(p);
+    kern<<<(unsigned)(need < most ? need : most), threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -558,7 +590,10 @@ cudaError_t backward_reg(const Params &p, bool al, cudaStream_t s)
 {
     auto kern = al ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
                     : (p.x ? k_backward<T, false, NC, false> : k_backward<T, false, NC, true>);
-    const size_t smem = p.slots > 1 ? (size_t)p.cols * 2 * sizeof(float) : 0;
+    const size_t smem = ((size_t)NC * p.G * kChunk + (p.slots > 1 ? (size_t)p.cols * 2 : 0)) * sizeof(float);
+    int per_sm = 0, sms = 0;
+    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), p.G * p.slots * 32, smem, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
     kern<<<(unsigned)p.parts, p.G * p.slots * 32, smem, s>>>(p);
     return cudaGetLastError();
 }
