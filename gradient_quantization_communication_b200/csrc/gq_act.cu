@@ -1,7 +1,7 @@
 // gq_act.cu -- pack and unpack of the 8-bit activation checkpoint, and activation functions whose
 // forward pass writes the checkpoint of its input and whose backward pass reads it.
 //
-// All are one pass over their tensors: a warp takes 512 columns of a row at a time.  Bounded by
+// All are one pass over their tensors: a warp takes 512 or 1024 columns of a row at a time.  Bounded by
 // the bytes; the arithmetic leaves some 27 instruction slots an element at full bandwidth in 16-bit types.
 #include "gq_act.cuh"
 #include "gq_act.h"
@@ -11,7 +11,11 @@ namespace gq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItem = 2 * kChunk;  // columns of a row that a warp takes at a time
+constexpr int kWide = 4 * kChunk;
+// Chunks of a row that a warp takes at a time.  Four spread an item's addresses over the most elements; where a
+// chunk is two loads, or is shifted into place, their registers cost more (SiLU backward 70 us with two, 101 us
+// with four; forward 66 and 60 us, 16384 x 4096 bf16).
+__host__ __device__ constexpr int chunks_of(int op, bool al) { return op == kBackward || !al ? 2 : 4; }
 
 // f(x) and f'(x), in binary32.
 //   GELU       x Phi(x);  Phi(x) + x phi(x).  Phi = erfc(-x / sqrt 2) / 2, which keeps the negative
@@ -20,13 +24,15 @@ constexpr int kItem = 2 * kChunk;  // columns of a row that a warp takes at a ti
 //   SiLU       x s(x);  s (1 + x (1 - s)).
 // In 16-bit types, whose own step hides it, the exponential is the hardware's (2^-21 or so), and Phi's tail
 // comes from a polynomial; binary32 calls expf and erfcf.
-// exp(t) for t <= 0.
-template <bool FAST>
+// exp(t) for t <= 0.  FLUSH: 0 where it is subnormal.
+template <bool FAST, bool FLUSH = false>
 __device__ __forceinline__ float exp_neg(float t)
 {
     if constexpr (!FAST) return expf(t);
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));  // keeps subnormal results: x times them need not be
+    if constexpr (FLUSH) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));
+    else
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));
     return r;
 }
 // 1 / x for 1 <= x.
@@ -50,10 +56,10 @@ __device__ __forceinline__ void logistic(float t, float &s, float &one_minus)
 }
 
 // Phi(x) and exp(-x^2 / 2).
-template <bool FAST>
+template <bool FAST, bool FLUSH>
 __device__ __forceinline__ void normal(float x, float &Phi, float &e)
 {
-    e = exp_neg<FAST>(-0.5f * x * x);
+    e = exp_neg<FAST, FLUSH>(-0.5f * x * x);
     if constexpr (FAST) {
         // Phi(-z) exp(z^2 / 2) = t P(t) with t = 1 / (1 + 0.31 z), z = |x|: the smoothest of such maps of
         // [0, inf) to (0, 1].  P has degree 7, fitted on z <= 14.5 (beyond, the tail is below binary32's
@@ -83,13 +89,13 @@ struct Fn<GQ_FN_GELU, FAST> {
     static __device__ __forceinline__ float f(float x)
     {
         float P, e;
-        normal<FAST>(x, P, e);
+        normal<FAST, true>(x, P, e);  // where e is subnormal, |x P| is too
         return x * P;
     }
     static __device__ __forceinline__ float df(float x)
     {
         float P, e;
-        normal<FAST>(x, P, e);
+        normal<FAST, false>(x, P, e);
         return __fmaf_rn(x * 0.39894228f, e, P);
     }
 };
@@ -140,11 +146,52 @@ struct Params {
     Ckpt k;
 };
 
+// One item: up to chunks_of() chunks from column `base` of a row.  FULL: all of them exist.
+template <typename T, int OP, int KIND, bool AL, bool FULL>
+__device__ __forceinline__ void act_item(const Params &p, int64_t row, int base, int lane)
+{
+    constexpr bool READS = OP != kUnpack, WRITES = OP != kPack, DECODES = OP == kUnpack || OP == kBackward;
+    constexpr int U = chunks_of(OP, AL);
+    using F = Fn<KIND, sizeof(T) == 2>;
+    const T *a = static_cast<const T *>(p.a) + row * p.sa;
+    Raw<T, AL> raw[U];
+    RawCkpt rk[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (!FULL && u > 0 && base + u * kChunk >= p.cols) break;
+        if constexpr (READS) chunk_load<T, AL, FULL>(raw[u], a, base + u * kChunk, lane, p.cols);
+        if constexpr (DECODES) ckpt_load<FULL>(rk[u], p.k, row, base + u * kChunk, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = base + u * kChunk;
+        if (!FULL && u > 0 && at >= p.cols) break;
+        float in[8], v[8], o[8];
+        if constexpr (READS) {
+            const Words<T> w = in_place<T, AL>(raw[u], a);
+            to_floats(w, in);
+            if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store<T, FULL>(w, in, p.k, row, at, lane);
+        }
+        if constexpr (DECODES) ckpt_floats(rk[u], v);
+        if constexpr (OP == kUnpack) saturate<T>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (OP == kUnpack) o[j] = v[j];
+            else if constexpr (OP == kBackward) o[j] = in[j] * F::df(v[j]);
+            else if constexpr (WRITES) o[j] = F::f(in[j]);
+        }
+        if constexpr (WRITES) {
+            Words<T> out;
+            from_floats(out, o);
+            chunk_store<T, AL, FULL>(out, static_cast<T *>(p.b) + row * p.sb, at, lane, p.cols);
+        }
+    }
+}
+
 template <typename T, int OP, int KIND, bool AL>
 __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params p)
 {
-    constexpr bool READS = OP != kUnpack, WRITES = OP != kPack, DECODES = OP == kUnpack || OP == kBackward;
-    using F = Fn<KIND, sizeof(T) == 2>;
+    constexpr int kItem = chunks_of(OP, AL) * kChunk;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
     int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -153,38 +200,8 @@ __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params
     int place = (int)(id - row * p.per_row);
     for (; id < p.items; id += warps) {
         const int base = place * kItem;
-        const T *a = static_cast<const T *>(p.a) + row * p.sa;
-        Raw<T, AL> raw[kItem / kChunk];
-        RawCkpt rk[kItem / kChunk];
-#pragma unroll
-        for (int u = 0; u < kItem / kChunk; ++u) {
-            if constexpr (READS) chunk_load<T, AL>(raw[u], a, base + u * kChunk, lane, p.cols);
-            if constexpr (DECODES) ckpt_load(rk[u], p.k, row, base + u * kChunk, lane);
-        }
-#pragma unroll
-        for (int u = 0; u < kItem / kChunk; ++u) {
-            const int at = base + u * kChunk;
-            if (u > 0 && at >= p.cols) break;
-            float in[8], v[8], o[8];
-            if constexpr (READS) {
-                const Words<T> w = in_place<T, AL>(raw[u], a);
-                to_floats(w, in);
-                if constexpr (OP == kPack || OP == kForwardKeep) ckpt_store<T>(w, in, p.k, row, at, lane);
-            }
-            if constexpr (DECODES) ckpt_floats(rk[u], v);
-            if constexpr (OP == kUnpack) saturate<T>(v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (OP == kUnpack) o[j] = v[j];
-                else if constexpr (OP == kBackward) o[j] = in[j] * F::df(v[j]);
-                else if constexpr (WRITES) o[j] = F::f(in[j]);
-            }
-            if constexpr (WRITES) {
-                Words<T> out;
-                from_floats(out, o);
-                chunk_store<T, AL>(out, static_cast<T *>(p.b) + row * p.sb, at, lane, p.cols);
-            }
-        }
+        if (AL && base + kItem <= p.cols) act_item<T, OP, KIND, AL, true>(p, row, base, lane);
+        else act_item<T, OP, KIND, AL, false>(p, row, base, lane);
         row += p.drow;
         place += p.dplace;
         if (place >= p.per_row) {
@@ -195,13 +212,17 @@ __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params
 }
 
 template <typename T, int OP, int KIND>
-cudaError_t launch(const ActArgs &a, cudaStream_t stream)
+cudaError_t launch(ActArgs a, cudaStream_t stream)
 {
+    // Rows without gaps, in the tensors and in the checkpoint, are one long row: cut it into rows of whole items.
+    const int64_t n = a.rows * a.cols;
+    if (a.cols % 128 == 0 && n % kWide == 0 && (OP == kUnpack || a.a.stride == a.cols) && (OP == kPack || a.b.stride == a.cols)) {
+        a.cols = a.a.stride = a.b.stride = kWide;
+        a.rows = n / kWide;
+    }
     const CkptLayout l = ckpt_layout(a.rows, a.cols);
     Params p;
     p.cols = (int)a.cols;
-    p.per_row = (int)((a.cols + kItem - 1) / kItem);
-    p.items = a.rows * p.per_row;
     p.a = a.a.p;
     p.sa = a.a.stride;
     p.b = const_cast<void *>(a.b.p);
@@ -211,6 +232,9 @@ cudaError_t launch(const ActArgs &a, cudaStream_t stream)
     // whether every row starts on 16 bytes (the bases do)
     const int per16 = 16 / (int)sizeof(T);
     const bool al = (OP == kUnpack || a.rows == 1 || p.sa % per16 == 0) && (OP == kPack || a.rows == 1 || p.sb % per16 == 0);
+    const int item = chunks_of(OP, al) * kChunk;
+    p.per_row = (int)((a.cols + item - 1) / item);
+    p.items = a.rows * p.per_row;
     auto kern = al ? k_act<T, OP, KIND, true> : k_act<T, OP, KIND, false>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);

@@ -91,12 +91,13 @@ __device__ __forceinline__ void shift_words(const uint32_t (&in)[N + 4], uint32_
     for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], bits);
 }
 
-template <typename T, bool AL>
+// FULL: all 256 columns of the chunk exist.
+template <typename T, bool AL, bool FULL = false>
 __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base, int lane, int cols)
 {
     const int c0 = base + lane * 8;
     if constexpr (AL) {
-        if (c0 + 8 <= cols) {
+        if (FULL || c0 + 8 <= cols) {
             const uint4 *p = reinterpret_cast<const uint4 *>(row + c0);
             const uint4 a = __ldg(p);
             r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
@@ -115,7 +116,7 @@ __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = first + i * E;
-            if (c >= 0 && c + E <= cols) {
+            if (c >= 0 && ((FULL && i + 1 < P) || c + E <= cols)) {
                 const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + c));
                 r.w[4 * i] = a.x; r.w[4 * i + 1] = a.y; r.w[4 * i + 2] = a.z; r.w[4 * i + 3] = a.w;
             } else {
@@ -188,14 +189,14 @@ __device__ __forceinline__ void from_floats(Words<__half> &r, const float (&v)[8
 }
 
 // Every lane of the warp calls it.
-template <typename T, bool AL>
+template <typename T, bool AL, bool FULL = false>
 __device__ __forceinline__ void chunk_store(const Words<T> &r, T *row, int base, int lane, int cols)
 {
     constexpr int W = 2 * sizeof(T);
     const int c0 = base + lane * 8;
     const uint32_t shift = AL ? 0u : row_shift(row);
     if (AL || shift == 0u) {
-        if (c0 + 8 <= cols) {
+        if (FULL || c0 + 8 <= cols) {
             uint4 *p = reinterpret_cast<uint4 *>(row + c0);
             p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
             if constexpr (sizeof(T) == 4) p[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
@@ -312,14 +313,20 @@ __device__ __forceinline__ uint32_t group_of(const Words<float> &r)
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     return group_exp(m);
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 template <typename W>
 __device__ __forceinline__ uint32_t max16x2(const W &r)
 {
     uint32_t m = r.w[0] & 0x7fff7fffu;
 #pragma unroll
-    for (int j = 1; j < 4; ++j) m = __vmaxu2(m, r.w[j] & 0x7fff7fffu);
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    for (int j = 1; j < 4; ++j) m = max_u16x2(m, r.w[j] & 0x7fff7fffu);
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     return max(m & 0xffffu, m >> 16);
 }
 __device__ __forceinline__ uint32_t group_of(const Words<__nv_bfloat16> &r) { return group_exp(max16x2(r) << 16); }
@@ -330,14 +337,14 @@ __device__ __forceinline__ uint32_t group_of(const Words<__half> &r)
 
 // Encode a lane's 8 elements (0 past the last column; r and v hold the same) of a chunk; every lane of the
 // warp calls it.
-template <typename T>
+template <typename T, bool FULL = false>
 __device__ __forceinline__ void ckpt_store(const Words<T> &r, const float (&v)[8], const Ckpt &k, int64_t row, int base, int lane)
 {
     const uint32_t E = group_of(r);
     const uint2 q = group_codes(v, E);
     const int c0 = base + lane * 8;
-    if (c0 < k.code_pitch) *reinterpret_cast<uint2 *>(k.codes + row * k.code_pitch + c0) = q;
-    if ((lane & 3) == 0 && (c0 >> 5) < k.exp_pitch) k.exps[row * k.exp_pitch + (c0 >> 5)] = (uint8_t)E;
+    if (FULL || c0 < k.code_pitch) *reinterpret_cast<uint2 *>(k.codes + row * k.code_pitch + c0) = q;
+    if ((lane & 3) == 0 && (FULL || (c0 >> 5) < k.exp_pitch)) k.exps[row * k.exp_pitch + (c0 >> 5)] = (uint8_t)E;
 }
 
 // A lane's codes and their exponent, as loaded.
@@ -345,11 +352,12 @@ struct RawCkpt {
     uint32_t q[2], e;
 };
 
+template <bool FULL = false>
 __device__ __forceinline__ void ckpt_load(RawCkpt &r, const Ckpt &k, int64_t row, int base, int lane)
 {
     const int c0 = base + lane * 8;
-    r.q[0] = r.q[1] = r.e = 0;
-    if (c0 < k.code_pitch) {
+    if (!FULL) r.q[0] = r.q[1] = r.e = 0;
+    if (FULL || c0 < k.code_pitch) {
         const uint2 a = __ldg(reinterpret_cast<const uint2 *>(k.codes + row * k.code_pitch + c0));
         r.q[0] = a.x;
         r.q[1] = a.y;
