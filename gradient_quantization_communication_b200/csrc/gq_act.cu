@@ -146,7 +146,7 @@ struct Params {
     Ckpt k;
 };
 
-// One item: up to chunks_of() chunks from column `base` of a row.  FULL: all of them exist.
+// One item: up to chunks_of() chunks from column `base` of a row.  FULL: all of them are inner chunks.
 template <typename T, int OP, int KIND, bool AL, bool FULL>
 __device__ __forceinline__ void act_item(const Params &p, int64_t row, int base, int lane)
 {
@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads) k_act(const __grid_constant__ Params
     int place = (int)(id - row * p.per_row);
     for (; id < p.items; id += warps) {
         const int base = place * kItem;
-        if (AL && base + kItem <= p.cols) act_item<T, OP, KIND, AL, true>(p, row, base, lane);
+        if (inner_chunk<T, AL>(base, p.cols) && inner_chunk<T, AL>(base + kItem - kChunk, p.cols))
+            act_item<T, OP, KIND, AL, true>(p, row, base, lane);
         else act_item<T, OP, KIND, AL, false>(p, row, base, lane);
         row += p.drow;
         place += p.dplace;

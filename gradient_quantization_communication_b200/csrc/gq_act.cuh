@@ -91,7 +91,7 @@ __device__ __forceinline__ void shift_words(const uint32_t (&in)[N + 4], uint32_
     for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], bits);
 }
 
-// FULL: all 256 columns of the chunk exist.
+// FULL: all lanes' 16-byte pieces lie inside the row (inner_chunk).
 template <typename T, bool AL, bool FULL = false>
 __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base, int lane, int cols)
 {
@@ -116,7 +116,7 @@ __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int c = first + i * E;
-            if (c >= 0 && ((FULL && i + 1 < P) || c + E <= cols)) {
+            if (FULL || (c >= 0 && c + E <= cols)) {
                 const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + c));
                 r.w[4 * i] = a.x; r.w[4 * i + 1] = a.y; r.w[4 * i + 2] = a.z; r.w[4 * i + 3] = a.w;
             } else {
@@ -126,6 +126,14 @@ __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base
             }
         }
     }
+}
+
+// Whether all pieces of the chunk at column base lie inside the row: then nothing is checked lane by lane.
+// Unaligned rows need up to 8 columns more on either side.
+template <typename T, bool AL>
+__device__ __forceinline__ bool inner_chunk(int base, int cols)
+{
+    return AL ? base + kChunk <= cols : base > 0 && base + kChunk + 8 <= cols;
 }
 
 // The loaded elements in place.
@@ -215,18 +223,18 @@ __device__ __forceinline__ void chunk_store(const Words<T> &r, T *row, int base,
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[W + i] = __shfl_down_sync(0xffffffffu, r.w[i], 1);
     shift_words<W>(w, 16u - shift, o);
-    const bool whole = lane < 31 && c0 + head + 8 <= cols;
+    const bool whole = lane < 31 && (FULL || c0 + head + 8 <= cols);
     if (whole) {
         uint4 *p = reinterpret_cast<uint4 *>(row + c0 + head);
         p[0] = make_uint4(o[0], o[1], o[2], o[3]);
         if constexpr (sizeof(T) == 4) p[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     // elements no piece covers: the first lane's head, and the last lanes' rest
-    const bool own_head = lane == 0 || c0 + head > cols;
+    const bool own_head = lane == 0 || (!FULL && c0 + head > cols);
     if (own_head || !whole) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c0 + j < cols && (j < head ? own_head : !whole)) row[c0 + j] = elem_get<T>(r.w, j);
+            if ((FULL || c0 + j < cols) && (j < head ? own_head : !whole)) row[c0 + j] = elem_get<T>(r.w, j);
     }
 }
 

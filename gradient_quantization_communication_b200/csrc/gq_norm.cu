@@ -77,12 +77,12 @@ __device__ __forceinline__ void row_floats(float (&v)[8], const T *row, int base
     chunk_load<T, AL>(r, row, base, lane, cols);
     to_floats(in_place<T, AL>(r, row), v);
 }
-template <typename T, bool AL>
+template <typename T, bool AL, bool FULL = false>
 __device__ __forceinline__ void row_store(const float (&v)[8], T *row, int base, int lane, int cols)
 {
     Words<T> r;
     from_floats(r, v);
-    chunk_store<T, AL>(r, row, base, lane, cols);
+    chunk_store<T, AL, FULL>(r, row, base, lane, cols);
 }
 
 // Sum over the G warps that share a row; `buf` holds one float per warp.  One barrier: the caller
@@ -128,13 +128,16 @@ inline Shape backward_shape(int64_t cols) { return shape_of(cols, 2); }
 
 // gamma or beta of all columns in shared memory, binary32, read again for every row: n chunks of 256 columns,
 // of which lane l's first four (columns 8 l ..) lie at words 4 l and its others at 128 + 4 l, so that 8 lanes
-// read all banks.  Columns past the last hold 0.
+// read all banks.  What columns past the last hold is not used.
 template <typename T>
-__device__ __forceinline__ void params_to_shared(float *dst, const void *src, int f32, float fill, int n, int cols)
+__device__ __forceinline__ void params_to_shared(float *dst, const void *src, int f32, float fill, int n, int cols, int warp, int lane)
 {
-    for (int i = threadIdx.x; i < n * kChunk; i += blockDim.x) {
-        const int c = i & (kChunk - 1), at = (i - c) + (c & 4) * 32 + (c >> 3) * 4 + (c & 3);
-        dst[at] = i >= cols ? 0.0f : !src ? fill : f32 ? static_cast<const float *>(src)[i] : to_f(static_cast<const T *>(src)[i]);
+    for (int i = warp; i < n; i += blockDim.x >> 5) {
+        float v[8];
+        param_load<T>(v, src, f32, fill, i * kChunk, lane, cols);
+        float4 *d = reinterpret_cast<float4 *>(dst + i * kChunk) + lane;
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[32] = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
 __device__ __forceinline__ void params_shared(float (&v)[8], const float *src, int base, int lane)
@@ -156,7 +159,8 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 {
     extern __shared__ float4 shared_params[];
     __shared__ float4 buf[2][16];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
+    const int lane = threadIdx.x & 31, G = p.G;
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);  // known to be the same in all lanes
     const int slot = warp / G, wslot = warp - slot * G;
     const float inv_c = 1.0f / (float)p.cols;
     float mine = 0.0f;  // columns of this warp
@@ -164,16 +168,20 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
     for (int c = 0; c < NC; ++c) mine += (float)min(max(p.cols - (wslot + c * G) * kChunk, 0), kChunk);
     const float inv_mine = 1.0f / mine;
     float *gamma = reinterpret_cast<float *>(shared_params), *beta = gamma + NC * G * kChunk;
-    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols);
-    params_to_shared<T>(beta, p.beta, p.params_f32, 0.0f, NC * G, p.cols);
+    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols, warp, lane);
+    params_to_shared<T>(beta, p.beta, p.params_f32, 0.0f, NC * G, p.cols, warp, lane);
     __syncthreads();
     const int64_t step = (int64_t)gridDim.x * p.slots;
     int64_t row = (int64_t)blockIdx.x * p.slots + slot;
     Raw<T, AL> next[NC];
+    auto inner = [&](int c) { return inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
     auto fetch = [&](int64_t r) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            chunk_load<T, AL>(next[c], static_cast<const T *>(p.x) + r * p.sx, (wslot + c * G) * kChunk, lane, p.cols);
+        for (int c = 0; c < NC; ++c) {
+            const T *x = static_cast<const T *>(p.x) + r * p.sx;
+            if (inner(c)) chunk_load<T, AL, true>(next[c], x, (wslot + c * G) * kChunk, lane, p.cols);
+            else chunk_load<T, AL, false>(next[c], x, (wslot + c * G) * kChunk, lane, p.cols);
+        }
     };
     if (row < p.rows) fetch(row);
     int turn = 0;
@@ -186,7 +194,10 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
             to_floats(w, v[c]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[c][j];
-            if constexpr (KEEP) ckpt_store<T>(w, v[c], p.k, row, (wslot + c * G) * kChunk, lane);
+            if constexpr (KEEP) {
+                if (inner(c)) ckpt_store<T, true>(w, v[c], p.k, row, (wslot + c * G) * kChunk, lane);
+                else ckpt_store<T, false>(w, v[c], p.k, row, (wslot + c * G) * kChunk, lane);
+            }
         }
         if (row + step < p.rows) fetch(row + step);
         // the warp's own mean and squares around it, then all warps' put together with one barrier:
@@ -235,7 +246,9 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
             params_shared(b, beta, base, lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn((v[c][j] - mean) * rstd, g[j], b[j]);
-            row_store<T, AL>(v[c], static_cast<T *>(p.y) + row * p.sy, base, lane, p.cols);
+            T *y = static_cast<T *>(p.y) + row * p.sy;
+            if (inner(c)) row_store<T, AL, true>(v[c], y, base, lane, p.cols);
+            else row_store<T, AL, false>(v[c], y, base, lane, p.cols);
         }
         if (wslot == 0 && lane == 0) {
             p.mean[row] = mean;
@@ -258,15 +271,22 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
     Raw<T, AL> ndy[NC], nx[FROM_CKPT ? 1 : NC];
     RawCkpt nk[FROM_CKPT ? NC : 1];
     float nmean = 0.0f, nrstd = 0.0f;
+    auto inner = [&](int c) { return inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
     auto fetch = [&](int64_t r) {
         nmean = __ldg(p.mean + r);
         nrstd = __ldg(p.rstd + r);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int base = (wslot + c * G) * kChunk;
-            chunk_load<T, AL>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
-            if constexpr (FROM_CKPT) ckpt_load(nk[c], p.k, r, base, lane);
-            else chunk_load<T, AL>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
+            if (inner(c)) {
+                chunk_load<T, AL, true>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
+                if constexpr (FROM_CKPT) ckpt_load<true>(nk[c], p.k, r, base, lane);
+                else chunk_load<T, AL, true>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
+            } else {
+                chunk_load<T, AL, false>(ndy[c], static_cast<const T *>(p.dy) + r * p.sdy, base, lane, p.cols);
+                if constexpr (FROM_CKPT) ckpt_load<false>(nk[c], p.k, r, base, lane);
+                else chunk_load<T, AL, false>(nx[c], static_cast<const T *>(p.x) + r * p.sx, base, lane, p.cols);
+            }
         }
     };
     float sg[NC][8], sb[NC][8];
@@ -276,7 +296,7 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
         for (int j = 0; j < 8; ++j) sg[c][j] = sb[c][j] = 0.0f;
     if (row < p.rows) fetch(row);
     float *gamma = reinterpret_cast<float *>(shared_params);
-    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols);
+    params_to_shared<T>(gamma, p.gamma, p.params_f32, 1.0f, NC * G, p.cols, warp, lane);
     __syncthreads();
     int turn = 0;
     for (; row < p.rows; row += step, turn ^= 1) {
@@ -327,7 +347,9 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[c][j] = __fmaf_rn(x[c][j], a1, __fmaf_rn(d[c][j], rstd, a0));
-            row_store<T, AL>(d[c], static_cast<T *>(p.y) + row * p.sy, (wslot + c * G) * kChunk, lane, p.cols);
+            T *y = static_cast<T *>(p.y) + row * p.sy;
+            if (inner(c)) row_store<T, AL, true>(d[c], y, (wslot + c * G) * kChunk, lane, p.cols);
+            else row_store<T, AL, false>(d[c], y, (wslot + c * G) * kChunk, lane, p.cols);
         }
     }
     if (!p.part_b) return;
