@@ -36,11 +36,11 @@ constexpr int kBBytes = kHalf * kTok * 2;
 constexpr int kCodeBytes = kHalf * kTok;
 constexpr int kExpBytes = kTok * 4;      // four groups' exponents of every token
 constexpr int kBlockBytes = kTok * 128;  // 64 columns x 64 tokens of a 16-bit operand
-// Two rings.  What is fetched (B, codes, exponents) lives from the start of its copy to the end of its MMA,
-// some 3000 cycles of which the copy takes half; the decoded A lives for its decoding and its MMA.
-constexpr int kLoads = 6, kDecoded = 5;
-constexpr int kLoadBytes = kBBytes + kCodeBytes;
-constexpr int kSmemBytes = kLoads * (kLoadBytes + kExpBytes) + kDecoded * kABytes + 1024;
+// Five stages of everything.  A ring of its own for the decoded A, so that six stages could be under way,
+// needs one more signal and wait a stage and measured slower (1.81 against 1.74 ms, 16384 x 4096 x 16384).
+constexpr int kStages = 5;
+constexpr int kStageBytes = kABytes + kBBytes + kCodeBytes;
+constexpr int kSmemBytes = kStages * (kStageBytes + kExpBytes) + 1024;
 // Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums round
 // toward zero, 16 products at a time: over 8192 tokens they came out 7e-6 small (relative), over 16384
 // 1.6e-5, where a chain rounded to nearest is off by 1e-6.  512 tokens lose 4e-7, and sums of such runs,
@@ -212,6 +212,18 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const float *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(
+            __float_as_uint(v[0])),
+        "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
+        "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+        "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])),
+        "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])), "r"(addr)
+        : "memory");
+}
+
 // ---------------------------------------------------------------------------------------------
 // Decoding 16 codes of one group.  Of four codes in a word, the even and the odd ones make a pair each
 // (a mask instead of a byte permutation), so columns 1 and 2 of every four change places in A; the
@@ -327,17 +339,15 @@ __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
 }
 
 struct Shared {
-    unsigned long long full[kLoads];       // codes, exponents and B have arrived (this CTA)
-    unsigned long long empty[kLoads];      // the MMAs have read B (and A, so the codes have been read)
-    unsigned long long ready[kDecoded];    // both CTAs have decoded A (the leader's is used)
-    unsigned long long a_empty[kDecoded];  // the MMAs have read A
-    unsigned long long acc_full[2];        // a run's sums are complete
-    unsigned long long acc_empty[2];       // both CTAs have read them (the leader's is used)
+    unsigned long long full[kStages];   // codes, exponents and B have arrived (this CTA)
+    unsigned long long ready[kStages];  // both CTAs have decoded A (the leader's is used)
+    unsigned long long empty[kStages];  // the MMAs have read A and B
+    unsigned long long acc_full[2];     // a run's sums are complete
+    unsigned long long acc_empty[2];    // both CTAs have read them (the leader's is used)
     uint32_t tmem;
 };
 
-// Position in a ring of N stages; wrapped: every stage has been used before.
-template <int N>
+// Position in the ring of stages; wrapped: every stage has been used before.
 struct Ring {
     int st = 0;
     uint32_t ph = 0;
@@ -345,8 +355,8 @@ struct Ring {
     __device__ __forceinline__ void next(int by = 1)
     {
         st += by;
-        if (st >= N) {
-            st -= N;
+        if (st >= kStages) {
+            st -= kStages;
             ph ^= 1u;
             wrapped = true;
         }
@@ -354,11 +364,48 @@ struct Ring {
     __device__ __forceinline__ void back()
     {
         if (--st < 0) {
-            st = N - 1;
+            st = kStages - 1;
             ph ^= 1u;
         }
     }
 };
+
+// 128 n of a tile from TMEM to dw, or to the workspace; a wait that gave up (ok false) leaves NaN.
+__device__ __forceinline__ void store_tile(const Params &p, const Item &it, uint32_t cols, int n_off, int kl, bool ok)
+{
+    const int64_t k = (int64_t)it.tk * kTile + kl;
+    const int n0 = it.tn * kTile + n_off;
+    const bool part = it.part >= 0;
+    const int n = part ? kTile / 2 : k < p.in ? p.out - n0 : 0;  // how many of the lane's n exist
+    const bool add = !part && p.accumulate;
+    const int64_t step = part ? kTile : p.sdw;
+    float *o = part ? p.parts + (it.part * kTile + n_off) * kTile + kl : p.dw + (int64_t)n0 * p.sdw + k;
+#pragma unroll 1
+    for (int c = 0; c < kTile / 2; c += 16) {
+        float v[16];
+        tmem_load16(cols + c, v);
+        if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7fffffffu);
+        }
+        if (add) {
+            float old[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) old[j] = c + j < n ? o[j * step] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] += old[j];
+        }
+        if (c + 16 <= n) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j * step] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < n) o[j * step] = v[j];
+        }
+        o += 16 * step;
+    }
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ Params p)
@@ -366,19 +413,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     extern __shared__ unsigned char raw_smem[];
     __shared__ Shared sh;
     const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
-    const uint32_t decoded = stages + kLoads * kLoadBytes, exps = decoded + kDecoded * kABytes;
+    const uint32_t exps = stages + kStages * kStageBytes;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kLoads; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1 + 32);
-            mbar_init(&sh.empty[i], 1);
-        }
-        for (int i = 0; i < kDecoded; ++i) {
             mbar_init(&sh.ready[i], kConvWarps);  // half of the warps, of two CTAs
-            mbar_init(&sh.a_empty[i], 1);
+            mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -400,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
             // TMA: codes and B of every stage
-            Ring<kLoads> r;
-            Ring<kDecoded> ra;
+            Ring r;
             bool ok = true;
             Item it;
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
@@ -414,13 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                         break;
                     }
                     const int t0 = (int)tb * kTok;
-                    const uint32_t base = stages + r.st * kLoadBytes, bar = smem_u32(&sh.full[r.st]);
+                    const uint32_t base = stages + r.st * kStageBytes, bar = smem_u32(&sh.full[r.st]);
                     mbar_arrive_expect_tx(&sh.full[r.st], kBBytes + kCodeBytes);
-                    tma_load_2d(base + kBBytes, &p.codes, k0, t0, bar);
-                    tma_load_3d(base, &p.dy, n0, t0, plane, bar);
-                    tma_load_3d(base + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
+                    tma_load_2d(base + kABytes + kBBytes, &p.codes, k0, t0, bar);
+                    tma_load_3d(base + kABytes, &p.dy, n0, t0, plane, bar);
+                    tma_load_3d(base + kABytes + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
                     r.next();
-                    ra.next();
                     if (++tb == p.s.tok_blocks) {
                         tb = 0;
                         ++plane;
@@ -429,11 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             }
             // what is still under way into this CTA's shared memory arrives before the CTA may leave: the
             // MMAs' signals (after which the copies have been read), or, where a wait gave up, the copies
-            const int left = r.wrapped ? kLoads : r.st, left_a = ok ? ra.wrapped ? kDecoded : ra.st : 0;
-            for (int i = 0; i < left_a; ++i) {
-                ra.back();
-                wait_thread(smem_u32(&sh.a_empty[ra.st]), ra.ph, p.limit);
-            }
+            const int left = r.wrapped ? kStages : r.st;
             for (int i = 0; i < left; ++i) {
                 r.back();
                 wait_thread(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit);
@@ -443,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             // lane issues
             const bool one = elect_one();
             const uint32_t idesc = instr_desc(BF16);
-            Ring<kLoads> r;
-            Ring<kDecoded> ra;
+            Ring r;
             int64_t runs = 0;
             bool ok = true;
             Item it;
@@ -460,22 +497,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                     const int n = (int)(it.last - b < kRun ? it.last - b : kRun);
                     b += n;
                     for (int j = 0; j < n; ++j) {
-                        if (!wait_warp(smem_u32(&sh.ready[ra.st]), ra.ph, p.limit)) {
+                        if (!wait_warp(smem_u32(&sh.ready[r.st]), r.ph, p.limit)) {
                             ok = false;
                             break;
                         }
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint64_t da = operand_desc(decoded + ra.st * kABytes), db = operand_desc(stages + r.st * kLoadBytes);
+                        const uint32_t base = stages + r.st * kStageBytes;
+                        const uint64_t da = operand_desc(base), db = operand_desc(base + kABytes);
                         if (one) {
 #pragma unroll
                             for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of 8, 2048 bytes
                                 mma(d, da + (uint64_t)(k * 2048 >> 4), db + (uint64_t)(k * 2048 >> 4), idesc, j > 0 || k > 0);
-                            commit_pair(smem_u32(&sh.a_empty[ra.st]));
                             commit_pair(smem_u32(&sh.empty[r.st]));
                         }
                         __syncwarp();
                         r.next();
-                        ra.next();
                     }
                     if (ok && one) commit_pair(smem_u32(&sh.acc_full[buf]));
                     __syncwarp();
@@ -484,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         } else if (warp == 2) {
             // Exponents of every stage: one word a token, two tokens a lane.  Loaded here and not by the warps
             // that decode: their signals would wait for loads of their own.
-            Ring<kLoads> r;
+            Ring r;
             bool ok = true;
             Item it;
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
@@ -526,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         const int n_off = (warp - kCtlWarps >= 4) ? kTile / 2 : 0;
         const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), 0);
         const uint32_t cols = tmem + ((uint32_t)(quarter * 32) << 16) + n_off;
+        const int kl = (int)rank * kHalf + quarter * 32 + (lane & 28) + ((lane & 1) << 1) + (lane >> 1 & 1);
         int64_t runs = 0;
         bool ok = true;
         Item it;
@@ -544,33 +581,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
 #pragma unroll
                     for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
                 }
+                if (b + kRun >= it.last) {
+                    // The tile's sums go back to TMEM, and from there to memory 16 at a time, in a loop that stays
+                    // in the instruction cache: storing the registers takes 128 stores of straight code, which
+                    // ran once a tile and took 20000 cycles.
+#pragma unroll
+                    for (int c = 0; c < kTile / 2; c += 16) tmem_store16(cols + buf * kTile + c, acc + c);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    store_tile(p, it, cols + buf * kTile, n_off, kl, ok);
+                }
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_cluster(acc_empty + buf * 8);
-            }
-            if (!ok) {  // a wait gave up: the tile's sums are not known
-#pragma unroll
-                for (int j = 0; j < kTile / 2; ++j) acc[j] = __uint_as_float(0x7fffffffu);
-            }
-            const int kl = (int)rank * kHalf + quarter * 32 + (lane & 28) + ((lane & 1) << 1) + (lane >> 1 & 1);
-            const int64_t k = (int64_t)it.tk * kTile + kl;
-            const int n0 = it.tn * kTile + n_off;
-            if (it.part >= 0) {
-                float *o = p.parts + (it.part * kTile + n_off) * kTile + kl;
-#pragma unroll
-                for (int j = 0; j < kTile / 2; ++j) o[j * kTile] = acc[j];
-            } else if (k < p.in) {
-                float *o = p.dw + (int64_t)n0 * p.sdw + k;
-                const int n = p.out - n0;
-                if (p.accumulate) {
-#pragma unroll
-                    for (int j = 0; j < kTile / 2; ++j)
-                        if (j < n) o[j * p.sdw] += acc[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kTile / 2; ++j)
-                        if (j < n) o[j * p.sdw] = acc[j];
-                }
             }
         }
     } else {
@@ -586,18 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         const int c = lane & 3, block = lane >> 3 & 1;
         const int pr = lane >> 4, x = (lane & 4) ? pr ^ 5 : pr;      // token & 7 of the first of four
         const int t = (w & 3) * 16 + x;
-        const uint32_t from = stages + kBBytes + t * 128 + (((block * 4 + c) ^ x) << 4);
-        const uint32_t to = decoded + block * kBlockBytes + t * 128 + (((2 * c) ^ x) << 4);  // and the piece beside it
+        const uint32_t from = stages + kABytes + kBBytes + t * 128 + (((block * 4 + c) ^ x) << 4);
+        const uint32_t to = stages + block * kBlockBytes + t * 128 + (((2 * c) ^ x) << 4);  // and the piece beside it
         const uint32_t ex = exps + t * 4 + block * 2 + (c >> 1);
-        Ring<kLoads> r;
-        Ring<kDecoded> ra;
+        Ring r;
         r.next(w >> 2);
-        ra.next(w >> 2);
-        for (int64_t i = w >> 2; i < total; i += 2, r.next(2), ra.next(2)) {
-            if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit) ||
-                (ra.wrapped && !wait_warp(smem_u32(&sh.a_empty[ra.st]), ra.ph ^ 1u, p.limit)))
-                break;
-            const uint32_t off = r.st * kLoadBytes, off_a = ra.st * kABytes;
+        for (int64_t i = w >> 2; i < total; i += 2, r.next(2)) {
+            if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit)) break;
+            const uint32_t off = r.st * kStageBytes;
             uint4 q[4];
             uint32_t E[4];
 #pragma unroll
@@ -610,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                              : "r"(ex + (h & 1) * 8 + (h >> 1) * 32 + r.st * kExpBytes));
             }
             auto put = [&](int h, const uint32_t (&o)[8]) {
-                const uint32_t at = (to ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off_a;
+                const uint32_t at = (to ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off;
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                              : "memory");
                 asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
@@ -636,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             // signal carries no more than that, and a release to the cluster would take some 1300 cycles
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) arrive_cluster(ready + ra.st * 8);
+            if (lane == 0) arrive_cluster(ready + r.st * 8);
         }
     }
     __syncwarp();
