@@ -13,7 +13,10 @@
 // wide the tile is: a stage's 64 x 128 codes cost about 180 issue slots of each scheduler, under the
 // 512 cycles or so that its four MMAs take.
 //
-// Bounded by the tensor pipe for long batches, by the bytes of dw for few tokens.
+// Bounded for long batches by shared memory, through which 80 KB a stage pass in each CTA: B and the codes in
+// (24), the codes out (8), A in (16), the MMAs' operands out (32); at 128 bytes a cycle 640 cycles, where the
+// MMAs take 512 and a stage some 700.  Fetching the codes into registers instead leaves 64 KB, but the signal
+// that A is decoded then waits for the loads ahead (twice the time).  For few tokens bounded by the bytes of dw.
 //
 // float32 gradients are cut into three bf16 planes without loss (8 significant bits each, by
 // truncation) by a pass before, and the contraction runs over 3 x tokens; so are rows that TMA cannot
@@ -616,22 +619,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         for (int64_t i = w >> 2; i < total; i += 2, r.next(2)) {
             if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit)) break;
             const uint32_t off = r.st * kStageBytes;
+            // tokens t, t + 2 (whose swizzle differs in bit 1), and 8 on
+            const uint32_t f[2] = {from + off, (from ^ 32u) + off};
+            const uint32_t at[4] = {to + off, (to ^ 16u) + off, (to ^ 32u) + off, (to ^ 48u) + off};
             uint4 q[4];
             uint32_t E[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {  // tokens t, t + 2 (its swizzle differs in bit 1), and 8 on
+            for (int h = 0; h < 4; ++h) {
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(q[h].x), "=r"(q[h].y), "=r"(q[h].z), "=r"(q[h].w)
-                             : "r"((from ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off));
+                             : "r"(f[h & 1] + (h & 1) * 256 + (h >> 1) * 1024));
                 asm volatile("ld.shared.u8 %0, [%1];"
                              : "=r"(E[h])
                              : "r"(ex + (h & 1) * 8 + (h >> 1) * 32 + r.st * kExpBytes));
             }
             auto put = [&](int h, const uint32_t (&o)[8]) {
-                const uint32_t at = (to ^ ((h & 1) * 32)) + (h & 1) * 256 + (h >> 1) * 1024 + off;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                const int d = (h & 1) * 256 + (h >> 1) * 1024;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at[(h & 1) * 2] + d), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                             "r"(o[3])
                              : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at[(h & 1) * 2 + 1] + d), "r"(o[4]), "r"(o[5]),
+                             "r"(o[6]), "r"(o[7])
                              : "memory");
             };
             if (usual<BF16>(E[0]) && usual<BF16>(E[1]) && usual<BF16>(E[2]) && usual<BF16>(E[3])) {
