@@ -485,28 +485,44 @@ __global__ void __launch_bounds__(512) k_backward_rows_any(const __grid_constant
     }
 }
 
-// Partial sums over the rows: warp (chunk c, part q) walks rows q, q + parts, ...
+// Partial sums over the rows: warp (chunk c, part q) walks rows q, q + parts, ..., eight (with the
+// input: two) at a time.
 template <typename T, bool AL, bool NORM>
 __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
 {
+    constexpr int U = NORM ? 2 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int base = ((int)blockIdx.x * 4 + warp) * kChunk;
     if (base >= p.cols) return;
+    const bool inner = inner_chunk<T, AL>(base, p.cols);
     float sg[8], sb[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sg[j] = sb[j] = 0.0f;
-    for (int64_t row = blockIdx.y; row < p.rows; row += p.parts) {
-        float d[8];
-        row_floats<T, AL>(d, static_cast<const T *>(p.dy) + row * p.sdy, base, lane, p.cols);
-        if constexpr (NORM) {
-            float x[8];
-            input_load<T, AL>(x, p, row, base, lane);
-            const float mean = p.mean[row], rstd = p.rstd[row];
+    for (int64_t row = blockIdx.y; row < p.rows; row += (int64_t)U * p.parts) {
+        Raw<T, AL> r[U];
+        float x[U][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sg[j] = __fmaf_rn(d[j], (x[j] - mean) * rstd, sg[j]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = row + (int64_t)u * p.parts;
+            if (t >= p.rows) break;
+            if (inner) chunk_load<T, AL, true>(r[u], static_cast<const T *>(p.dy) + t * p.sdy, base, lane, p.cols);
+            else chunk_load<T, AL, false>(r[u], static_cast<const T *>(p.dy) + t * p.sdy, base, lane, p.cols);
+            if constexpr (NORM) input_load<T, AL>(x[u], p, t, base, lane);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sb[j] += d[j];
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = row + (int64_t)u * p.parts;
+            if (t >= p.rows) break;
+            float d[8];
+            to_floats(in_place<T, AL>(r[u], static_cast<const T *>(p.dy) + t * p.sdy), d);
+            if constexpr (NORM) {
+                const float mean = p.mean[t], rstd = p.rstd[t];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sg[j] = __fmaf_rn(d[j], (x[u][j] - mean) * rstd, sg[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sb[j] += d[j];
+        }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -685,8 +701,11 @@ int64_t norm_parts(int64_t rows, int64_t cols)
 
 int64_t colsum_parts(int64_t rows, int64_t cols)
 {
-    (void)cols;
-    return rows < 128 ? rows : 128;
+    // enough parts for two blocks an SM, of at least 8 rows each (the partial rows stay few bytes)
+    const int64_t across = (cols + 4 * kChunk - 1) / (4 * kChunk);
+    int64_t n = (296 + across - 1) / across;
+    if (n > (rows + 7) / 8) n = (rows + 7) / 8;
+    return n;
 }
 
 cudaError_t launch_norm_forward(const NormArgs &a, cudaStream_t stream)

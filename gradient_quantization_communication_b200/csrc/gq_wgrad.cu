@@ -18,6 +18,8 @@
 // MMAs take 512 and a stage some 700.  Fetching the codes into registers instead leaves 64 KB, but the signal
 // that A is decoded then waits for the loads ahead (twice the time).  For few tokens bounded by the bytes of dw.
 //
+// A few tokens of a small layer go to a kernel of their own, k_few.
+//
 // float32 gradients are cut into three bf16 planes without loss (8 significant bits each, by
 // truncation) by a pass before, and the contraction runs over 3 x tokens; so are rows that TMA cannot
 // fetch (a stride that is no multiple of 16 bytes, or rows that overlap) copied to aligned ones.
@@ -73,8 +75,7 @@ struct Params {
     Schedule s;
     int64_t tokens;
     int in, out;
-    const uint8_t *exps;
-    int exp_pitch;
+    Ckpt k;
     float *dw;
     int64_t sdw;
     int accumulate;
@@ -341,6 +342,28 @@ __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
     return true;
 }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+// n (1 .. 4) values to o, or added to what is there.
+__device__ __forceinline__ void store4(float *o, float4 v, int n, int accumulate)
+{
+    if (n == 4 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+        float4 *p = reinterpret_cast<float4 *>(o);
+        if (accumulate) {
+            const float4 a = *p;
+            v = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+        }
+        *p = v;
+        return;
+    }
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) o[i] = accumulate ? o[i] + e[i] : e[i];
+}
+
 struct Shared {
     unsigned long long full[kStages];   // codes, exponents and B have arrived (this CTA)
     unsigned long long ready[kStages];  // both CTAs have decoded A (the leader's is used)
@@ -531,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 const bool any = k0 < p.in;
                 const int64_t end = p.s.tok_blocks * kTok;
                 int64_t t = it.first % p.s.tok_blocks * kTok + lane;
-                const uint8_t *src = p.exps + (any ? t * p.exp_pitch + (k0 >> 5) : 0);
+                const uint8_t *src = p.k.exps + (any ? t * p.k.exp_pitch + (k0 >> 5) : 0);
                 for (int64_t b = it.first; b < it.last; ++b) {
                     if (r.wrapped && !wait_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
                         ok = false;
@@ -540,17 +563,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                     const uint32_t dst = exps + r.st * kExpBytes + lane * 4;
                     // tokens past the last, and columns past the last, read as 0 (their codes are 0)
                     const bool in0 = any && t < p.tokens, in1 = any && t + 32 < p.tokens;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in0 ? src : p.exps), "r"(in0 ? 4 : 0)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in0 ? src : p.k.exps), "r"(in0 ? 4 : 0)
                                  : "memory");
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 128),
-                                 "l"(in1 ? src + 32 * p.exp_pitch : p.exps), "r"(in1 ? 4 : 0)
+                                 "l"(in1 ? src + 32 * p.k.exp_pitch : p.k.exps), "r"(in1 ? 4 : 0)
                                  : "memory");
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[r.st])) : "memory");
                     r.next();
                     t += kTok;
-                    if (any) src += kTok * p.exp_pitch;
+                    if (any) src += kTok * p.k.exp_pitch;
                     if (t >= end) {  // the next plane
-                        if (any) src -= end * p.exp_pitch;
+                        if (any) src -= end * p.k.exp_pitch;
                         t -= end;
                     }
                 }
@@ -672,25 +695,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The cut tiles' sums, run by run in order, into dw.
+// The cut tiles' sums, run by run in order, into dw.  A block takes 4 n of a tile, a thread 4 adjacent k of one.
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
     Item it;
     const int64_t cut = blockIdx.x / (kTile / 4);
-    const int n = (int)(blockIdx.x % (kTile / 4)) * 4;
+    const int n = (int)(blockIdx.x % (kTile / 4)) * 4 + (int)(threadIdx.x >> 6), kl = (int)(threadIdx.x & 63) * 4;
     item_of(p.s, p.s.whole + cut, it);
-    const int64_t k = (int64_t)it.tk * kTile + threadIdx.x;
-    if (k >= p.in) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = (int64_t)it.tn * kTile + n + j;
-        if (row >= p.out) return;
-        const float *s = p.parts + (cut * p.s.split * kTile + n + j) * kTile + threadIdx.x;
-        float v = 0.0f;
-        for (int r = 0; r < p.s.split; ++r) v += s[(int64_t)r * kTile * kTile];
-        float *o = p.dw + row * p.sdw + k;
-        *o = p.accumulate ? *o + v : v;
+    const int64_t k = (int64_t)it.tk * kTile + kl, row = (int64_t)it.tn * kTile + n;
+    if (k >= p.in || row >= p.out) return;
+    const float *s = p.parts + (cut * p.s.split * kTile + n) * kTile + kl;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int r = 0; r < p.s.split; ++r) {
+        const float4 a = *reinterpret_cast<const float4 *>(s + (int64_t)r * kTile * kTile);
+        v.x += a.x;
+        v.y += a.y;
+        v.z += a.z;
+        v.w += a.w;
     }
+    store4(p.dw + row * p.sdw + k, v, (int)min((int64_t)4, p.in - k), p.accumulate);
 }
 
 __global__ void __launch_bounds__(256) k_zero(float *dw, int64_t sdw, int in, int out)
@@ -699,37 +723,140 @@ __global__ void __launch_bounds__(256) k_zero(float *dw, int64_t sdw, int in, in
         for (int k = threadIdx.x; k < in; k += 256) dw[n * sdw + k] = 0.0f;
 }
 
-// dy into rows of `pitch` 16-bit values: float32 as three bf16 planes that add up to it exactly (smallest
-// first), 16-bit types as they are.
-template <typename T>
-__global__ void __launch_bounds__(256) k_stage(const T *dy, int64_t sdy, int64_t tokens, int out, int64_t pitch, uint16_t *dst)
+// ---------------------------------------------------------------------------------------------
+// A few tokens and not many columns: tiles of 256 x 256 leave most SMs without one.  A block
+// takes 64 n x 128 k, a lane 4 k of the 8 n of its warp, on the ordinary cores: every type as it is, and the
+// bias's gradient along with it.
+// ---------------------------------------------------------------------------------------------
+constexpr int kFewTokens = 32, kFewN = 64, kFewK = 128;
+// Measured in a graph, this kernel against the tiles: 1024 x 1024 with 1, 16, 32 and 64 tokens 3, 5, 8 and 13.6 us
+// against 12 to 13 us; 4096 x 4096 with 16 tokens 36 against 21 us, with 64 117 against 21 us.
+inline bool few(int64_t tokens, int64_t in, int64_t out)
 {
-    const int per_row = (out + 255) / 256;
-    const int64_t n = tokens * per_row;
-    for (int64_t id = blockIdx.x; id < n; id += gridDim.x) {
-        const int64_t t = id / per_row;
-        const int c = (int)(id - t * per_row) * 256 + threadIdx.x;
-        if (c >= out) continue;
-        if constexpr (sizeof(T) == 2) {
-            dst[t * pitch + c] = (uint16_t)elem_bits(dy[t * sdy + c]);
-        } else {
-            const float v = dy[t * sdy + c];
-            const uint32_t bits = __float_as_uint(v);
-            uint32_t hi = bits >> 16, mid = 0, lo = 0;
-            if ((bits & 0x7f800000u) == 0x7f800000u) {
-                if (bits & 0x007fffffu) hi |= 0x40u;  // a NaN stays one
-            } else {
-                const float r = v - __uint_as_float(bits & 0xffff0000u);
-                const uint32_t m = __float_as_uint(r);
-                mid = m >> 16;
-                lo = __float_as_uint(r - __uint_as_float(m & 0xffff0000u)) >> 16;
+    return tokens <= kFewTokens && tokens * in * out <= int64_t(1) << 26;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_few(const __grid_constant__ Params p, const T *dy, int64_t sdy, float *db)
+{
+    __shared__ float sd[kFewTokens][kFewN];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tiles_k = (p.in + kFewK - 1) / kFewK;
+    const int64_t tn = blockIdx.x / tiles_k;
+    const int k = (int)(blockIdx.x - tn * tiles_k) * kFewK + lane * 4, tokens = (int)p.tokens;
+    const int64_t n0 = tn * kFewN;
+    for (int i = threadIdx.x; i < tokens * kFewN; i += 256) {
+        const int t = i / kFewN, n = i % kFewN;
+        sd[t][n] = n0 + n < p.out ? to_float(dy[t * sdy + n0 + n]) : 0.0f;
+    }
+    __syncthreads();
+    float acc[8][4] = {};
+    const bool in = k < p.k.code_pitch;
+    for (int t0 = 0; t0 < tokens; t0 += 8) {  // eight tokens' codes at once: their latency is most of the time
+        uint32_t q[8], e[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool has = in && t0 + u < tokens;
+            q[u] = has ? __ldg(reinterpret_cast<const uint32_t *>(p.k.codes + (int64_t)(t0 + u) * p.k.code_pitch + k)) : 0u;
+            e[u] = has ? __ldg(p.k.exps + (int64_t)(t0 + u) * p.k.exp_pitch + (k >> 5)) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int t = t0 + u;
+            if (t >= tokens) break;
+            const float scale = group_scale(e[u]);
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] = (float)(int)(int8_t)(q[u] >> (8 * j)) * scale;
+                if constexpr (__is_same(T, __half)) {
+                    x[j] = x[j] > 65504.0f ? 65504.0f : x[j] < -65504.0f ? -65504.0f : x[j];
+                    x[j] = __half2float(__float2half_rn(x[j]));
+                }
             }
-            const int64_t plane = tokens * pitch, at = t * pitch + c;
-            dst[at] = (uint16_t)lo;
-            dst[plane + at] = (uint16_t)mid;
-            dst[2 * plane + at] = (uint16_t)hi;
+            float d[8];
+            *reinterpret_cast<float4 *>(d) = *reinterpret_cast<const float4 *>(&sd[t][warp * 8]);
+            *reinterpret_cast<float4 *>(d + 4) = *reinterpret_cast<const float4 *>(&sd[t][warp * 8 + 4]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(d[i], x[j], acc[i][j]);
         }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + warp * 8 + i;
+        if (n < p.out && k < p.in)
+            store4(p.dw + n * p.sdw + k, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]), min(4, p.in - k), p.accumulate);
+    }
+    if (db && k == lane * 4 && threadIdx.x < kFewN && n0 + threadIdx.x < p.out) {
+        float v = 0.0f;
+        for (int t = 0; t < tokens; ++t) v += sd[t][threadIdx.x];
+        float *o = db + n0 + threadIdx.x;
+        *o = p.accumulate ? *o + v : v;
+    }
+}
+
+// dy into rows of `pitch` 16-bit values: float32 as three bf16 planes that add up to it exactly (smallest
+// first), 16-bit types as they are.  A warp takes 256 columns of a row.
+template <typename T, bool AL>
+__global__ void __launch_bounds__(256) k_stage(const T *dy, int64_t sdy, int64_t tokens, int out, int64_t pitch, uint16_t *dst)
+{
+    const int per_row = (out + kChunk - 1) / kChunk, lane = threadIdx.x & 31;
+    const int64_t n = tokens * per_row, warps = (int64_t)gridDim.x * 8;
+    for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += warps) {
+        const int64_t t = id / per_row;
+        const int base = (int)(id - t * per_row) * kChunk, c = base + lane * 8;
+        const T *row = dy + t * sdy;
+        Raw<T, AL> r;
+        if (inner_chunk<T, AL>(base, out)) chunk_load<T, AL, true>(r, row, base, lane, out);
+        else chunk_load<T, AL, false>(r, row, base, lane, out);
+        const Words<T> w = in_place<T, AL>(r, row);
+        if (c >= pitch) continue;  // pitch and c are multiples of 8
+        uint16_t *o = dst + t * pitch + c;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]);
+        } else {
+            uint32_t part[3][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t bits = w.w[j];
+                uint32_t hi = bits >> 16, mid = 0, lo = 0;
+                if ((bits & 0x7f800000u) == 0x7f800000u) {
+                    if (bits & 0x007fffffu) hi |= 0x40u;  // a NaN stays one
+                } else {
+                    const float rest = __uint_as_float(bits) - __uint_as_float(bits & 0xffff0000u);
+                    const uint32_t m = __float_as_uint(rest);
+                    mid = m >> 16;
+                    lo = __float_as_uint(rest - __uint_as_float(m & 0xffff0000u)) >> 16;
+                }
+                const uint32_t e[3] = {lo, mid, hi};
+#pragma unroll
+                for (int i = 0; i < 3; ++i) part[i][j >> 1] = (j & 1) ? part[i][j >> 1] | e[i] << 16 : e[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<uint4 *>(o + i * tokens * pitch) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_stage(const void *dy, int64_t sdy, int64_t tokens, int64_t out, int64_t pitch, unsigned char *dst, cudaStream_t s)
+{
+    const int64_t need = (tokens * ((out + kChunk - 1) / kChunk) + 7) / 8;
+    const unsigned grid = (unsigned)(need < 148 * 8 ? need : 148 * 8);
+    auto kern = tokens == 1 || sdy % (16 / (int)sizeof(T)) == 0 ? k_stage<T, true> : k_stage<T, false>;
+    kern<<<grid, 256, 0, s>>>(static_cast<const T *>(dy), sdy, tokens, (int)out, pitch, reinterpret_cast<uint16_t *>(dst));
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_few(const Params &p, const WgradArgs &a, cudaStream_t s)
+{
+    const int64_t blocks = ((a.in + kFewK - 1) / kFewK) * ((a.out + kFewN - 1) / kFewN);
+    k_few<T><<<(unsigned)blocks, 256, 0, s>>>(p, static_cast<const T *>(a.dy.p), a.dy.stride, a.db);
+    return cudaGetLastError();
 }
 
 bool staged(int dtype, int64_t tokens, int64_t out, int64_t dy_stride)
@@ -745,7 +872,8 @@ Spaces spaces(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_str
 {
     const Schedule s = schedule(dtype, tokens, in, out);
     Spaces w;
-    w.staged = 0;
+    w.staged = w.parts = w.cols = w.bytes = 0;
+    if (few(tokens, in, out)) return w;
     w.parts = staged(dtype, tokens, out, dy_stride)
                   ? (size_t)(tokens * staged_pitch(out)) * (dtype == GQ_FLOAT32 ? 6 : 2) : 0;
     w.cols = w.parts + (size_t)(s.cut * s.split) * kTile * kTile * sizeof(float);
@@ -803,28 +931,27 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     p.tokens = a.tokens;
     p.in = (int)a.in;
     p.out = (int)a.out;
-    p.exps = static_cast<const uint8_t *>(a.ckpt) + l.exps_off;
-    p.exp_pitch = (int)l.exp_pitch;
+    uint8_t *ck = static_cast<uint8_t *>(const_cast<void *>(a.ckpt));
+    p.k = Ckpt{ck, ck + l.exps_off, (int)l.code_pitch, (int)l.exp_pitch};
     p.dw = a.dw;
     p.sdw = a.dw_stride;
     p.accumulate = a.accumulate;
     p.parts = reinterpret_cast<float *>(a.ws + w.parts);
     p.limit = 4000000000ll;  // two seconds; the longest wait, for a run of stages, is some microseconds
 
+    if (few(a.tokens, a.in, a.out)) {
+        if (a.dtype == GQ_FLOAT32) return launch_few<float>(p, a, stream);
+        if (a.dtype == GQ_BFLOAT16) return launch_few<__nv_bfloat16>(p, a, stream);
+        return launch_few<__half>(p, a, stream);
+    }
+
     const void *dy = a.dy.p;
     int64_t pitch = a.tokens > 1 ? a.dy.stride : staged_pitch(a.out);
     const int planes = a.dtype == GQ_FLOAT32 ? 3 : 1;
     if (staged(a.dtype, a.tokens, a.out, a.dy.stride)) {
         pitch = staged_pitch(a.out);
-        const int64_t need = a.tokens * ((a.out + 255) / 256);
-        const unsigned grid = (unsigned)(need < 148 * 8 ? need : 148 * 8);
-        if (a.dtype == GQ_FLOAT32)
-            k_stage<float><<<grid, 256, 0, stream>>>(static_cast<const float *>(dy), a.dy.stride, a.tokens, (int)a.out, pitch,
-                                                    reinterpret_cast<uint16_t *>(a.ws));
-        else
-            k_stage<__half><<<grid, 256, 0, stream>>>(static_cast<const __half *>(dy), a.dy.stride, a.tokens, (int)a.out,
-                                                     pitch, reinterpret_cast<uint16_t *>(a.ws));
-        e = cudaGetLastError();
+        e = a.dtype == GQ_FLOAT32 ? launch_stage<float>(dy, a.dy.stride, a.tokens, a.out, pitch, a.ws, stream)
+                                  : launch_stage<__half>(dy, a.dy.stride, a.tokens, a.out, pitch, a.ws, stream);
         if (e != cudaSuccess) return e;
         dy = a.ws;
     }

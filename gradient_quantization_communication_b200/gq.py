@@ -264,21 +264,22 @@ def _dtype(t, what):
 
 def _matrix(t, what, dtype=None, shape=None):
     """(pointer, row stride) of a 2-D tensor whose columns are adjacent."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    st = t.stride()
+    if len(st) != 2 or (st[1] != 1 and t.shape[1] > 1):
         raise ValueError("%s: a 2-D tensor with adjacent columns expected, got shape %s, strides %s"
-                         % (what, tuple(t.shape), t.stride()))
+                         % (what, tuple(t.shape), st))
     if dtype is not None and _dtype(t, what) != dtype:
         raise TypeError("%s: its type differs from the other tensors' (%s)" % (what, t.dtype))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s: shape %s expected, got %s" % (what, shape, tuple(t.shape)))
-    return t.data_ptr(), t.stride(0)
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: shape %s expected, got %s" % (what, tuple(shape), tuple(t.shape)))
+    return t.data_ptr(), st[0]
 
 
 def _vector(t, what, n, dtype=GQ_FLOAT32):
     """Pointer of a contiguous vector of n values (None: NULL)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s: a contiguous vector of %d values expected, got shape %s, strides %s"
                          % (what, n, tuple(t.shape), t.stride()))
     if _dtype(t, what) != dtype:
@@ -290,9 +291,8 @@ def _ckpt(t, rows, cols):
     """Pointer of a checkpoint buffer of rows x cols values (None: NULL)."""
     if t is None:
         return None
-    cp, ep = (cols + 31) // 32 * 32, (cols + 127) // 128 * 4
-    need = (rows * cp + 15) // 16 * 16 + (rows * ep + 15) // 16 * 16
-    if t.element_size() != 1 or t.dim() != 1 or t.shape[0] < need or (t.shape[0] > 1 and t.stride(0) != 1):
+    need = (rows * ((cols + 31) // 32 * 32) + 15) // 16 * 16 + (rows * ((cols + 127) // 128 * 4) + 15) // 16 * 16
+    if t.element_size() != 1 or t.dim() != 1 or t.shape[0] < need or not t.is_contiguous():
         raise ValueError("ckpt: a contiguous uint8 vector of at least %d bytes expected, got %s of shape %s"
                          % (need, t.dtype, tuple(t.shape)))
     return t.data_ptr()
@@ -301,16 +301,11 @@ def _ckpt(t, rows, cols):
 def _launch(fn, what, stream, tensors, *args):
     """Call fn(*args, stream) on the tensors' device; the stream defaults to that device's current one."""
     import torch
-    dev = None
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("%s: CUDA tensors expected, got one on %s" % (what, t.device))
-        if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
-            raise ValueError("%s: tensors on different devices" % what)
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("%s: CUDA tensors of one device expected, got %s"
+                             % (what, ", ".join(str(x.device) for x in tensors if x is not None)))
     if stream is None:
         stream = torch.cuda.current_stream(dev).cuda_stream
     elif not isinstance(stream, int):
