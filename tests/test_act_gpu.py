@@ -328,6 +328,35 @@ def test_weight_grad_sizes_of_values(dtype):
         assert ((gdw.cpu().double() - dw).abs() <= _wgrad_tol(90, size) + 90 * 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens", [255, 25])
+def test_weight_grad_decodes_every_code_and_exponent(dtype, tokens):
+    """Token t holds every code under exponent byte E and dy is 1 at (t, t) and 0 elsewhere, so row t of dw
+    is the decoded row, exactly; with all 255 finite exponents, and with some of them a few tokens at a time."""
+    for lo in range(0, 255, tokens):
+        n = min(tokens, 255 - lo)
+        exps = np.repeat(np.arange(lo, lo + n, dtype=np.uint8)[:, None], 8, 1)
+        codes = np.tile(np.arange(-128, 128).astype(np.int8), (n, 1))
+        # -128 * 2^121 is -2^128, beyond binary32: no number, and no code that a pack writes
+        codes[exps[:, 0] == 254, 0] = -127
+        want = A.as_type(A.decode(codes, exps, 256), dtype if dtype == torch.float16 else torch.float32).float()
+        dw = torch.empty(n, 256, device="cuda")
+        G.gq_act_weight_grad(torch.from_numpy(A.to_buffer(codes, exps)).cuda(), torch.eye(n, dtype=dtype, device="cuda"), dw)
+        assert torch.equal(dw.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,cin,cout", [(32, 40, 70), (33, 40, 70), (32, 2048, 1024), (32, 2048, 1025), (8, 1000, 8389),
+                                             (64, 256, 256), (65, 257, 255)])
+def test_weight_grad_around_the_choice_of_kernel(dtype, tokens, cin, cout):
+    x, dy = _values(tokens, cin, dtype, 3), _values(tokens, cout, dtype, 4, 0.1)
+    ck, dw, size, db, dsize = _wgrad_want(x, dy)
+    gdw, gdb = torch.empty(cout, cin, device="cuda"), torch.empty(cout, device="cuda")
+    G.gq_act_weight_grad(ck, dy.cuda(), gdw, gdb)
+    assert ((gdw.cpu().double() - dw).abs() <= _wgrad_tol(tokens, size)).all()
+    assert ((gdb.cpu().double() - db).abs() <= (tokens + 16) * 2.0 ** -24 * dsize + 1e-37).all()
+
+
 def test_weight_grad_against_differences():
     """dw against differences of the loss sum(dy * (xh W^T)), which is linear in W: exact up to rounding."""
     x, dy = _values(30, 40, torch.bfloat16, 12), _values(30, 8, torch.bfloat16, 13)
