@@ -353,29 +353,41 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
         }
     }
     if (!p.part_b) return;
-    // the slots' sums, slot by slot in order (slots > 1: in shared memory behind gamma)
+    // the slots' sums, slot by slot in order (slots > 1: in shared memory behind gamma, chunks of 256 columns as
+    // gamma's, so that 8 lanes use all banks)
     float *fold = gamma + NC * G * kChunk;
     for (int t = 0; t < p.slots; ++t) {
         if (slot == t) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c) {
+                const int base = (wslot + c * G) * kChunk, col = base + lane * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int col = (wslot + c * G) * kChunk + lane * 8 + j;
-                    if (col >= p.cols) continue;
-                    float a = sg[c][j], b = sb[c][j];
+                for (int k = 0; k < 2; ++k) {  // dgamma, dbeta
+                    float(&a)[8] = k ? sb[c] : sg[c];
+                    float *f = fold + k * NC * G * kChunk;
                     if (t > 0) {
-                        a += fold[col];
-                        b += fold[p.cols + col];
+                        float old[8];
+                        params_shared(old, f, base, lane);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) a[j] += old[j];
                     }
                     if (t + 1 < p.slots) {
-                        fold[col] = a;
-                        fold[p.cols + col] = b;
+                        float4 *d = reinterpret_cast<float4 *>(f + base) + lane;
+                        d[0] = make_float4(a[0], a[1], a[2], a[3]);
+                        d[32] = make_float4(a[4], a[5], a[6], a[7]);
+                        continue;
+                    }
+                    float *o = (k ? p.part_b : p.part_g) + (int64_t)blockIdx.x * p.cols + col;
+                    if (p.cols % 4 == 0 && col + 8 <= p.cols) {
+                        reinterpret_cast<float4 *>(o)[0] = make_float4(a[0], a[1], a[2], a[3]);
+                        reinterpret_cast<float4 *>(o)[1] = make_float4(a[4], a[5], a[6], a[7]);
                     } else {
-                        p.part_g[(int64_t)blockIdx.x * p.cols + col] = a;
-                        p.part_b[(int64_t)blockIdx.x * p.cols + col] = b;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (col + j < p.cols) o[j] = a[j];
                     }
                 }
+            }
         }
         if (p.slots > 1) __syncthreads();
     }
@@ -534,26 +546,38 @@ __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
     }
 }
 
-// Column sums of the partial rows, in a fixed order: 8 warps take 8 interleaved sets of rows of 32
-// columns, and their sums are added in warp order.
-__global__ void __launch_bounds__(256) k_parts_reduce(const float *part0, const float *part1, int64_t parts, int cols,
+// Column sums of the partial rows, in a fixed order: 16 warps take 16 interleaved sets of rows of 32 columns,
+// eight loads at a time, and their sums are added in warp order.  It is launched to start as the kernel before
+// it drains, and waits here for its rows.
+__global__ void __launch_bounds__(512) k_parts_reduce(const float *part0, const float *part1, int64_t parts, int cols,
                                                       float *out0, float *out1, int accumulate)
 {
-    __shared__ float s[8][33];
+    cudaGridDependencySynchronize();
+    __shared__ float s[16][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float *part = blockIdx.y ? part1 : part0;
     float *out = blockIdx.y ? out1 : out0;
     if (!out) return;
     const int c = (int)blockIdx.x * 32 + lane;
     float v = 0.0f;
-    if (c < cols)
-        for (int64_t q = warp; q < parts; q += 8) v += part[q * cols + c];
+    if (c < cols) {
+        const float *p = part + c;
+        int64_t q = warp;
+        for (; q + 7 * 16 < parts; q += 8 * 16) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = p[(q + u * 16) * cols];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += x[u];
+        }
+        for (; q < parts; q += 16) v += p[q * cols];
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < cols) {
         v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += s[i][lane];
+        for (int i = 0; i < 16; ++i) v += s[i][lane];
         out[c] = accumulate ? out[c] + v : v;
     }
 }
@@ -628,7 +652,7 @@ cudaError_t backward_reg(const Params &p, bool al, cudaStream_t s)
 {
     auto kern = al ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
                     : (p.x ? k_backward<T, false, NC, false> : k_backward<T, false, NC, true>);
-    const size_t smem = ((size_t)NC * p.G * kChunk + (p.slots > 1 ? (size_t)p.cols * 2 : 0)) * sizeof(float);
+    const size_t smem = (size_t)NC * p.G * kChunk * (p.slots > 1 ? 3 : 1) * sizeof(float);
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), p.G * p.slots * 32, smem, &per_sm, &sms);
     if (e != cudaSuccess) return e;
@@ -738,9 +762,16 @@ cudaError_t launch_colsum(int dtype, int64_t rows, int64_t cols, Mat dy, float *
 cudaError_t launch_parts_reduce(const float *part0, const float *part1, int64_t parts, int64_t cols, float *out0,
                                 float *out1, int accumulate, cudaStream_t stream)
 {
-    k_parts_reduce<<<dim3((unsigned)((cols + 31) / 32), out1 ? 2u : 1u), 256, 0, stream>>>(part0, part1, parts, (int)cols,
-                                                                                        out0, out1, accumulate);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((cols + 31) / 32), out1 ? 2u : 1u);
+    cfg.blockDim = dim3(512);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_parts_reduce, part0, part1, parts, (int)cols, out0, out1, accumulate);
 }
 
 }  // namespace gq

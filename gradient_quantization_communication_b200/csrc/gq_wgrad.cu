@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
 // The cut tiles' sums, run by run in order, into dw.  A block takes 4 n of a tile, a thread 4 adjacent k of one.
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
+    cudaGridDependencySynchronize();  // launched to start as k_wgrad drains
     Item it;
     const int64_t cut = blockIdx.x / (kTile / 4);
     const int n = (int)(blockIdx.x % (kTile / 4)) * 4 + (int)(threadIdx.x >> 6), kl = (int)(threadIdx.x & 63) * 4;
@@ -1000,8 +1001,12 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return e;
     if (p.s.cut) {
-        k_join<<<(unsigned)(p.s.cut * (kTile / 4)), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
+        cfg.gridDim = dim3((unsigned)(p.s.cut * (kTile / 4)));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        e = cudaLaunchKernelEx(&cfg, k_join, p);
         if (e != cudaSuccess) return e;
     }
     if (!a.db) return cudaSuccess;
