@@ -725,9 +725,9 @@ int64_t norm_parts(int64_t rows, int64_t cols)
 
 int64_t colsum_parts(int64_t rows, int64_t cols)
 {
-    // enough parts for two blocks an SM, of at least 8 rows each (the partial rows stay few bytes)
+    // parts of 8 rows, which a warp loads at once, up to eight blocks an SM: waiting for them is most of the time
     const int64_t across = (cols + 4 * kChunk - 1) / (4 * kChunk);
-    int64_t n = (296 + across - 1) / across;
+    int64_t n = (8 * 148 + across - 1) / across;
     if (n > (rows + 7) / 8) n = (rows + 7) / 8;
     return n;
 }

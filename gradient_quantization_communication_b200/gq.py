@@ -363,13 +363,20 @@ def gq_act_unpack(ckpt, x, stream=None):
             _ckpt(ckpt, rows, cols), px, sx)
 
 
+def _kind(kind):
+    k = FUNCTIONS.get(kind, kind)
+    if not isinstance(k, int):
+        raise ValueError("kind: one of %s expected, got %r" % (sorted(FUNCTIONS), kind))
+    return k
+
+
 def gq_act_fn_forward(kind, x, y, ckpt=None, stream=None):
     """kind: "gelu", "gelu_tanh", "silu" or the C constant."""
     dt = _dtype(x, "x")
     rows, cols = x.shape
     px, sx = _matrix(x, "x")
     py, sy = _matrix(y, "y", dt, (rows, cols))
-    _launch(lib().gq_act_fn_forward, "gq_act_fn_forward", stream, (x, y, ckpt), FUNCTIONS.get(kind, kind), dt, rows, cols,
+    _launch(lib().gq_act_fn_forward, "gq_act_fn_forward", stream, (x, y, ckpt), _kind(kind), dt, rows, cols,
             px, sx, py, sy, _ckpt(ckpt, rows, cols))
 
 
@@ -378,7 +385,7 @@ def gq_act_fn_backward(kind, ckpt, dy, dx, stream=None):
     rows, cols = dy.shape
     pdy, sdy = _matrix(dy, "dy")
     pdx, sdx = _matrix(dx, "dx", dt, (rows, cols))
-    _launch(lib().gq_act_fn_backward, "gq_act_fn_backward", stream, (dy, dx, ckpt), FUNCTIONS.get(kind, kind), dt, rows,
+    _launch(lib().gq_act_fn_backward, "gq_act_fn_backward", stream, (dy, dx, ckpt), _kind(kind), dt, rows,
             cols, _ckpt(ckpt, rows, cols), pdy, sdy, pdx, sdx)
 
 

@@ -356,7 +356,8 @@ GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, vo
  *
  * Conventions, besides those above:
  *   - Stateless: no plan, no status word, no allocation.  Calls that may overlap on the GPU (other
- *     streams, other captured graphs) need outputs and workspaces of their own.
+ *     streams, other captured graphs) need outputs and workspaces of their own.  The first call of a
+ *     kind in a process loads its kernels: make it before any stream capture.
  *   - A matrix is rows of cols elements of type `dtype`, its rows `stride` elements apart; a column
  *     step other than 1 is not supported.  Rows of an input may repeat (stride 0) or overlap; those
  *     of an output may not (stride >= cols).  With one row the stride is not used.  Rows that start
@@ -369,6 +370,8 @@ GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, vo
  *     wider buffer with the same stride do not share any.
  *   - Non-finite values pass through as in the formulas; a group with one in a checkpoint reads as
  *     NaN throughout.  Sums are binary32 and their order is fixed: equal calls give equal bits.
+ *   - Should a kernel's bounded wait give up (a fault: no wait is expected to last a second), the
+ *     outputs it was computing are NaN; there is no status word to ask.
  */
 #define GQ_ACT_MAX_COLS (1 << 24)
 

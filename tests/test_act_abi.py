@@ -140,6 +140,8 @@ def test_binding_refuses_types_and_shapes():
         (TypeError, lambda: G.gq_act_fn_forward("gelu", x, x.half())),
         (ValueError, lambda: G.gq_act_fn_forward("gelu", x, torch.zeros(4, 41))),
         (ValueError, lambda: G.gq_act_fn_backward("gelu", _u8(8), x, x.clone())),
+        (ValueError, lambda: G.gq_act_fn_forward("relu", x, x.clone())),
+        (ValueError, lambda: G.gq_act_fn_backward("relu", ck, x, x.clone())),
         (ValueError, lambda: G.gq_act_weight_grad(ck, x, torch.zeros(39, 40))),
         (TypeError, lambda: G.gq_act_weight_grad(ck, x, torch.zeros(40, 40).bfloat16())),
         (ValueError, lambda: G.gq_act_weight_grad(ck, x, torch.zeros(40, 40), torch.zeros(39))),
