@@ -60,14 +60,19 @@ static_assert(kCtlWarps * kRegsCtl + kEpiWarps * kRegsEpi + kConvWarps * kRegsCo
               "setmaxnreg: the shares come from the block's own registers at launch");
 constexpr int kPairs = 74;               // CTA pairs of the 148 SMs: the schedule is made for these
 
-// How the tiles are spread over the pairs: whole rounds first, and the tiles of the last, partial round
-// each cut into `split` runs of tokens, whose partial sums meet in the workspace.
+// How the tiles are spread over the pairs: whole rounds of a tile a pair first; the stages of the last, partial
+// round's tiles are one line, tile after tile, cut into `ranges` equal ranges, one a pair.  A range's part of a
+// tile goes to the workspace, where a second kernel joins them, unless it is the whole tile.
 struct Schedule {
     int tiles_k, tiles_n;
-    int64_t whole, cut;  // tiles done by one pair; tiles cut
-    int split;
-    int64_t blocks;      // stages of a whole tile: planes x ceil(tokens / 64)
+    int64_t whole, cut;  // tiles of the whole rounds; tiles of the last
+    int pairs, ranges;   // pairs launched; of them, those with a range
+    int64_t blocks;      // stages of a tile: planes x ceil(tokens / 64)
     int64_t tok_blocks;  // ceil(tokens / 64)
+    // from here on worked out before the launch: divisions of 64 bits in every thread took 5 us a call
+    int64_t start[kPairs + 1];               // each range's first stage, counted from the first cut tile's first
+    uint8_t tile[kPairs];                    // the cut tile that it lies in
+    uint8_t from[kPairs], to[kPairs];        // the ranges of each cut tile's first and last stage
 };
 
 struct Params {
@@ -92,17 +97,39 @@ Schedule schedule(int dtype, int64_t tokens, int64_t in, int64_t out)
     s.blocks = s.tok_blocks * (dtype == GQ_FLOAT32 ? 3 : 1);
     const int64_t tiles = (int64_t)s.tiles_k * s.tiles_n;
     s.cut = tiles % kPairs;
-    s.split = 1;
-    if (s.cut) {
-        int64_t most = kPairs / s.cut;
-        const int64_t by_len = s.blocks / 8;
-        if (most > by_len) most = by_len;
-        s.split = most < 1 ? 1 : (int)most;
-    }
-    if (s.split == 1) s.cut = 0;
     s.whole = tiles - s.cut;
+    s.ranges = (int)s.cut;
+    if (s.cut) {
+        // A tile a pair, as many equal parts of every tile as there are pairs for, or equal ranges for all pairs.
+        // A partial tile, written and read again, costs the others' stages about 0.3 of one; the second kernel
+        // ten; ranges under 8 stages do not pay.
+        const int64_t total = s.cut * s.blocks, most = total / 8 < kPairs ? total / 8 : kPairs;
+        double best = (double)s.blocks;
+        for (int64_t r = 2 * s.cut; r < most + s.cut; r += s.cut) {
+            if (r > most) r = most;
+            if (r <= s.cut) break;
+            const double parts = r % s.cut == 0 ? (double)r : (double)(s.cut + r - 1);
+            const double cost = (double)((total + r - 1) / r) + 0.3 * parts + 10.0;
+            if (cost < best) {
+                best = cost;
+                s.ranges = (int)r;
+            }
+            if (r == most) break;
+        }
+    }
+    s.pairs = s.whole ? kPairs : s.ranges;
+    for (int p = 0; p <= s.ranges; ++p) s.start[p] = s.ranges ? s.cut * s.blocks * p / s.ranges : 0;
+    for (int p = 0; p < s.ranges; ++p) s.tile[p] = (uint8_t)(s.start[p] / s.blocks);
+    for (int c = 0, p = 0; c < s.cut; ++c) {
+        while (s.start[p + 1] <= c * s.blocks) ++p;
+        s.from[c] = (uint8_t)p;
+        while (s.start[p + 1] < (c + 1) * s.blocks) ++p;
+        s.to[c] = (uint8_t)p;
+    }
     return s;
 }
+// Partial tiles that the workspace holds: range p's part of tile c at c + p.
+int64_t part_tiles(const Schedule &s) { return s.ranges > s.cut ? s.cut + s.ranges - 1 : 0; }
 
 // ---------------------------------------------------------------------------------------------
 // PTX
@@ -306,13 +333,24 @@ __device__ __forceinline__ void decode16_any(const uint4 &codes, uint32_t E, uin
 }
 
 // ---------------------------------------------------------------------------------------------
-// The kernel: one CTA pair per SM pair, walking work items (whole tiles, then runs of cut tiles).
+// The kernel: one CTA pair per SM pair, walking work items (whole tiles, then the parts of its range).
 // ---------------------------------------------------------------------------------------------
 struct Item {
     int tk, tn;              // tile
     int64_t first, last;     // its stages
     int64_t part;            // partial tile in the workspace, -1: the whole tile
 };
+
+// Bands of 8 k tiles, walked along n: pairs that run together share their operands in L2.
+__device__ __forceinline__ void tile_place(const Schedule &s, int64_t tile, Item &it)
+{
+    const int64_t band = (int64_t)8 * s.tiles_n;
+    const int64_t g = tile / band;
+    const int rest = (int)(tile - g * band);
+    const int wide = min(8, s.tiles_k - (int)g * 8);
+    it.tn = rest / wide;
+    it.tk = (int)g * 8 + rest - it.tn * wide;
+}
 
 __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
 {
@@ -323,22 +361,18 @@ __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
         it.last = s.blocks;
         it.part = -1;
     } else {
-        const int64_t c = i - s.whole;
-        if (c >= s.cut * s.split) return false;
-        // run r of cut tile c % cut
-        const int64_t r = c / s.cut;
-        tile = s.whole + (c - r * s.cut);
-        it.first = s.blocks * r / s.split;
-        it.last = s.blocks * (r + 1) / s.split;
-        it.part = (tile - s.whole) * s.split + r;
+        // part m of pair p's range, which lies in the m-th tile that the range touches
+        const uint32_t j = (uint32_t)(i - s.whole), m = j / (uint32_t)s.pairs, p = j - m * (uint32_t)s.pairs;
+        if (p >= (uint32_t)s.ranges) return false;
+        const int64_t lo = s.start[p], hi = s.start[p + 1];
+        const int64_t c = s.tile[p] + m, at = c * s.blocks;
+        it.first = (lo > at ? lo : at) - at;
+        it.last = (hi < at + s.blocks ? hi : at + s.blocks) - at;
+        if (it.first >= it.last) return false;
+        it.part = it.first == 0 && it.last == s.blocks ? -1 : c + p;
+        tile = s.whole + c;
     }
-    // bands of 8 k tiles, walked along n: pairs that run together share their operands in L2
-    const int64_t band = (int64_t)8 * s.tiles_n;
-    const int64_t g = tile / band;
-    const int rest = (int)(tile - g * band);
-    const int wide = min(8, s.tiles_k - (int)g * 8);
-    it.tn = rest / wide;
-    it.tk = (int)g * 8 + rest - it.tn * wide;
+    tile_place(s, tile, it);
     return true;
 }
 
@@ -442,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     const uint32_t exps = stages + kStages * kStageBytes;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int64_t pair = blockIdx.x >> 1, pairs = p.s.pairs;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -695,20 +729,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The cut tiles' sums, run by run in order, into dw.  A block takes 4 n of a tile, a thread 4 adjacent k of one.
+// The cut tiles' sums, range by range in order, into dw.  A block takes 4 n of a tile, a thread 4 adjacent k of one.
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
     cudaGridDependencySynchronize();  // launched to start as k_wgrad drains
-    Item it;
-    const int64_t cut = blockIdx.x / (kTile / 4);
+    const int64_t c = blockIdx.x / (kTile / 4);
     const int n = (int)(blockIdx.x % (kTile / 4)) * 4 + (int)(threadIdx.x >> 6), kl = (int)(threadIdx.x & 63) * 4;
-    item_of(p.s, p.s.whole + cut, it);
+    const int lo = p.s.from[c], hi = p.s.to[c];
+    if (lo == hi) return;  // one range has the whole tile, and has stored it
+    Item it;
+    tile_place(p.s, p.s.whole + c, it);
     const int64_t k = (int64_t)it.tk * kTile + kl, row = (int64_t)it.tn * kTile + n;
     if (k >= p.in || row >= p.out) return;
-    const float *s = p.parts + (cut * p.s.split * kTile + n) * kTile + kl;
+    const float *s = p.parts + ((c + lo) * kTile + n) * kTile + kl;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int r = 0; r < p.s.split; ++r) {
+    for (int r = 0; r <= hi - lo; ++r) {
         const float4 a = *reinterpret_cast<const float4 *>(s + (int64_t)r * kTile * kTile);
         v.x += a.x;
         v.y += a.y;
@@ -871,13 +907,13 @@ struct Spaces {
 };
 Spaces spaces(int dtype, int64_t tokens, int64_t in, int64_t out, int64_t dy_stride, bool bias)
 {
-    const Schedule s = schedule(dtype, tokens, in, out);
     Spaces w;
     w.staged = w.parts = w.cols = w.bytes = 0;
-    if (few(tokens, in, out)) return w;
+    if (few(tokens, in, out)) return w;  // no tokens among them
+    const Schedule s = schedule(dtype, tokens, in, out);
     w.parts = staged(dtype, tokens, out, dy_stride)
                   ? (size_t)(tokens * staged_pitch(out)) * (dtype == GQ_FLOAT32 ? 6 : 2) : 0;
-    w.cols = w.parts + (size_t)(s.cut * s.split) * kTile * kTile * sizeof(float);
+    w.cols = w.parts + (size_t)part_tiles(s) * kTile * kTile * sizeof(float);
     w.bytes = w.cols + (bias ? (size_t)(colsum_parts(tokens, out) * out) * sizeof(float) : 0);
     return w;
 }
@@ -928,7 +964,6 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     cudaError_t e = cudaSuccess;
 
     Params p;
-    p.s = schedule(a.dtype, a.tokens, a.in, a.out);
     p.tokens = a.tokens;
     p.in = (int)a.in;
     p.out = (int)a.out;
@@ -946,6 +981,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
         return launch_few<__half>(p, a, stream);
     }
 
+    p.s = schedule(a.dtype, a.tokens, a.in, a.out);
     const void *dy = a.dy.p;
     int64_t pitch = a.tokens > 1 ? a.dy.stride : staged_pitch(a.out);
     const int planes = a.dtype == GQ_FLOAT32 ? 3 : 1;
@@ -984,10 +1020,8 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     static const int regs[2] = {num_regs(k_wgrad<false>), num_regs(k_wgrad<true>)};
     if (regs[0] < kRegsLaunch || regs[1] < kRegsLaunch) return cudaErrorInvalidKernelImage;  // setmaxnreg would wait
-    const int64_t items = p.s.whole + p.s.cut * p.s.split;
-    const int64_t pairs = items < kPairs ? items : kPairs;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.gridDim = dim3((unsigned)(2 * p.s.pairs));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
@@ -1000,7 +1034,7 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return e;
-    if (p.s.cut) {
+    if (part_tiles(p.s)) {
         cfg.gridDim = dim3((unsigned)(p.s.cut * (kTile / 4)));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;

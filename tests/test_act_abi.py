@@ -31,6 +31,25 @@ def test_sizes_refused(rows, cols):
     assert G.lib().gq_act_weight_grad_workspace(BF16, rows, 8, cols, 8, 1, ctypes.byref(b)) == G.GQ_ERR_INVALID
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("tokens", [0, 1, 32, 33, 64, 65, 4096, 100000, 2 ** 31 - 1])
+@pytest.mark.parametrize("cin,cout", [(1, 1), (256, 256), (257, 8), (1000, 2499), (4096, 16384), (1 << 24, 1 << 24)])
+def test_weight_grad_workspace(dtype, tokens, cin, cout):
+    """The workspace's size is worked out for every size, never negative, larger by the bias's partial rows
+    with a bias, and 0 without tokens."""
+    sizes = []
+    for bias in (0, 1):
+        b = ctypes.c_size_t(123)
+        assert G.lib().gq_act_weight_grad_workspace(dtype, tokens, cin, cout, (cout + 7) // 8 * 8, bias,
+                                                    ctypes.byref(b)) == G.GQ_OK
+        sizes.append(b.value)
+    assert 0 <= sizes[0] <= sizes[1] < 1 << 62
+    if tokens == 0:
+        assert sizes == [0, 0]
+    if dtype == F32 and tokens > 32:   # three bf16 planes of dy
+        assert sizes[0] >= 6 * tokens * cout
+
+
 CALLS = {
     # name: (arguments in order, keyword -> position of each)
     "gq_act_pack": dict(dtype=BF16, rows=4, cols=40, x=P, x_stride=40, ckpt=P + FAR, stream=None),
