@@ -291,24 +291,24 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-__device__ __forceinline__ uint2 group_codes(const float (&v)[8], uint32_t E)
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float inv)
 {
-    float w[8], inv = __uint_as_float((260u - E) << 23);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = v[j];
-    if (E - 6u > 247u) {
-        // The scale leaves binary32's range (E < 6: in two steps), a code may pass 127 (E = 254), or the group
-        // has no codes (E = 255: all 0; the bounds swallow NaN).
-        const float bound = E < 6u ? __uint_as_float(0x7f800000u) : E == 254u ? 127.0f * 0x1p121f : 0.0f;
-        const float pre = E < 6u ? 0x1p64f : 1.0f;
-        inv = E < 6u ? __uint_as_float((196u - E) << 23) : 0x1p-121f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(fminf(fmaxf(v[j], -bound), bound), pre);
-    }
     uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = group_code(w[j], inv);
+    for (int j = 0; j < 8; ++j) q[j] = group_code(v[j], inv);
     return make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+}
+__device__ __forceinline__ uint2 group_codes(const float (&v)[8], uint32_t E)
+{
+    if (E - 6u <= 247u) return codes_of(v, __uint_as_float((260u - E) << 23));
+    // The scale leaves binary32's range (E < 6: in two steps), a code may pass 127 (E = 254), or the group has
+    // no codes (E = 255: all 0; the bounds swallow NaN).
+    const float bound = E < 6u ? __uint_as_float(0x7f800000u) : E == 254u ? 127.0f * 0x1p121f : 0.0f;
+    const float pre = E < 6u ? 0x1p64f : 1.0f;
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(fminf(fmaxf(v[j], -bound), bound), pre);
+    return codes_of(w, E < 6u ? __uint_as_float((196u - E) << 23) : 0x1p-121f);
 }
 
 // E of the group that a lane's 8 elements belong to (4 lanes hold it); every lane of the warp calls it.

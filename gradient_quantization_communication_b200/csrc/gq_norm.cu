@@ -7,6 +7,8 @@
 //   backward  xh = (x - mean) rstd, g = dy gamma;
 //             dx = rstd (g - sum g / C - xh sum(g xh) / C);
 //             dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy.
+// Measured at 16384 x 4096 bf16, of 6554 GB/s: forward 63 us (65 %), with the checkpoint 89 us (58 %), backward
+// from the input 81 us (76 %), from the checkpoint 81 us (64 %).
 // Sums are binary32.  The squares are summed around the mean, not as sum x^2 - (sum x)^2 / C, which
 // cancels for rows whose mean is large against their spread.
 #include "gq_act.cuh"
@@ -154,9 +156,13 @@ __device__ __forceinline__ void slot_sync(int slot, int G)
     asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
 }
 
-template <typename T, bool AL, int NC, bool KEEP>
+// How the rows lie: anywhere; from 16-byte boundaries; so, and all of a warp's chunks are whole.
+enum Rows { kAnywhere, kAligned, kWhole };
+
+template <typename T, int ROWS, int NC, bool KEEP>
 __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params p)
 {
+    constexpr bool AL = ROWS != kAnywhere;
     extern __shared__ float4 shared_params[];
     __shared__ float4 buf[2][16];
     const int lane = threadIdx.x & 31, G = p.G;
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
     const int64_t step = (int64_t)gridDim.x * p.slots;
     int64_t row = (int64_t)blockIdx.x * p.slots + slot;
     Raw<T, AL> next[NC];
-    auto inner = [&](int c) { return inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
+    auto inner = [&](int c) { return ROWS == kWhole || inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int c0 = (wslot + c * G) * kChunk;
-            if (c0 + kChunk <= p.cols) {
+            if (ROWS == kWhole || c0 + kChunk <= p.cols) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float d = v[c][j] - wmean;
@@ -258,9 +264,10 @@ __global__ void __launch_bounds__(512) k_forward(const __grid_constant__ Params 
 }
 
 // dx, and the block's partial sums of dgamma and dbeta (part_g, part_b: one row a block).
-template <typename T, bool AL, int NC, bool FROM_CKPT>
+template <typename T, int ROWS, int NC, bool FROM_CKPT>
 __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params p)
 {
+    constexpr bool AL = ROWS != kAnywhere;
     extern __shared__ float4 shared_params[];
     __shared__ float2 buf[2][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.G;
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(512) k_backward(const __grid_constant__ Params
     Raw<T, AL> ndy[NC], nx[FROM_CKPT ? 1 : NC];
     RawCkpt nk[FROM_CKPT ? NC : 1];
     float nmean = 0.0f, nrstd = 0.0f;
-    auto inner = [&](int c) { return inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
+    auto inner = [&](int c) { return ROWS == kWhole || inner_chunk<T, AL>((wslot + c * G) * kChunk, p.cols); };
     auto fetch = [&](int64_t r) {
         nmean = __ldg(p.mean + r);
         nrstd = __ldg(p.rstd + r);
@@ -613,8 +620,10 @@ bool rows_aligned(int64_t rows, const Mat &m, int per16) { return !m.p || rows =
 template <typename T, int NC>
 cudaError_t forward_reg(const Params &p, bool al, cudaStream_t s)
 {
-    auto kern = al ? (p.k.codes ? k_forward<T, true, NC, true> : k_forward<T, true, NC, false>)
-                    : (p.k.codes ? k_forward<T, false, NC, true> : k_forward<T, false, NC, false>);
+    const bool whole = al && p.cols == NC * p.G * kChunk;
+    auto kern = whole ? (p.k.codes ? k_forward<T, kWhole, NC, true> : k_forward<T, kWhole, NC, false>)
+                : al  ? (p.k.codes ? k_forward<T, kAligned, NC, true> : k_forward<T, kAligned, NC, false>)
+                      : (p.k.codes ? k_forward<T, kAnywhere, NC, true> : k_forward<T, kAnywhere, NC, false>);
     const int threads = p.G * p.slots * 32;
     const size_t smem = (size_t)NC * p.G * kChunk * 2 * sizeof(float);
     int per_sm = 0, sms = 0;
@@ -650,8 +659,10 @@ cudaError_t forward(const NormArgs &a, cudaStream_t s)
 template <typename T, int NC>
 cudaError_t backward_reg(const Params &p, bool al, cudaStream_t s)
 {
-    auto kern = al ? (p.x ? k_backward<T, true, NC, false> : k_backward<T, true, NC, true>)
-                    : (p.x ? k_backward<T, false, NC, false> : k_backward<T, false, NC, true>);
+    const bool whole = al && p.cols == NC * p.G * kChunk;
+    auto kern = whole ? (p.x ? k_backward<T, kWhole, NC, false> : k_backward<T, kWhole, NC, true>)
+                : al  ? (p.x ? k_backward<T, kAligned, NC, false> : k_backward<T, kAligned, NC, true>)
+                      : (p.x ? k_backward<T, kAnywhere, NC, false> : k_backward<T, kAnywhere, NC, true>);
     const size_t smem = (size_t)NC * p.G * kChunk * (p.slots > 1 ? 3 : 1) * sizeof(float);
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), p.G * p.slots * 32, smem, &per_sm, &sms);

@@ -10,13 +10,15 @@
 //   B  256 n: dy as it is, 128 n in each CTA.
 // Decoding is exact (q * 2^e has 7 significant bits), so the products are too, and rounding happens in
 // the binary32 sums only.  A is the decoded operand because the M side holds 128 columns a CTA however
-// wide the tile is: a stage's 64 x 128 codes cost about 180 issue slots of each scheduler, under the
-// 512 cycles or so that its four MMAs take.
+// wide the tile is: a stage's 64 x 128 codes cost some 250 issue slots of each scheduler, under the 512
+// cycles that its four MMAs take.
 //
 // Bounded for long batches by shared memory, through which 80 KB a stage pass in each CTA: B and the codes in
 // (24), the codes out (8), A in (16), the MMAs' operands out (32); at 128 bytes a cycle 640 cycles, where the
 // MMAs take 512 and a stage some 700.  Fetching the codes into registers instead leaves 64 KB, but the signal
 // that A is decoded then waits for the loads ahead (twice the time).  For few tokens bounded by the bytes of dw.
+// Measured, bf16: 8192 tokens, 4096 x 4096 223 us (1.23 PFLOP/s); 16384 tokens, 4096 x 16384 1.73 ms (1.27, 78 % of
+// the library's measured peak), 2.0 ms under a sustained power cap; 64 tokens, 4096 x 4096 21 us.
 //
 // A few tokens of a small layer go to a kernel of their own, k_few.
 //

@@ -248,14 +248,23 @@ def gq_elias_unpack(cfg, emsg, msg, stream=None):
 # ---------------------------------------------------------------------------------------------
 # activations kept in 8 bits: these take tensors, whose sizes, strides and types are the arguments
 # ---------------------------------------------------------------------------------------------
-_dtypes = None
+_torch = _dtypes = _current_stream = None
+
+
+def _setup():
+    """torch, looked up once: it is imported by the first call that takes tensors."""
+    global _torch, _dtypes, _current_stream
+    import torch
+    _dtypes = {torch.float32: GQ_FLOAT32, torch.bfloat16: GQ_BFLOAT16, torch.float16: GQ_FLOAT16}
+    # the handle itself where torch offers it: building a Stream object around it takes a microsecond
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _torch = torch
 
 
 def _dtype(t, what):
-    global _dtypes
     if _dtypes is None:
-        import torch
-        _dtypes = {torch.float32: GQ_FLOAT32, torch.bfloat16: GQ_BFLOAT16, torch.float16: GQ_FLOAT16}
+        _setup()
     d = _dtypes.get(t.dtype)
     if d is None:
         raise TypeError("%s: float32, bfloat16 or float16 expected, got %s" % (what, t.dtype))
@@ -300,20 +309,19 @@ def _ckpt(t, rows, cols):
 
 def _launch(fn, what, stream, tensors, *args):
     """Call fn(*args, stream) on the tensors' device; the stream defaults to that device's current one."""
-    import torch
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError("%s: CUDA tensors of one device expected, got %s"
                              % (what, ", ".join(str(x.device) for x in tensors if x is not None)))
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _current_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _torch.cuda.current_device() == dev:
         st = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(dev):
             st = fn(*args, stream)
     if st != GQ_OK:
         raise GQError(st, what)
