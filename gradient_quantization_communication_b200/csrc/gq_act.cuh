@@ -91,6 +91,17 @@ __device__ __forceinline__ void shift_words(const uint32_t (&in)[N + 4], uint32_
     for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], bits);
 }
 
+// Eight words at once, to a 32-byte boundary: two stores of 16 bytes write each sector in halves (unpacking
+// 8192 x 4096 to float32 took 44 us with them, 33 us so).
+template <typename W>
+__device__ __forceinline__ void store32(void *p, const W &w)
+{
+    if constexpr (sizeof(w) >= 32)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+}
+
 // FULL: all lanes' 16-byte pieces lie inside the row (inner_chunk).
 template <typename T, bool AL, bool FULL = false>
 __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base, int lane, int cols)
@@ -206,8 +217,12 @@ __device__ __forceinline__ void chunk_store(const Words<T> &r, T *row, int base,
     if (AL || shift == 0u) {
         if (FULL || c0 + 8 <= cols) {
             uint4 *p = reinterpret_cast<uint4 *>(row + c0);
-            p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-            if constexpr (sizeof(T) == 4) p[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+            if (sizeof(T) == 4 && (reinterpret_cast<uintptr_t>(row) & 31u) == 0) {
+                store32(p, r.w);
+            } else {
+                p[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+                if constexpr (sizeof(T) == 4) p[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
