@@ -4,8 +4,8 @@
 // All are one pass over their tensors: a warp takes 512 or 1024 columns of a row at a time.  At
 // full bandwidth 16-bit types leave some 27 instruction slots an element: pack (10) and unpack (8) are bound by
 // the bytes, GELU (30 forward with the checkpoint, 34 backward) by instructions.  Measured at 16384 x 4096
-// bf16, of 6554 GB/s: pack 34 us (92 %), unpack 36 us (86 %), GELU forward with the checkpoint 74 us (70 %),
-// backward 85 us (61 %), SiLU 60 and 78 us.
+// bf16, of 6554 GB/s: pack 34 us (92 %), unpack 36 us (86 %), GELU forward with the checkpoint 72 us (72 %),
+// backward 84 us (61 %), SiLU 60 and 78 us.
 #include "gq_act.cuh"
 #include "gq_act.h"
 #include "gq_internal.h"

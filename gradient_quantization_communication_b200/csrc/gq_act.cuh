@@ -26,7 +26,7 @@ constexpr int kChunk = 256;  // columns of a row that one warp handles at a time
 // AL: every row starts on 16 bytes, and the 8 elements are one or two 16-byte accesses.
 // else: rows start anywhere (on their element size).  A lane loads the aligned 16-byte pieces its elements
 // lie in and shifts them into place when it uses them; a store shifts its elements, with the next lane's
-// first ones behind them, onto aligned pieces.  Loading element by element took 2 to 3 times as long.
+// first ones behind them, onto aligned pieces.  Loading element by element took twice as long.
 // ---------------------------------------------------------------------------------------------
 template <typename T>
 struct Words {
@@ -277,9 +277,6 @@ __device__ __forceinline__ uint32_t group_code(float v, float inv)
     return __float_as_uint(__fmaf_rn(v, inv, 12582912.0f));
 }
 
-// The codes of a lane's 8 values of a group under E, as two words.
-__device__ __forceinline__ uint2 group_codes(const float (&v)[8], uint32_t E);
-
 // 2^(E - 133), NaN for E = 255.
 __device__ __forceinline__ float group_scale(uint32_t E)
 {
@@ -306,6 +303,7 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// The codes of a lane's 8 values of a group, as two words: with the scale 1 / inv, and under E.
 __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float inv)
 {
     uint32_t q[8];

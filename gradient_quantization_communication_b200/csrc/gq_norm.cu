@@ -7,8 +7,8 @@
 //   backward  xh = (x - mean) rstd, g = dy gamma;
 //             dx = rstd (g - sum g / C - xh sum(g xh) / C);
 //             dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy.
-// Measured at 16384 x 4096 bf16, of 6554 GB/s: forward 63 us (65 %), with the checkpoint 89 us (58 %), backward
-// from the input 81 us (76 %), from the checkpoint 81 us (64 %).
+// Measured at 16384 x 4096 bf16, of 6554 GB/s: forward 50 us (81 %), with the checkpoint 71 us (73 %), backward
+// from the input 78 us (79 %), from the checkpoint 79 us (65 %): bound by instructions.
 // Sums are binary32.  The squares are summed around the mean, not as sum x^2 - (sum x)^2 / C, which
 // cancels for rows whose mean is large against their spread.
 #include "gq_act.cuh"
