@@ -76,7 +76,7 @@ size_t wgrad_workspace(int dtype, int64_t tokens, int64_t in, int64_t out, int64
 cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream);
 
 // Sums over rows: part[p][c] = sum over the rows of part p of dy[row][c], then
-// out[c] = (accumulate ? out[c] : 0) + sum over p, in a fixed order.
+// out[c] = (accumulate ? out[c] : 0) + sum over p, in a fixed order.  0 parts: few rows, summed in one kernel.
 int64_t colsum_parts(int64_t rows, int64_t cols);
 cudaError_t launch_colsum(int dtype, int64_t rows, int64_t cols, Mat dy, float *parts, float *out, int accumulate,
                           cudaStream_t stream);

@@ -58,7 +58,7 @@ CALLS = {
                               ckpt=P + 2 * FAR, stream=None),
     "gq_act_fn_backward": dict(kind=0, dtype=BF16, rows=4, cols=40, ckpt=P, dy=P + FAR, dy_stride=40, dx=P + 2 * FAR,
                                dx_stride=40, stream=None),
-    "gq_act_weight_grad": dict(dtype=BF16, tokens=64, cin=40, cout=24, ckpt=P, dy=P + FAR, dy_stride=24, dw=P + 2 * FAR,
+    "gq_act_weight_grad": dict(dtype=F32, tokens=64, cin=40, cout=24, ckpt=P, dy=P + FAR, dy_stride=24, dw=P + 2 * FAR,
                                dw_stride=40, db=P + 3 * FAR, accumulate=0, workspace=P + 4 * FAR,
                                workspace_bytes=1 << 30, stream=None),
     "gq_layer_norm_forward": dict(dtype=BF16, param_dtype=F32, rows=4, cols=40, x=P, x_stride=40, gamma=P + FAR,

@@ -178,6 +178,28 @@ def test_fn(kind, dtype, rows, cols, pad):
     assert (wide[:, cols:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("cols", [64, 72])
+def test_fn_between_halves_of_one_buffer(dtype, cols):
+    """Input and output as column halves of one buffer share rows but no element; nothing else is touched."""
+    x, dy = _fn_inputs(50, cols, dtype, 3)
+    buf = torch.full((50, 2 * cols + 16), 7.0, dtype=dtype, device="cuda")
+    a, b = buf[:, :cols], buf[:, cols + 8:2 * cols + 8]
+    a.copy_(x)
+    want, ck = torch.empty(50, cols, dtype=dtype, device="cuda"), torch.zeros(G.gq_act_layout(50, cols)[0], dtype=torch.uint8,
+                                                                            device="cuda")
+    G.gq_act_fn_forward("silu", x.cuda(), want)
+    G.gq_act_fn_forward("silu", a, b, ck)
+    assert torch.equal(b, want) and torch.equal(a.cpu(), x)
+    assert (buf[:, cols:cols + 8] == 7.0).all() and (buf[:, 2 * cols + 8:] == 7.0).all()
+    G.gq_act_fn_backward("silu", ck, dy.cuda(), want)
+    a.copy_(dy)
+    G.gq_act_fn_backward("silu", ck, a, b)
+    assert torch.equal(b, want) and torch.equal(a.cpu(), dy)
+    with pytest.raises(G.GQError):
+        G.gq_act_fn_forward("silu", a, buf[:, cols - 8:2 * cols - 8])
+
+
 @pytest.mark.parametrize("kind", ["gelu", "gelu_tanh", "silu"])
 def test_fn_far_values(kind):
     """Far out the functions are 0 or x and their derivatives 0 or 1, also where x^2 or x^3 overflows."""
@@ -347,7 +369,7 @@ def test_weight_grad_decodes_every_code_and_exponent(dtype, tokens):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,cin,cout", [(32, 40, 70), (33, 40, 70), (32, 2048, 1024), (32, 2048, 1025), (8, 1000, 8389),
-                                             (64, 256, 256), (65, 257, 255)])
+                                             (64, 256, 256), (65, 257, 255), (512, 64, 300), (513, 64, 301)])
 def test_weight_grad_around_the_choice_of_kernel(dtype, tokens, cin, cout):
     x, dy = _values(tokens, cin, dtype, 3), _values(tokens, cout, dtype, 4, 0.1)
     ck, dw, size, db, dsize = _wgrad_want(x, dy)
@@ -372,6 +394,27 @@ def test_weight_grad_against_differences():
         e[n, k] = 0.5
         diff = loss(w + e) - loss(w - e)
         assert abs(gdw[n, k].item() - diff.item()) <= _wgrad_tol(30, size[n, k].item()) + 1e-9 * abs(loss(w).item() + 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_grad_first_in_a_capture_of_its_own_workspace(dtype):
+    """A captured call that allocates its workspace itself (from the graph's pool), twice in one graph."""
+    x, dy = _values(600, 520, dtype, 8), _values(600, 264, dtype, 9, 0.1)
+    ck, _, _ = _ckpt(x)
+    gdy = dy.cuda()
+    want, wantb = torch.empty(264, 520, device="cuda"), torch.empty(264, device="cuda")
+    G.gq_act_weight_grad(ck, gdy, want, wantb)
+    outs = [(torch.zeros_like(want), torch.zeros_like(wantb)) for _ in range(2)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for dw, db in outs:
+            G.gq_act_weight_grad(ck, gdy, dw, db)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for dw, db in outs:
+        assert torch.equal(dw, want) and torch.equal(db, wantb)
 
 
 # ------------------------------------------------------------------------------------------------
