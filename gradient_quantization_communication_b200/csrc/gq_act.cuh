@@ -247,9 +247,12 @@ __device__ __forceinline__ void chunk_store(const Words<T> &r, T *row, int base,
     // elements no piece covers: the first lane's head, and the last lanes' rest
     const bool own_head = lane == 0 || (!FULL && c0 + head > cols);
     if (own_head || !whole) {
+        const uint32_t heads = (1u << head) - 1u;
+        uint32_t mine = (own_head ? heads : 0u) | (whole ? 0u : ~heads);
+        if (!FULL) mine &= (1u << min(max(cols - c0, 0), 8)) - 1u;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if ((FULL || c0 + j < cols) && (j < head ? own_head : !whole)) row[c0 + j] = elem_get<T>(r.w, j);
+            if (mine & 1u << j) row[c0 + j] = elem_get<T>(r.w, j);
     }
 }
 
