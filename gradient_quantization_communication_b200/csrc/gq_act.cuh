@@ -4,10 +4,11 @@
 // Format (include/gq.h, gq_act_layout).  A group is 32 consecutive columns of a row.  With
 // m = max |x| of the group, e is the smallest integer that keeps |rint(x * 2^-e)| <= 127 for all of
 // its values, so m * 2^-e lies in [63.75, 127.5): between 6 and 7 bits and a sign are kept of the
-// largest value.  The exponent byte is E = e + 133: m's biased binary32 exponent after m's mantissa
-// was rounded up from 127.5/128.  Because the scale is a power of two, q * 2^e has at most 7
-// significant bits: bf16 and binary32 hold every decoded value exactly, down to E = 0 (2^-133 is
-// bf16's smallest subnormal), and the products that read a checkpoint round nothing of it.
+// largest value.  The exponent byte is E = e + 133: m's biased binary32 exponent, one more where m is
+// at least 127.5/128 of the next power of two, and at least 0.  Because the scale is a power of two,
+// q * 2^e has at most 7 significant bits: bf16 and binary32 hold every decoded value exactly, down to
+// E = 0 (2^-133 is bf16's smallest subnormal), and the products that read a checkpoint round nothing
+// of it.
 // E = 255 marks a group with a NaN or an infinity; it decodes to NaN.  The largest finite groups
 // (E would be 255) keep E = 254 and saturate their codes at 127.
 #pragma once
@@ -269,7 +270,9 @@ struct Ckpt {
 // E of a group whose largest |x| has these bits (a NaN's or infinity's bits give 255).
 __device__ __forceinline__ uint32_t group_exp(uint32_t abs_bits)
 {
-    const uint32_t e = min((abs_bits + 0x10000u) >> 23, 254u);
+    // the border is 127.5 of the scale: of a subnormal's last place 2^-149, 127.5 * 2^16
+    const uint32_t up = abs_bits < 0x00800000u ? 0x8000u : 0x10000u;
+    const uint32_t e = min((abs_bits + up) >> 23, 254u);
     return abs_bits >= 0x7f800000u ? 255u : e;
 }
 
