@@ -25,16 +25,15 @@ __host__ __device__ constexpr int chunks_of(int op, bool al) { return op == kBac
 //              tail's digits, where 1 + erf would cancel.
 //   GELU tanh  x s(2u), u = sqrt(2/pi) (x + 0.044715 x^3)  [= x (1 + tanh u) / 2], s the logistic function;
 //   SiLU       x s(x);  s (1 + x (1 - s)).
-// In 16-bit types, whose own step hides it, the exponential is the hardware's (2^-21 or so), and Phi's tail
-// comes from a polynomial; binary32 calls expf and erfcf.
-// exp(t) for t <= 0.  FLUSH: 0 where it is subnormal.
-template <bool FAST, bool FLUSH = false>
+// In 16-bit types, whose own step hides it, the exponential is the hardware's (2^-22 of its result, besides what
+// its argument's roundings make of it: 2^-17 where the result nears 2^-126), and Phi's tail comes from a
+// polynomial; binary32 calls expf and erfcf.
+// exp(t) for t <= 0, subnormal results included.
+template <bool FAST>
 __device__ __forceinline__ float exp_neg(float t)
 {
     if constexpr (!FAST) return expf(t);
     float r;
-    if constexpr (FLUSH) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));
-    else
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(t * 1.4426950f));
     return r;
 }
@@ -58,28 +57,35 @@ __device__ __forceinline__ void logistic(float t, float &s, float &one_minus)
     one_minus = t >= 0.0f ? b : a;
 }
 
-// Phi(x) and exp(-x^2 / 2).
-template <bool FAST, bool FLUSH>
+// Phi(x) and exp(-x^2 / 2) * kUp<FAST>.  The fast exponential flushes results below 2^-126 to 0, where bf16 and
+// binary32 still have values: it is formed 2^24 times as large, down to 2^-150, and the factors after it are that
+// much smaller, for no more instructions (the offset joins the product with log2 e).
+template <bool FAST>
+constexpr float kUp = FAST ? 0x1p24f : 1.0f;
+
+template <bool FAST>
 __device__ __forceinline__ void normal(float x, float &Phi, float &e)
 {
-    e = exp_neg<FAST, FLUSH>(-0.5f * x * x);
     if constexpr (FAST) {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(-0.72134752f * x, x, 24.0f)));
         // Phi(-z) exp(z^2 / 2) = t P(t) with t = 1 / (1 + 0.31 z), z = |x|: the smoothest of such maps of
         // [0, inf) to (0, 1].  P has degree 7, fitted on z <= 14.5 (beyond, the tail is below binary32's
-        // range) by Lawson's weighted least squares to the smallest largest relative error, 1.6e-7; 5e-7 in
-        // binary32 arithmetic.
+        // range) by Lawson's weighted least squares to the smallest largest relative error: 1.9e-7 with the
+        // coefficients as rounded here, 5e-7 in binary32 arithmetic.
+        constexpr float d = 1.0f / kUp<true>;
         const float t = inverse<true>(__fmaf_rn(0.31f, fabsf(x), 1.0f));
-        float h = 0.035870399326086044f;
-        h = __fmaf_rn(h, t, -0.1417304277420044f);
-        h = __fmaf_rn(h, t, 0.15529736876487732f);
-        h = __fmaf_rn(h, t, -0.015128081664443016f);
-        h = __fmaf_rn(h, t, 0.11023717373609543f);
-        h = __fmaf_rn(h, t, 0.10772977769374847f);
-        h = __fmaf_rn(h, t, 0.12406746298074722f);
-        h = __fmaf_rn(h, t, 0.12365640699863434f);
+        float h = 0.035870399326086044f * d;
+        h = __fmaf_rn(h, t, -0.1417304277420044f * d);
+        h = __fmaf_rn(h, t, 0.15529736876487732f * d);
+        h = __fmaf_rn(h, t, -0.015128081664443016f * d);
+        h = __fmaf_rn(h, t, 0.11023717373609543f * d);
+        h = __fmaf_rn(h, t, 0.10772977769374847f * d);
+        h = __fmaf_rn(h, t, 0.12406746298074722f * d);
+        h = __fmaf_rn(h, t, 0.12365640699863434f * d);
         const float tail = h * t * e;
         Phi = x >= 0.0f ? 1.0f - tail : tail;
     } else {
+        e = expf(-0.5f * x * x);
         Phi = 0.5f * erfcf(-x * 0.70710678f);
     }
 }
@@ -92,14 +98,14 @@ struct Fn<GQ_FN_GELU, FAST> {
     static __device__ __forceinline__ float f(float x)
     {
         float P, e;
-        normal<FAST, true>(x, P, e);  // where e is subnormal, |x P| is too
+        normal<FAST>(x, P, e);
         return x * P;
     }
     static __device__ __forceinline__ float df(float x)
     {
         float P, e;
-        normal<FAST, false>(x, P, e);
-        return __fmaf_rn(x * 0.39894228f, e, P);
+        normal<FAST>(x, P, e);
+        return __fmaf_rn(x * (0.39894228f / kUp<FAST>), e, P);
     }
 };
 template <bool FAST>
