@@ -423,7 +423,7 @@ __device__ __forceinline__ int grid_pos(float u, float mn, float scale)
 
 // ---------------------------------------------------------------------------------------------
 // Bulk asynchronous copies (TMA, 1-D, into this CTA only) into shared memory, completed on an mbarrier.
-// Every wait is bounded: after kWaitLimitNs of global time it gives up and reports failure.
+// Every wait is bounded: after kWaitLimitNs of global time, or a number of cycles, it gives up and reports failure.
 // ---------------------------------------------------------------------------------------------
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // one second
 
@@ -458,15 +458,19 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, unsigned b
                  : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait(unsigned long long *bar, unsigned parity)
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, unsigned parity)
 {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait(unsigned long long *bar, unsigned parity)
+{
+    return mbar_try_wait(smem_u32(bar), parity);
 }
 
 __device__ __forceinline__ unsigned long long global_ns()
@@ -487,6 +491,25 @@ __device__ __forceinline__ bool mbar_wait_warp(unsigned long long *bar, unsigned
         const bool late = global_ns() - t0 > limit_ns;
         if (__any_sync(kFull, late)) return false;
     }
+}
+
+// Bounded waits on a barrier at a shared-memory address, by the SM's clock: reading the global timer takes longer
+// than most waits between the warps of one kernel.  Of one thread; false if it gave up after `limit` cycles.
+__device__ __forceinline__ bool mbar_wait_cycles(uint32_t bar, uint32_t parity, long long limit)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > limit) return false;
+    }
+}
+// The same, of a warp: every lane acquires, and all agree on the outcome.
+__device__ __forceinline__ bool mbar_wait_cycles_warp(uint32_t bar, uint32_t parity, long long limit)
+{
+    return __all_sync(kFull, mbar_wait_cycles(bar, parity, limit));
 }
 
 }  // namespace gq

@@ -136,35 +136,6 @@ int64_t part_tiles(const Schedule &s) { return s.ranges > s.cut ? s.cut + s.rang
 // ---------------------------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait of one thread; false if it gave up.  By the SM's clock: reading the global timer takes
-// longer than most waits here.
-__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity, long long limit)
-{
-    if (try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (try_wait(bar, parity)) return true;
-        if (clock64() - t0 > limit) return false;
-    }
-}
-// The same, of a warp: every lane acquires, and all agree on the outcome.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, long long limit)
-{
-    return __all_sync(kFull, wait_thread(bar, parity, limit));
-}
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
 {
     uint32_t r;
@@ -514,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 int plane = (int)(it.first / p.s.tok_blocks);
                 int64_t tb = it.first - plane * p.s.tok_blocks;
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (r.wrapped && !wait_thread(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
+                    if (r.wrapped && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
                         ok = false;
                         break;
                     }
@@ -536,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             const int left = r.wrapped ? kStages : r.st;
             for (int i = 0; i < left; ++i) {
                 r.back();
-                wait_thread(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit);
+                mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit);
             }
         } else if (warp == 1 && rank == 0) {
             // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one
@@ -550,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             for (int64_t i = pair; ok && item_of(p.s, i, it); i += pairs) {
                 for (int64_t b = it.first; ok && b < it.last; ++runs) {
                     const int buf = (int)(runs & 1);
-                    if (runs >= 2 && !wait_warp(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit)) {
+                    if (runs >= 2 && !mbar_wait_cycles_warp(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit)) {
                         ok = false;
                         break;
                     }
@@ -559,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                     const int n = (int)(it.last - b < kRun ? it.last - b : kRun);
                     b += n;
                     for (int j = 0; j < n; ++j) {
-                        if (!wait_warp(smem_u32(&sh.ready[r.st]), r.ph, p.limit)) {
+                        if (!mbar_wait_cycles_warp(smem_u32(&sh.ready[r.st]), r.ph, p.limit)) {
                             ok = false;
                             break;
                         }
@@ -592,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 int64_t t = it.first % p.s.tok_blocks * kTok + lane;
                 const uint8_t *src = p.k.exps + (any ? t * p.k.exp_pitch + (k0 >> 5) : 0);
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (r.wrapped && !wait_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
+                    if (r.wrapped && !mbar_wait_cycles_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
                         ok = false;
                         break;
                     }
@@ -634,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             for (int j = 0; j < kTile / 2; ++j) acc[j] = 0.0f;
             for (int64_t b = it.first; b < it.last; b += kRun, ++runs) {
                 const int buf = (int)(runs & 1);
-                ok = ok && wait_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
+                ok = ok && mbar_wait_cycles_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
                 for (int c = 0; c < kTile / 2; c += 16) {
@@ -676,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         Ring r;
         r.next(w >> 2);
         for (int64_t i = w >> 2; i < total; i += 2, r.next(2)) {
-            if (!wait_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit)) break;
+            if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit)) break;
             const uint32_t off = r.st * kStageBytes;
             // tokens t, t + 2 (whose swizzle differs in bit 1), and 8 on
             const uint32_t f[2] = {from + off, (from ^ 32u) + off};
@@ -975,7 +946,9 @@ cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t stream)
     p.sdw = a.dw_stride;
     p.accumulate = a.accumulate;
     p.parts = reinterpret_cast<float *>(a.ws + w.parts);
-    p.limit = 4000000000ll;  // two seconds; the longest wait, for a run of stages, is some microseconds
+    // two seconds at 1.97 GHz, three at the 1.39 GHz of the power cap; the longest wait, for a run of stages, is some
+    // microseconds
+    p.limit = 4000000000ll;
 
     if (few(a.tokens, a.in, a.out)) {
         if (a.dtype == GQ_FLOAT32) return launch_few<float>(p, a, stream);

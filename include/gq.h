@@ -338,10 +338,11 @@ GQ_API gq_status_t gq_plan_status(gq_plan_t plan, void *stream);
 
 /* Self-test of the failure path, no counterpart in the pages: every wait of the kernels for a
  * bulk copy is bounded in time and, when it gives up, raises the plan's timeout flag instead of
- * hanging.  This call enqueues one warp that waits, with the same bounded wait, on a barrier
- * that nothing completes; after limit_ns nanoseconds (clamped to [1e6, 1e9]) it raises the flag
- * and exits.  gq_plan_status then returns GQ_ERR_TIMEOUT, and the plan and the context stay
- * usable.  Returns GQ_ERR_INVALID for a NULL plan, GQ_ERR_CUDA if the launch fails. */
+ * hanging; the waits inside gq_act_weight_grad are bounded in cycles.  This call enqueues three
+ * warps that wait, with those same bounded waits, on barriers that nothing completes; after
+ * limit_ns nanoseconds (clamped to [1e6, 1e9]) and twice as many cycles they give up, and once
+ * all have, the flag is raised.  gq_plan_status then returns GQ_ERR_TIMEOUT, and the plan and the
+ * context stay usable.  Returns GQ_ERR_INVALID for a NULL plan, GQ_ERR_CUDA if the launch fails. */
 GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, void *stream);
 
 /*
