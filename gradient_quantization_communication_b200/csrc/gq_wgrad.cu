@@ -22,9 +22,10 @@
 //
 // A few tokens of a small layer go to a kernel of their own, k_few.
 //
-// float32 gradients are cut into three bf16 planes without loss (8 significant bits each, by
-// truncation) by a pass before, and the contraction runs over 3 x tokens; so are rows that TMA cannot
-// fetch (a stride that is no multiple of 16 bytes, or rows that overlap) copied to aligned ones.
+// float32 gradients are cut into three bf16 planes (8 significant bits each, by truncation) by a pass before, and
+// the contraction runs over 3 x tokens.  The planes add up to the gradient exactly, but for what lies below bf16's
+// smallest value, 2^-133, which is cut off (gradients under 2^-110 may have such bits).  Rows that TMA cannot
+// fetch (a stride that is no multiple of 16 bytes, or rows that overlap) are copied to aligned ones.
 #include <cuda.h>
 
 #include "gq_act.cuh"
@@ -807,8 +808,8 @@ __global__ void __launch_bounds__(256) k_few(const __grid_constant__ Params p, c
     }
 }
 
-// dy into rows of `pitch` 16-bit values: float32 as three bf16 planes that add up to it exactly (smallest
-// first), 16-bit types as they are.  A warp takes 256 columns of a row.
+// dy into rows of `pitch` 16-bit values: float32 as three bf16 planes that add up to it (smallest first; bits
+// below 2^-133 cut off), 16-bit types as they are.  A warp takes 256 columns of a row.
 template <typename T, bool AL>
 __global__ void __launch_bounds__(256) k_stage(const T *dy, int64_t sdy, int64_t tokens, int out, int64_t pitch, uint16_t *dst)
 {

@@ -419,7 +419,7 @@ GQ_API gq_status_t gq_act_fn_backward(int kind, int dtype, int64_t rows, int64_t
  * accumulate = 1 adds to dw and db (micro-batches), 0 overwrites them.
  *   ckpt       checkpoint of tokens x in values; xh is decoded to dy's type, as by gq_act_unpack:
  *              exact for bfloat16 and float32.
- *   dy         tokens x out values of type dtype.
+ *   dy         tokens x out values of type dtype (float32: bits below 2^-133 may be cut off).
  *   workspace  device, at least gq_act_weight_grad_workspace bytes (given the same arguments; bias
  *              is db != NULL), 16-byte aligned; NULL if that is 0.  Its contents do not outlive the call.
  */

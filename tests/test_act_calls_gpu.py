@@ -68,3 +68,41 @@ def test_rows_that_repeat_or_overlap(dtype, stride):
         G.gq_act_weight_grad(ck, t, dw, db)
         outs.append((dw, db))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_every_value_of_a_gradient(dtype, tokens):
+    """All 65536 patterns of a 16-bit gradient (of float32 the upper halves, the lower at random), in one token,
+    against inputs 1, -2, 0.5 and 0: products as the formulas have them, infinities, NaN and subnormals included."""
+    bits = torch.arange(-32768, 32768, dtype=torch.int32)
+    if dtype == torch.float32:
+        low = torch.randint(0, 1 << 16, bits.shape, generator=torch.Generator().manual_seed(4), dtype=torch.int32)
+        v = ((bits << 16) | low).view(dtype)
+    else:
+        v = bits.to(torch.int16).view(dtype)
+    if tokens == 2:      # a few tokens, few columns: another kernel
+        v = v[::4]
+    v = v.cuda()
+    x = torch.zeros(tokens, 64, dtype=dtype, device="cuda")
+    x[1, :3] = torch.tensor([1.0, -2.0, 0.5], dtype=dtype)
+    ck = torch.zeros(G.gq_act_layout(tokens, 64)[0], dtype=torch.uint8, device="cuda")
+    G.gq_act_pack(x, ck)
+    dy = torch.zeros(tokens, v.numel(), dtype=dtype, device="cuda")
+    dy[1] = v
+    dw, db = torch.empty(v.numel(), 64, device="cuda"), torch.empty(v.numel(), device="cuda")
+    G.gq_act_weight_grad(ck, dy, dw, db)
+    d = v.double()
+    number = torch.isfinite(d)
+    # float32 in three bf16 planes: what lies below bf16's smallest value, 2^-133, is cut off
+    cut = 2.0 ** -133 if dtype == torch.float32 and tokens > 2 else 0.0
+    for k, f in enumerate((1.0, -2.0, 0.5)):
+        want = (d * f).float().double()
+        got = dw[:, k].double()
+        fits = number & torch.isfinite(want)
+        # half of the smallest values: a tie, rounded or cut
+        assert ((got - want).abs()[fits] <= cut * abs(f) + (2.0 ** -149 if f == 0.5 else 0.0)).all()
+        assert torch.equal(torch.isnan(got), torch.isnan(d))
+        assert torch.equal(got[~number & ~torch.isnan(d)], want[~number & ~torch.isnan(d)])
+    assert torch.equal(torch.isnan(dw[:, 3]), ~number) and (dw[:, 3][number] == 0).all()
+    assert torch.equal(torch.nan_to_num(db, nan=-1.0), torch.nan_to_num(v.float(), nan=-1.0))
