@@ -3,9 +3,9 @@
 //
 // All are one pass over their tensors: a warp takes 512 or 1024 columns of a row at a time.  At
 // full bandwidth 16-bit types leave some 27 instruction slots an element: pack (10) and unpack (8) are bound by
-// the bytes, GELU (30 forward with the checkpoint, 34 backward) by instructions.  Measured at 16384 x 4096
-// bf16, of 6554 GB/s: pack 34 us (92 %), unpack 36 us (86 %), GELU forward with the checkpoint 72 us (72 %),
-// backward 84 us (61 %), SiLU 60 and 78 us.
+// the bytes.  GELU (28 an element forward with the checkpoint, 29 backward) would take 51 and 53 us by issue alone at
+// 1.965 GHz; issue is 75 and 71 % active, and the rest is latency, in the backward pass that of its loads.  Measured in a graph at 16384 x 4096 bf16, of 6554 GB/s: pack 34 us (92 %), unpack 36 us (86 %), GELU forward
+// with the checkpoint 72 us (72 %), backward 79 us (65 %), SiLU 60 and 76 us (86 and 68 %), GELU tanh 71 and 91 us.
 #include "gq_act.cuh"
 #include "gq_act.h"
 #include "gq_internal.h"
@@ -16,8 +16,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWide = 4 * kChunk;
 // Chunks of a row that a warp takes at a time.  Four spread an item's addresses over the most elements; where a
-// chunk is two loads, or is shifted into place, their registers cost more (SiLU backward 70 us with two, 101 us
-// with four; forward 66 and 60 us, 16384 x 4096 bf16).
+// chunk is two loads, or is shifted into place, their registers cost more.  At 16384 x 4096, two against four: SiLU
+// backward bf16 76 and 102 us, forward with the checkpoint 59 and 60 us, GELU's 74 and 72 us, SiLU's of float32 112
+// and 100 us; at 16384 x 4095 bf16 (shifted) SiLU forward with the checkpoint 106 and 140 us.
 __host__ __device__ constexpr int chunks_of(int op, bool al) { return op == kBackward || !al ? 2 : 4; }
 
 // f(x) and f'(x), in binary32.

@@ -7,8 +7,11 @@
 //   backward  xh = (x - mean) rstd, g = dy gamma;
 //             dx = rstd (g - sum g / C - xh sum(g xh) / C);
 //             dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy.
-// Measured at 16384 x 4096 bf16, of 6554 GB/s: forward 50 us (81 %), with the checkpoint 71 us (73 %), backward
-// from the input 78 us (79 %), from the checkpoint 79 us (65 %): bound by instructions.
+// Measured in a graph at 16384 x 4096 bf16, of 6554 GB/s: forward 51 us (81 %), with the checkpoint 72 us (72 %),
+// backward from the input 79 us (78 %), from the checkpoint 80 us (64 %).  Issue alone (22 and 26 instructions an
+// element, where full bandwidth leaves 27 slots) would take less than the bytes do, and is 59 and 66 % active: at 128
+// registers a thread a quarter of the warps fit, too few to hide a row's way from its load through shuffles and
+// the join of its warps to its store.
 // Sums are binary32.  The squares are summed around the mean, not as sum x^2 - (sum x)^2 / C, which
 // cancels for rows whose mean is large against their spread.
 #include "gq_act.cuh"
@@ -555,8 +558,8 @@ __global__ void __launch_bounds__(128) k_cols(const __grid_constant__ Params p)
 
 // Column sums of few rows in one kernel: a block takes a chunk of 256 columns, its 16 warps every 16th row each,
 // eight at a time, and their sums are added in warp order.  Against partial rows and their reduction, a launch
-// more: 64 rows 16.8 and 18.6 us (with the rest of the weight gradient, in a graph), 512 rows 16.0 and 15.1 us but
-// 19.6 and 21.8 us by calls, 1024 rows 22.9 and 18.2 us.
+// more: 64 rows 16.8 and 18.6 us (with the rest of the weight gradient, in a graph), 1024 rows 22.9 and 18.2 us; 512
+// rows 19.6 and 21.8 us by calls, which set the border, but 16.0 and 15.1 us in a graph, which would have it lower.
 constexpr int kFewRows = 512;
 
 template <typename T, bool AL>

@@ -361,8 +361,9 @@ GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, vo
  *     kind in a process loads its kernels: make it before any stream capture.
  *   - A matrix is rows of cols elements of type `dtype`, its rows `stride` elements apart; a column
  *     step other than 1 is not supported.  Rows of an input may repeat (stride 0) or overlap; those
- *     of an output may not (stride >= cols).  With one row the stride is not used.  Rows that start
- *     on 16 bytes take the faster loads.
+ *     of an output may not (stride >= cols).  With one row the stride is not used.  The first row
+ *     starts on 16 bytes, as every device pointer; the others may start anywhere, and take the faster
+ *     loads where they too start on 16 bytes.
  *   - 0 <= rows < 2^31, 1 <= cols <= GQ_ACT_MAX_COLS.  With rows = 0 nothing is read; gradients that
  *     sum over the rows are then written as 0 (or left as they are when accumulating).
  *   - float32 outputs (gradients, mean, rstd) and mean/rstd inputs need 4-byte alignment only, so
@@ -370,7 +371,8 @@ GQ_API gq_status_t gq_selftest_bounded_wait(gq_plan_t plan, int64_t limit_ns, vo
  *   - No output may share memory with an input or another output (GQ_ERR_INVALID); columns of one
  *     wider buffer with the same stride do not share any.
  *   - Non-finite values pass through as in the formulas; a group with one in a checkpoint reads as
- *     NaN throughout.  Sums are binary32 and their order is fixed: equal calls give equal bits.
+ *     NaN throughout.  Sums are binary32 and their order is fixed: equal calls give equal bits.  The
+ *     order may depend on the call's sizes: a row may get other last bits among another number of rows.
  *   - Should a kernel's bounded wait give up (a fault: no wait is expected to last a second), the
  *     outputs it was computing are NaN; there is no status word to ask.
  */
@@ -431,7 +433,8 @@ GQ_API gq_status_t gq_act_weight_grad(int dtype, int64_t tokens, int64_t in, int
 
 /*
  * Layer norm over each row: y = (x - mean) * rstd * gamma + beta, rstd = 1 / sqrt(var + eps), var the
- * population variance around the mean.
+ * population variance around the mean.  The squares and their sums are binary32 too: rows whose spread is
+ * above some 1e17, or, with eps = 0, below some 1e-19, leave its range, and rstd is then 0, inexact or infinite.
  *   gamma, beta  cols values of type param_dtype (dtype or GQ_FLOAT32); NULL: 1 and 0.
  *   mean, rstd   device, rows float32, written for the backward pass.
  *   ckpt         receives the checkpoint of x, in the same pass (NULL: none).
