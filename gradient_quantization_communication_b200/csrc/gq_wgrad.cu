@@ -34,6 +34,7 @@
 #include "gq_act.h"
 #include "gq_device.cuh"
 #include "gq_internal.h"
+#include "gq_ring.cuh"
 
 namespace gq {
 namespace {
@@ -46,9 +47,6 @@ constexpr int kBBytes = kHalf * kTok * 2;
 constexpr int kCodeBytes = kHalf * kTok;
 constexpr int kExpBytes = kTok * 4;      // four groups' exponents of every token
 constexpr int kBlockBytes = kTok * 128;  // 64 columns x 64 tokens of a 16-bit operand
-// Five stages of everything.  A ring of its own for the decoded A, so that six stages could be under way,
-// needs one more signal and wait a stage and measured slower (1.81 against 1.74 ms, 16384 x 4096 x 16384).
-constexpr int kStages = 5;
 constexpr int kStageBytes = kABytes + kBBytes + kCodeBytes;
 constexpr int kSmemBytes = kStages * (kStageBytes + kExpBytes) + 1024;
 // Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums round
@@ -375,35 +373,12 @@ __device__ __forceinline__ void store4(float *o, float4 v, int n, int accumulate
 }
 
 struct Shared {
-    unsigned long long full[kStages];   // codes, exponents and B have arrived (this CTA)
+    unsigned long long full[kFullBars]; // codes, exponents and B have arrived (this CTA): Ring::full
     unsigned long long ready[kStages];  // both CTAs have decoded A (the leader's is used)
     unsigned long long empty[kStages];  // the MMAs have read A and B
     unsigned long long acc_full[2];     // a run's sums are complete
     unsigned long long acc_empty[2];    // both CTAs have read them (the leader's is used)
     uint32_t tmem;
-};
-
-// Position in the ring of stages; wrapped: every stage has been used before.
-struct Ring {
-    int st = 0;
-    uint32_t ph = 0;
-    bool wrapped = false;
-    __device__ __forceinline__ void next(int by = 1)
-    {
-        st += by;
-        if (st >= kStages) {
-            st -= kStages;
-            ph ^= 1u;
-            wrapped = true;
-        }
-    }
-    __device__ __forceinline__ void back()
-    {
-        if (--st < 0) {
-            st = kStages - 1;
-            ph ^= 1u;
-        }
-    }
 };
 
 // 128 n of a tile from TMEM to dw, or to the workspace; a wait that gave up (ok false) leaves NaN.
@@ -455,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
     const int64_t pair = blockIdx.x >> 1, pairs = p.s.pairs;
 
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kFullBars; ++i) mbar_init(&sh.full[i], 1 + 32);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1 + 32);
             mbar_init(&sh.ready[i], kConvWarps);  // half of the warps, of two CTAs
             mbar_init(&sh.empty[i], 1);
         }
@@ -488,13 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 int plane = (int)(it.first / p.s.tok_blocks);
                 int64_t tb = it.first - plane * p.s.tok_blocks;
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (r.wrapped && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
+                    if (r.wrapped && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
                         ok = false;
                         break;
                     }
                     const int t0 = (int)tb * kTok;
-                    const uint32_t base = stages + r.st * kStageBytes, bar = smem_u32(&sh.full[r.st]);
-                    mbar_arrive_expect_tx(&sh.full[r.st], kBBytes + kCodeBytes);
+                    const uint32_t base = stages + r.st * kStageBytes, bar = smem_u32(&sh.full[r.full()]);
+                    mbar_arrive_expect_tx(&sh.full[r.full()], kBBytes + kCodeBytes);
                     tma_load_2d(base + kABytes + kBBytes, &p.codes, k0, t0, bar);
                     tma_load_3d(base + kABytes, &p.dy, n0, t0, plane, bar);
                     tma_load_3d(base + kABytes + kBlockBytes, &p.dy, n0 + 64, t0, plane, bar);
@@ -510,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
             const int left = r.wrapped ? kStages : r.st;
             for (int i = 0; i < left; ++i) {
                 r.back();
-                mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.ph, p.limit);
+                if (ok) mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity(), p.limit);
+                else mbar_wait_cycles(smem_u32(&sh.full[r.full()]), r.full_parity(), p.limit);
             }
         } else if (warp == 1 && rank == 0) {
             // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one
@@ -533,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                     const int n = (int)(it.last - b < kRun ? it.last - b : kRun);
                     b += n;
                     for (int j = 0; j < n; ++j) {
-                        if (!mbar_wait_cycles_warp(smem_u32(&sh.ready[r.st]), r.ph, p.limit)) {
+                        if (!mbar_wait_cycles_warp(smem_u32(&sh.ready[r.st]), r.parity(), p.limit)) {
                             ok = false;
                             break;
                         }
@@ -566,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                 int64_t t = it.first % p.s.tok_blocks * kTok + lane;
                 const uint8_t *src = p.k.exps + (any ? t * p.k.exp_pitch + (k0 >> 5) : 0);
                 for (int64_t b = it.first; b < it.last; ++b) {
-                    if (r.wrapped && !mbar_wait_cycles_warp(smem_u32(&sh.empty[r.st]), r.ph ^ 1u, p.limit)) {
+                    if (r.wrapped && !mbar_wait_cycles_warp(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
                         ok = false;
                         break;
                     }
@@ -578,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 128),
                                  "l"(in1 ? src + 32 * p.k.exp_pitch : p.k.exps), "r"(in1 ? 4 : 0)
                                  : "memory");
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[r.st])) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[r.full()])) : "memory");
                     r.next();
                     t += kTok;
                     if (any) src += kTok * p.k.exp_pitch;
@@ -650,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wgrad(const __grid_constant__ P
         Ring r;
         r.next(w >> 2);
         for (int64_t i = w >> 2; i < total; i += 2, r.next(2)) {
-            if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.ph, p.limit)) break;
+            if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.full()]), r.full_parity(), p.limit)) break;
             const uint32_t off = r.st * kStageBytes;
             // tokens t, t + 2 (whose swizzle differs in bit 1), and 8 on
             const uint32_t f[2] = {from + off, (from ^ 32u) + off};

@@ -106,3 +106,23 @@ def test_every_value_of_a_gradient(dtype, tokens):
         assert torch.equal(got[~number & ~torch.isnan(d)], want[~number & ~torch.isnan(d)])
     assert torch.equal(torch.isnan(dw[:, 3]), ~number) and (dw[:, 3][number] == 0).all()
     assert torch.equal(torch.nan_to_num(db, nan=-1.0), torch.nan_to_num(v.float(), nan=-1.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens,cin,cout,pad", [(5072, 859, 3264, 1), (5992, 153, 1931, 24), (16384, 1024, 1024, 0)])
+def test_repeats_give_equal_bits(dtype, tokens, cin, cout, pad):
+    """Long contractions, whose warps wait for one another some hundred times a tile, over and over."""
+    g, ck, xh = _inputs(tokens, cin, dtype, 5)
+    dy = (0.05 * torch.randn(tokens, cout + pad, generator=g, device="cuda")).to(dtype)[:, :cout]
+    first, again = torch.empty(cout, cin, device="cuda"), torch.empty(cout, cin, device="cuda")
+    ws = G.gq_act_weight_grad_workspace(ck, dy, first)
+    G.gq_act_weight_grad(ck, dy, first, workspace=ws)
+    d = dy.double()
+    total = tokens * (3 if dtype == torch.float32 else 1)
+    # runs of 512 tokens (of three planes) lose at most two steps every 16 tokens, their sums one rounding each
+    steps = 512 / 16 * 2 + 3 * total / 512 + 16
+    assert ((first.double() - d.t() @ xh).abs() <= steps * 2.0 ** -23 * (d.abs().t() @ xh.abs())).all()
+    for _ in range(100):
+        again.fill_(float("nan"))
+        G.gq_act_weight_grad(ck, dy, again, workspace=ws)
+        assert torch.equal(first, again)
