@@ -19,7 +19,7 @@
 // that A is decoded then waits for the loads ahead (twice the time).  For few tokens bounded by the bytes of dw.
 // Measured, bf16, in graphs of ten calls: 8192 tokens, 4096 x 4096 226 us (1.22 PFLOP/s); 16384 tokens, 4096 x 16384
 // 1.73 ms (1.27, 78 % of the library's measured peak); 64 tokens, 4096 x 4096 21 us.  In a long run of calls, under
-// the power cap, 263 us (1.04) and 1.98 ms (1.11).  gq_act_unpack and a library product after it, which round the sums
+// the power cap, 267 us (1.03) and 2.01 ms (1.09).  gq_act_unpack and a library product after it, which round the sums
 // less well and need the decoded tensor, take 186 us, 1.33 ms and 12 us in the same graphs.
 //
 // A few tokens of a small layer go to a kernel of their own, k_few.
