@@ -103,18 +103,25 @@ __device__ __forceinline__ void store32(void *p, const W &w)
                      : "memory");
 }
 
+// KEPT: nothing writes the memory while the kernel runs, so that the read-only path may be taken.
+template <bool KEPT>
+__device__ __forceinline__ uint4 load16(const void *p)
+{
+    if constexpr (KEPT) return __ldg(reinterpret_cast<const uint4 *>(p));
+    else return *reinterpret_cast<const uint4 *>(p);
+}
+
 // FULL: all lanes' 16-byte pieces lie inside the row (inner_chunk).
-template <typename T, bool AL, bool FULL = false>
+template <typename T, bool AL, bool FULL = false, bool KEPT = true>
 __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base, int lane, int cols)
 {
     const int c0 = base + lane * 8;
     if constexpr (AL) {
         if (FULL || c0 + 8 <= cols) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(row + c0);
-            const uint4 a = __ldg(p);
+            const uint4 a = load16<KEPT>(row + c0);
             r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
             if constexpr (sizeof(T) == 4) {
-                const uint4 b = __ldg(p + 1);
+                const uint4 b = load16<KEPT>(row + c0 + 4);
                 r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
             }
         } else {
@@ -129,7 +136,7 @@ __device__ __forceinline__ void chunk_load(Raw<T, AL> &r, const T *row, int base
         for (int i = 0; i < P; ++i) {
             const int c = first + i * E;
             if (FULL || (c >= 0 && c + E <= cols)) {
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(row + c));
+                const uint4 a = load16<KEPT>(row + c);
                 r.w[4 * i] = a.x; r.w[4 * i + 1] = a.y; r.w[4 * i + 2] = a.z; r.w[4 * i + 3] = a.w;
             } else {
 #pragma unroll

@@ -1,0 +1,57 @@
+// gq_adamw.h -- launch entry points of the AdamW kernels, shared by their translation units (not part of the
+// public ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gq.h"
+
+namespace gq {
+
+constexpr int kAdamChunk = 4096;  // elements of a tensor that one block updates
+
+// A moment of n elements in 8 bits.
+__host__ __device__ inline size_t adam_exps_off(int64_t n) { return (size_t)((n + 127) / 128 * 128); }
+inline size_t adam_bytes(int64_t n) { return adam_exps_off(n) + (size_t)(((n + 127) / 128 + 15) / 16 * 16); }
+
+// A tensor as the kernels read it.
+struct AdamTensor {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m, *v;
+    int64_t n;
+    int64_t start;      // elements of the tensors before it
+    float decay, lr_scale;
+    uint32_t number;    // in the caller's list
+    int32_t aligned;    // all of it starts on 16 bytes
+};
+// What block i works on: elements kAdamChunk * part and up of a tensor.
+struct AdamChunk {
+    uint32_t tensor, part;
+};
+
+struct AdamArgs {
+    int param_dtype, grad_dtype, state_bits;
+    bool master;
+    int64_t chunks;
+    const AdamTensor *tensors;  // device
+    const AdamChunk *table;     // device
+    uint64_t seed;
+};
+
+struct AdamStep {
+    gq_adamw_scalars_t now;
+    float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
+    const float *scale;
+    const gq_adamw_scalars_t *scalars;
+};
+cudaError_t launch_adamw(const AdamArgs &a, const AdamStep &s, cudaStream_t stream);
+cudaError_t launch_adamw_moments(const AdamArgs &a, int dtype, void *m, void *v, cudaStream_t stream);
+
+// Partial sums that the norm writes (binary64).
+constexpr int kNormParts = 148 * 4;
+cudaError_t launch_adamw_norm(const AdamArgs &a, double max_norm, double *parts, float *out, cudaStream_t stream);
+
+}  // namespace gq

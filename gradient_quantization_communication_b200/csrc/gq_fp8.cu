@@ -1,0 +1,336 @@
+// gq_fp8.cu -- packing matrices into 8-bit floating point along their rows and columns, and back.
+#include "gq_act.cuh"
+#include "gq_device.cuh"
+#include "gq_fp8.cuh"
+#include "gq_fp8.h"
+
+namespace gq {
+namespace {
+
+// A packed matrix in memory.
+struct Packed {
+    uint8_t *codes, *exps;
+    int64_t code_pitch, exp_pitch;
+    int blocks;  // of a row
+};
+Packed packed_of(void *p, int tile, int64_t rows, int64_t cols)
+{
+    const Fp8Layout l = fp8_layout(tile, rows, cols);
+    uint8_t *b = static_cast<uint8_t *>(p);
+    return Packed{b, b ? b + l.exps_off : nullptr, l.code_pitch, l.exp_pitch, (int)((cols + 127) / 128)};
+}
+
+struct Params {
+    const void *x;
+    int64_t sx, rows;
+    int cols, per_row;  // chunks of 256 columns a row
+    Packed p, t;        // along the rows, along the columns
+};
+
+// Largest absolute values: bits of binary32, or two 16-bit patterns in a word, which order like integers.
+template <typename T>
+__device__ __forceinline__ uint32_t abs_word(uint32_t w)
+{
+    return w & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b)
+{
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    else return max_u16x2(a, b);
+}
+// Binary32 bits of a pattern (the low 16 bits of a word for 16-bit types).
+template <typename T>
+__device__ __forceinline__ uint32_t float_bits(uint32_t b)
+{
+    if constexpr (sizeof(T) == 4) return b;
+    else if constexpr (__is_same(T, __half)) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)b)));
+    else return b << 16;
+}
+// Of a lane's words of one row: the largest of the 128 columns that its 16 lanes hold, as binary32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t row_max(const Words<T> &w)
+{
+    uint32_t m = abs_word<T>(w.w[0]);
+#pragma unroll
+    for (int i = 1; i < (int)(2 * sizeof(T)); ++i) m = max_word<T>(m, abs_word<T>(w.w[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_word<T>(m, __shfl_xor_sync(kFull, m, o));
+    return float_bits<T>(sizeof(T) == 4 ? m : max(m & 0xffffu, m >> 16));
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t E)
+{
+    const float inv = fp8_inverse(E);
+    return make_uint2(fp8_codes4<FMT>(v[0], v[1], v[2], v[3], inv, E), fp8_codes4<FMT>(v[4], v[5], v[6], v[7], inv, E));
+}
+
+// A lane's 8 codes of a row, its block's exponent, and, behind the row's last block, the exponents' padding.
+__device__ __forceinline__ void store_row(const Packed &p, int64_t row, int64_t exp_row, int base, int lane, uint2 q, uint32_t E,
+                                          bool exps)
+{
+    const int c = base + lane * 8;
+    if (c >= p.code_pitch) return;
+    *reinterpret_cast<uint2 *>(p.codes + row * p.code_pitch + c) = q;
+    if (exps && (lane & 15) == 0) {
+        uint8_t *e = p.exps + exp_row * p.exp_pitch;
+        const int b = c >> 7;
+        e[b] = (uint8_t)E;
+        if (b + 1 == p.blocks)
+            for (int i = b + 1; i < p.exp_pitch; ++i) e[i] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Along the rows only: a warp takes 256 columns of a row at a time.
+// ---------------------------------------------------------------------------------------------
+template <typename T, int FMT, bool AL>
+__global__ void __launch_bounds__(256) k_pack_rows(const __grid_constant__ Params p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t n = p.rows * p.per_row, warps = (int64_t)gridDim.x * 8;
+    for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += warps) {
+        const int64_t row = id / p.per_row;
+        const int base = (int)(id - row * p.per_row) * kChunk;
+        const T *const x = static_cast<const T *>(p.x) + row * p.sx;
+        Raw<T, AL> r;
+        chunk_load<T, AL>(r, x, base, lane, p.cols);
+        const Words<T> w = in_place<T, AL>(r, x);
+        const uint32_t E = fp8_exp<FMT>(row_max<T>(w));
+        float v[8];
+        to_floats(w, v);
+        store_row(p.p, row, row, base, lane, codes8<FMT>(v, E), E, true);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// 128 rows x 256 columns a block: along the columns, along both, and square tiles.  A warp takes 8 rows, a lane 8
+// columns of them, so that a lane's 8 codes of a column are one 8-byte piece of the transpose.
+// ---------------------------------------------------------------------------------------------
+constexpr int kTileWarps = 16;
+
+template <typename T, int FMT, bool TILE, bool AL>
+__global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_constant__ Params p)
+{
+    constexpr int W = 2 * (int)sizeof(T);  // words of a lane's 8 columns
+    __shared__ __align__(16) uint8_t codes[kChunk * kBlock];  // transposed codes; before that, the warps' largest values
+    __shared__ uint8_t exps[kChunk];                          // of every column (TILE: the first two, of the two tiles)
+    uint32_t *const most = reinterpret_cast<uint32_t *>(codes);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t tile = blockIdx.x / p.per_row;
+    const int base = (int)(blockIdx.x - tile * p.per_row) * kChunk;
+    const int64_t row0 = tile * kBlock + warp * 8;
+
+    Words<T> w[8];
+    {
+        Raw<T, AL> r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const T *const x = static_cast<const T *>(p.x) + (row0 + i) * p.sx;
+            if (row0 + i < p.rows) {
+                chunk_load<T, AL>(r[i], x, base, lane, p.cols);
+            } else {
+#pragma unroll
+                for (int k = 0; k < (int)(sizeof(r[i].w) / 4); ++k) r[i].w[k] = 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = in_place<T, AL>(r[i], static_cast<const T *>(p.x) + (row0 + i) * p.sx);
+    }
+
+    uint32_t col[W];  // largest of the warp's rows
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        col[k] = abs_word<T>(w[0].w[k]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) col[k] = max_word<T>(col[k], abs_word<T>(w[i].w[k]));
+    }
+    if constexpr (TILE) {
+        Words<T> c;
+#pragma unroll
+        for (int k = 0; k < W; ++k) c.w[k] = col[k];
+        const uint32_t m = row_max<T>(c);
+        if ((lane & 15) == 0) most[warp * 2 + (lane >> 4)] = m;
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) most[(warp * W + k) * 32 + lane] = col[k];
+    }
+    __syncthreads();
+    uint32_t E = 0;
+    if constexpr (TILE) {
+        if (threadIdx.x < 2) {
+            uint32_t m = 0;
+            for (int i = 0; i < kTileWarps; ++i) m = max(m, most[i * 2 + threadIdx.x]);
+            E = fp8_exp<FMT>(m);
+        }
+    } else if (threadIdx.x < kChunk) {
+        // column 8 l + j of the chunk: word j (or half of word j / 2) of lane l
+        const int l = threadIdx.x >> 3, j = threadIdx.x & 7;
+        uint32_t m = 0;
+        for (int i = 0; i < kTileWarps; ++i)
+            m = max_word<T>(m, most[(i * W + (sizeof(T) == 4 ? j : j >> 1)) * 32 + l]);
+        if (sizeof(T) == 2) m = (j & 1) ? m >> 16 : m & 0xffffu;
+        E = fp8_exp<FMT>(float_bits<T>(m));
+    }
+    if (threadIdx.x < (TILE ? 2 : kChunk)) {
+        exps[threadIdx.x] = (uint8_t)E;
+        if (p.t.codes) {
+            // the transpose's row: the column (TILE: 128 of them), its block: this one's rows
+            const int64_t r = TILE ? base / kBlock + threadIdx.x : base + threadIdx.x;
+            if (r < (TILE ? (p.cols + kBlock - 1) / kBlock : p.cols)) {
+                uint8_t *e = p.t.exps + r * p.t.exp_pitch;
+                e[tile] = (uint8_t)E;
+                if (tile + 1 == p.t.blocks)
+                    for (int64_t i = tile + 1; i < p.t.exp_pitch; ++i) e[i] = 0;
+            }
+        }
+    }
+    __syncthreads();
+
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) to_floats(w[i], v[i]);
+    if (p.p.codes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t e = TILE ? exps[lane >> 4] : fp8_exp<FMT>(row_max<T>(w[i]));
+            const uint2 q = codes8<FMT>(v[i], e);
+            if (row0 + i < p.rows) store_row(p.p, row0 + i, TILE ? tile : row0 + i, base, lane, q, e, !TILE || (warp == 0 && i == 0));
+        }
+    }
+    if (!p.t.codes) return;
+    // Piece `warp` (8 rows) of column c lies at piece warp ^ (c / 8 mod 16) of its 128 bytes: the 16 lanes of half a
+    // warp, 8 columns apart, then store to different banks.
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = lane * 8 + j;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v[i][j];
+        const uint32_t e = exps[TILE ? lane >> 4 : c];
+        *reinterpret_cast<uint2 *>(codes + c * kBlock + ((warp ^ (lane & 15)) << 3)) = codes8<FMT>(x, e);
+    }
+    __syncthreads();
+    // 16-byte pieces, two of 8, in order; a column's 128 bytes by 8 lanes
+    for (int i = threadIdx.x; i < kChunk * 8; i += kTileWarps * 32) {
+        const int c = i >> 3, f = (c >> 3) & 15, piece = (i & 7) * 2;
+        if (base + c >= p.cols) break;
+        uint4 q = *reinterpret_cast<const uint4 *>(codes + c * kBlock + (((piece ^ f) & 14) << 3));
+        if (f & 1) q = make_uint4(q.z, q.w, q.x, q.y);
+        *reinterpret_cast<uint4 *>(p.t.codes + (int64_t)(base + c) * p.t.code_pitch + tile * kBlock + piece * 8) = q;
+    }
+}
+
+template <typename T, int FMT, bool TILE, bool AL>
+__global__ void __launch_bounds__(256) k_unpack(const __grid_constant__ Params p, T *out)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t n = p.rows * p.per_row, warps = (int64_t)gridDim.x * 8;
+    for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += warps) {
+        const int64_t row = id / p.per_row;
+        const int base = (int)(id - row * p.per_row) * kChunk, c = base + lane * 8;
+        uint2 q = make_uint2(0u, 0u);
+        uint32_t E = 0;
+        if (c < p.cols) {
+            q = __ldg(reinterpret_cast<const uint2 *>(p.p.codes + row * p.p.code_pitch + c));
+            E = __ldg(p.p.exps + (TILE ? row / kBlock : row) * p.p.exp_pitch + (c >> 7));
+        }
+        float v[8];
+        fp8_decode8<FMT>(q, fp8_scale(E), v);
+        saturate<T>(v);
+        Words<T> w;
+        from_floats(w, v);
+        chunk_store<T, AL>(w, out + row * p.sx, base, lane, p.cols);
+    }
+}
+
+template <typename T>
+bool rows_aligned(const Params &p) { return p.rows <= 1 || p.sx % (16 / (int64_t)sizeof(T)) == 0; }
+
+unsigned warp_grid(const Params &p)
+{
+    const int64_t need = (p.rows * p.per_row + 7) / 8;
+    return (unsigned)(need < 148 * 16 ? need : 148 * 16);
+}
+
+template <typename T, int FMT>
+cudaError_t pack(const Params &p, int tile, cudaStream_t s)
+{
+    const bool al = rows_aligned<T>(p);
+    if (!tile && !p.t.codes) {
+        if (al) k_pack_rows<T, FMT, true><<<warp_grid(p), 256, 0, s>>>(p);
+        else k_pack_rows<T, FMT, false><<<warp_grid(p), 256, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    const int64_t blocks = (p.rows + kBlock - 1) / kBlock * p.per_row;
+    if (blocks > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)blocks, threads = kTileWarps * 32;
+    if (tile) {
+        if (al) k_pack_tile<T, FMT, true, true><<<grid, threads, 0, s>>>(p);
+        else k_pack_tile<T, FMT, true, false><<<grid, threads, 0, s>>>(p);
+    } else {
+        if (al) k_pack_tile<T, FMT, false, true><<<grid, threads, 0, s>>>(p);
+        else k_pack_tile<T, FMT, false, false><<<grid, threads, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T, int FMT>
+cudaError_t unpack(const Params &p, int tile, T *out, cudaStream_t s)
+{
+    const bool al = rows_aligned<T>(p);
+    if (tile) {
+        if (al) k_unpack<T, FMT, true, true><<<warp_grid(p), 256, 0, s>>>(p, out);
+        else k_unpack<T, FMT, true, false><<<warp_grid(p), 256, 0, s>>>(p, out);
+    } else {
+        if (al) k_unpack<T, FMT, false, true><<<warp_grid(p), 256, 0, s>>>(p, out);
+        else k_unpack<T, FMT, false, false><<<warp_grid(p), 256, 0, s>>>(p, out);
+    }
+    return cudaGetLastError();
+}
+
+Params params_of(const Fp8PackArgs &a)
+{
+    Params p = {};
+    p.x = a.x.p;
+    p.sx = a.rows > 1 ? a.x.stride : 0;
+    p.rows = a.rows;
+    p.cols = (int)a.cols;
+    p.per_row = (int)((a.cols + kChunk - 1) / kChunk);
+    p.p = packed_of(a.packed, a.tile, a.rows, a.cols);
+    p.t = packed_of(a.packed_t, a.tile, a.cols, a.rows);
+    return p;
+}
+
+template <typename T>
+cudaError_t pack_type(const Fp8PackArgs &a, cudaStream_t s)
+{
+    const Params p = params_of(a);
+    return a.format == GQ_FP8_E4M3 ? pack<T, GQ_FP8_E4M3>(p, a.tile, s) : pack<T, GQ_FP8_E5M2>(p, a.tile, s);
+}
+template <typename T>
+cudaError_t unpack_type(const Fp8PackArgs &a, cudaStream_t s)
+{
+    const Params p = params_of(a);
+    T *const out = static_cast<T *>(const_cast<void *>(a.x.p));
+    return a.format == GQ_FP8_E4M3 ? unpack<T, GQ_FP8_E4M3>(p, a.tile, out, s) : unpack<T, GQ_FP8_E5M2>(p, a.tile, out, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_pack(const Fp8PackArgs &a, cudaStream_t s)
+{
+    if (a.dtype == GQ_FLOAT32) return pack_type<float>(a, s);
+    if (a.dtype == GQ_BFLOAT16) return pack_type<__nv_bfloat16>(a, s);
+    return pack_type<__half>(a, s);
+}
+
+cudaError_t launch_fp8_unpack(const Fp8PackArgs &a, cudaStream_t s)
+{
+    if (a.dtype == GQ_FLOAT32) return unpack_type<float>(a, s);
+    if (a.dtype == GQ_BFLOAT16) return unpack_type<__nv_bfloat16>(a, s);
+    return unpack_type<__half>(a, s);
+}
+
+}  // namespace gq

@@ -21,6 +21,8 @@ SCHEMES = {"qsgd": GQ_QSGD, "terngrad": GQ_TERNGRAD, "bingrad_b": GQ_BINGRAD_B,
 
 GQ_FLOAT32, GQ_BFLOAT16, GQ_FLOAT16 = range(3)
 GQ_FN_GELU, GQ_FN_GELU_TANH, GQ_FN_SILU = range(3)
+GQ_FP8_E4M3, GQ_FP8_E5M2 = range(2)
+FP8_FORMATS = {"e4m3": GQ_FP8_E4M3, "e5m2": GQ_FP8_E5M2}
 FUNCTIONS = {"gelu": GQ_FN_GELU, "gelu_tanh": GQ_FN_GELU_TANH, "silu": GQ_FN_SILU}
 
 
@@ -28,6 +30,21 @@ class gq_config_t(ctypes.Structure):
     _fields_ = [("scheme", ctypes.c_int32), ("levels", ctypes.c_int32), ("bucket", ctypes.c_int32),
                 ("workers", ctypes.c_int32), ("error_feedback", ctypes.c_int32),
                 ("clip_sigma", ctypes.c_float), ("seed", ctypes.c_uint64), ("n", ctypes.c_int64)]
+
+
+class gq_adamw_config_t(ctypes.Structure):
+    _fields_ = [("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("seed", ctypes.c_uint64)]
+
+
+class gq_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float)]
+
+
+class gq_adamw_scalars_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("inv1", ctypes.c_float), ("inv2", ctypes.c_float), ("step", ctypes.c_uint32)]
 
 
 class GQError(RuntimeError):
@@ -84,6 +101,20 @@ def lib():
         L.gq_layer_norm_workspace.argtypes = [i64, i64, ctypes.POINTER(sz)]
         L.gq_layer_norm_backward.argtypes = [ci, ci, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, ci, vp,
                                              sz, vp]
+        L.gq_fp8_layout.argtypes = [ci, i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.gq_fp8_pack.argtypes = [ci, ci, ci, i64, i64, vp, i64, vp, vp, vp]
+        L.gq_fp8_unpack.argtypes = [ci, ci, ci, i64, i64, vp, vp, i64, vp]
+        L.gq_fp8_matmul_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+        L.gq_fp8_matmul.argtypes = [ci, i64, i64, i64, ci, ci, vp, ci, ci, vp, vp, vp, i64, ci, vp, sz, vp]
+        f64 = ctypes.c_double
+        L.gq_adamw_layout.argtypes = [i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.gq_adamw_create.argtypes = [ctypes.POINTER(gq_adamw_config_t), ctypes.POINTER(gq_adamw_tensor_t), ci,
+                                      ctypes.POINTER(vp)]
+        L.gq_adamw_destroy.argtypes = [vp]
+        L.gq_adamw_norm.argtypes = [vp, f64, vp, vp]
+        L.gq_adamw_scalars.argtypes = [f64, f64, f64, i64, ctypes.POINTER(gq_adamw_scalars_t)]
+        L.gq_adamw_step.argtypes = [vp, f64, f64, f64, f64, i64, vp, vp, vp]
+        L.gq_adamw_moments.argtypes = [vp, ci, vp, vp, vp]
         L.gq_status_string.argtypes = [ctypes.c_int]
         L.gq_status_string.restype = ctypes.c_char_p
         L.gq_version.restype = ctypes.c_char_p
@@ -94,7 +125,10 @@ def lib():
                   "gq_entropy_unpack", "gq_elias_layout", "gq_elias_used_bytes", "gq_elias_pack",
                   "gq_elias_unpack", "gq_act_layout", "gq_act_pack", "gq_act_unpack", "gq_act_fn_forward",
                   "gq_act_fn_backward", "gq_act_weight_grad_workspace", "gq_act_weight_grad",
-                  "gq_layer_norm_forward", "gq_layer_norm_workspace", "gq_layer_norm_backward"):
+                  "gq_layer_norm_forward", "gq_layer_norm_workspace", "gq_layer_norm_backward", "gq_fp8_layout",
+                  "gq_fp8_pack", "gq_fp8_unpack", "gq_fp8_matmul_workspace", "gq_fp8_matmul", "gq_adamw_layout",
+                  "gq_adamw_create", "gq_adamw_destroy", "gq_adamw_norm", "gq_adamw_scalars", "gq_adamw_step",
+                  "gq_adamw_moments"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -468,6 +502,233 @@ def gq_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumula
             (dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace), dt, pdt, rows, cols, pdy, sdy, px, sx, pk, _vector(gamma, "gamma", cols, pdt), _vector(mean, "mean", rows),
             _vector(rstd, "rstd", rows), pdx, sdx, _vector(dgamma, "dgamma", cols), _vector(dbeta, "dbeta", cols),
             int(bool(accumulate)), pws, nws)
+
+
+def _format(fmt):
+    f = FP8_FORMATS.get(fmt, fmt)
+    if f not in (GQ_FP8_E4M3, GQ_FP8_E5M2):
+        raise ValueError("fmt: one of %s expected, got %r" % (sorted(FP8_FORMATS), fmt))
+    return f
+
+
+def _fp8_bytes(tile, rows, cols):
+    return ((rows * ((cols + 127) // 128 * 128) + 15) // 16 * 16
+            + (((rows + 127) // 128 if tile else rows) * ((cols + 511) // 512 * 4) + 15) // 16 * 16)
+
+
+def _packed(t, what, tile, rows, cols):
+    """Pointer of the packed form of rows x cols values (None: NULL)."""
+    if t is None:
+        return None
+    need = _fp8_bytes(tile, rows, cols)
+    if t.element_size() != 1 or t.dim() != 1 or t.shape[0] < need or not t.is_contiguous():
+        raise ValueError("%s: a contiguous uint8 vector of at least %d bytes expected, got %s of shape %s"
+                         % (what, need, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def gq_fp8_layout(rows, cols, tile=False):
+    """(bytes, codes_off, exps_off) of the packed form of rows x cols values."""
+    b, c, e = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().gq_fp8_layout(int(bool(tile)), rows, cols, ctypes.byref(b), ctypes.byref(c), ctypes.byref(e)),
+           "gq_fp8_layout")
+    return b.value, c.value, e.value
+
+
+def gq_fp8_pack(x, packed=None, packed_t=None, fmt="e4m3", tile=False, stream=None):
+    """x (2-D) into packed (a uint8 vector) and its transpose into packed_t; either may be None.  fmt: "e4m3",
+    "e5m2" or the C constant; tile: one exponent for 128 x 128 values instead of 128 of a row."""
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+    tile = int(bool(tile))
+    _launch(lib().gq_fp8_pack, "gq_fp8_pack", stream, (x, packed, packed_t), _dtype(x, "x"), _format(fmt), tile, rows,
+            cols, px, sx, _packed(packed, "packed", tile, rows, cols), _packed(packed_t, "packed_t", tile, cols, rows))
+
+
+def gq_fp8_unpack(packed, x, fmt="e4m3", tile=False, stream=None):
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+    tile = int(bool(tile))
+    _launch(lib().gq_fp8_unpack, "gq_fp8_unpack", stream, (x, packed), _dtype(x, "x"), _format(fmt), tile, rows, cols,
+            _packed(packed, "packed", tile, rows, cols), px, sx)
+
+
+def _fp8_matmul_bytes(m, n, k):
+    b = ctypes.c_size_t()
+    _check(lib().gq_fp8_matmul_workspace(m, n, k, ctypes.byref(b)), "gq_fp8_matmul_workspace")
+    return b.value
+
+
+def gq_fp8_matmul_workspace(k, y):
+    """A workspace tensor for gq_fp8_matmul over k columns into a tensor of y's size (None if it needs none)."""
+    return _workspace(_fp8_matmul_bytes(y.shape[0], y.shape[1], k), y.device)
+
+
+def gq_fp8_matmul(a, b, k, y, bias=None, fmt=("e4m3", "e4m3"), tile=(False, False), accumulate=False, workspace=None,
+                  stream=None):
+    """y (m, n) = a b^T + bias, a and b the packed forms of (m, k) and (n, k) values; fmt, tile: of a and of b.
+    bias: a float32 vector.  Without a workspace one is allocated."""
+    py, sy = _matrix(y, "y")
+    m, n = y.shape
+    ta, tb = int(bool(tile[0])), int(bool(tile[1]))
+    if workspace is None:
+        workspace = _workspace(_fp8_matmul_bytes(m, n, k), y.device, stream)
+    pws, nws = _space(workspace, "gq_fp8_matmul")
+    _launch(lib().gq_fp8_matmul, "gq_fp8_matmul", stream, (y, a, b, bias, workspace), _dtype(y, "y"), m, n, k,
+            _format(fmt[0]), ta, _packed(a, "a", ta, m, k), _format(fmt[1]), tb, _packed(b, "b", tb, n, k),
+            _vector(bias, "bias", n), py, sy, int(bool(accumulate)), pws, nws)
+
+
+def gq_adamw_layout(n):
+    """(bytes, exps_off) of a moment of n elements in 8 bits."""
+    b, e = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().gq_adamw_layout(n, ctypes.byref(b), ctypes.byref(e)), "gq_adamw_layout")
+    return b.value, e.value
+
+
+class _AdamWHandle(ctypes.c_void_p):
+    """A gq_adamw_t, with its device's index and the elements of all its tensors."""
+
+
+def gq_adamw_create(params, grads, ms, vs, masters=None, weight_decay=0.0, lr_scale=1.0, state_bits=32, seed=0):
+    """The optimizer of lists of contiguous tensors.  ms, vs: float32 tensors, or uint8 vectors of gq_adamw_layout
+    bytes (state_bits = 8).  weight_decay, lr_scale: a number, or one for each tensor.  The tensors must outlive it."""
+    count = len(params)
+    lists = {"grads": grads, "ms": ms, "vs": vs, "masters": masters}
+    for what, ts in lists.items():
+        if ts is not None and len(ts) != count:
+            raise ValueError("%s: %d tensors expected, got %d" % (what, count, len(ts)))
+    per = {"weight_decay": weight_decay, "lr_scale": lr_scale}
+    for what, v in per.items():
+        per[what] = [float(v)] * count if isinstance(v, (int, float)) else [float(x) for x in v]
+        if len(per[what]) != count:
+            raise ValueError("%s: %d values expected, got %d" % (what, count, len(per[what])))
+    device = params[0].device if count else None
+    bits = int(state_bits)
+    array = (gq_adamw_tensor_t * count)()
+    total = 0
+    for i in range(count):
+        p, g, m, v = params[i], grads[i], ms[i], vs[i]
+        x = masters[i] if masters is not None else None
+        n = p.numel()
+        total += n
+        for what, t in (("params", p), ("grads", g), ("ms", m), ("vs", v), ("masters", x)):
+            if t is None:
+                continue
+            if t.device != device or device.type != "cuda":
+                raise ValueError("%s[%d]: CUDA tensors of one device expected, got %s" % (what, i, t.device))
+            if not t.is_contiguous():
+                raise ValueError("%s[%d]: a contiguous tensor expected, got strides %s" % (what, i, t.stride()))
+        if _dtype(p, "params[%d]" % i) != _dtype(params[0], "params") or _dtype(g, "grads[%d]" % i) != _dtype(grads[0], "grads"):
+            raise TypeError("tensor %d: its type differs from the first one's" % i)
+        if g.numel() != n or (x is not None and (x.numel() != n or _dtype(x, "masters[%d]" % i) != GQ_FLOAT32)):
+            raise ValueError("tensor %d: a gradient (and float32 master copy) of %d values expected" % (i, n))
+        for what, t in (("ms", m), ("vs", v)):
+            if bits == 8:
+                if t.element_size() != 1 or t.numel() < gq_adamw_layout(n)[0]:
+                    raise ValueError("%s[%d]: a uint8 vector of %d bytes expected" % (what, i, gq_adamw_layout(n)[0]))
+            elif t.numel() != n or _dtype(t, "%s[%d]" % (what, i)) != GQ_FLOAT32:
+                raise ValueError("%s[%d]: %d float32 values expected" % (what, i, n))
+        ptr = [t.data_ptr() if t is not None else None for t in (p, g, x, m, v)]
+        array[i] = gq_adamw_tensor_t(*ptr, n, per["weight_decay"][i], per["lr_scale"][i])
+    cfg = gq_adamw_config_t(_dtype(params[0], "params") if count else GQ_FLOAT32,
+                            _dtype(grads[0], "grads") if count else GQ_FLOAT32, bits, int(seed))
+    h = _AdamWHandle()
+    import torch
+    h.device = device.index if count else torch.cuda.current_device()
+    h.total = total
+    with torch.cuda.device(h.device):
+        _check(lib().gq_adamw_create(ctypes.byref(cfg), array, count, ctypes.byref(h)), "gq_adamw_create")
+    return h
+
+
+def gq_adamw_destroy(opt):
+    _check(lib().gq_adamw_destroy(opt), "gq_adamw_destroy")
+
+
+def _adamw_call(fn, what, opt, stream, tensors, *args):
+    import torch
+    for t in tensors:
+        if t is not None and t.get_device() != opt.device:
+            raise ValueError("%s: tensors on cuda:%d expected, got %s" % (what, opt.device, t.device))
+    if stream is None:
+        stream = torch.cuda.current_stream(opt.device).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == opt.device:
+        st = fn(opt, *args, stream)
+    else:
+        with torch.cuda.device(opt.device):
+            st = fn(opt, *args, stream)
+    _check(st, what)
+
+
+def gq_adamw_norm(opt, max_norm, out, stream=None):
+    """out: two float32 values, the gradients' norm and the clipping factor."""
+    _adamw_call(lib().gq_adamw_norm, "gq_adamw_norm", opt, stream, (out,), float(max_norm), _vector(out, "out", 2))
+
+
+def gq_adamw_scalars(lr, beta1, beta2, step):
+    """The 16 bytes that a step reads from device memory in the place of lr and step (a CPU uint8 tensor)."""
+    import torch
+    s = gq_adamw_scalars_t()
+    _check(lib().gq_adamw_scalars(float(lr), float(beta1), float(beta2), int(step), ctypes.byref(s)), "gq_adamw_scalars")
+    return torch.frombuffer(bytearray(bytes(s)), dtype=torch.uint8)
+
+
+def gq_adamw_step(opt, lr, beta1, beta2, eps, step, scale=None, scalars=None, stream=None):
+    """scale: one float32 value that multiplies the gradients; scalars: 16 bytes (gq_adamw_scalars), both on the device."""
+    if scalars is not None and (scalars.numel() * scalars.element_size() != 16 or not scalars.is_contiguous()):
+        raise ValueError("scalars: 16 contiguous bytes expected, got shape %s of %s" % (tuple(scalars.shape), scalars.dtype))
+    if scale is not None and (scale.numel() != 1 or _dtype(scale, "scale") != GQ_FLOAT32):
+        raise ValueError("scale: one float32 value expected, got shape %s of %s" % (tuple(scale.shape), scale.dtype))
+    _adamw_call(lib().gq_adamw_step, "gq_adamw_step", opt, stream, (scale, scalars), float(lr), float(beta1), float(beta2),
+                float(eps), int(step), _ptr(scale), _ptr(scalars))
+
+
+def gq_adamw_moments(opt, m=None, v=None, stream=None):
+    """The moments' values, all tensors one after another, into vectors of one type (either may be None)."""
+    some = m if m is not None else v
+    if some is None:
+        raise ValueError("gq_adamw_moments: at least one of m and v expected")
+    dt = _dtype(some, "m")
+    _adamw_call(lib().gq_adamw_moments, "gq_adamw_moments", opt, stream, (m, v), dt, _vector(m, "m", opt.total, dt),
+                _vector(v, "v", opt.total, dt))
+
+
+class AdamW:
+    """Owner of a gq_adamw_t and of references to its tensors (destroyed on close / exit of a ``with`` block)."""
+
+    def __init__(self, params, grads, ms, vs, masters=None, weight_decay=0.0, lr_scale=1.0, state_bits=32, seed=0):
+        self.handle = None
+        self.tensors = (list(params), list(grads), list(ms), list(vs), None if masters is None else list(masters))
+        self.handle = gq_adamw_create(*self.tensors, weight_decay, lr_scale, state_bits, seed)
+
+    def norm(self, max_norm, out, stream=None):
+        gq_adamw_norm(self.handle, max_norm, out, stream)
+
+    def step(self, lr, beta1, beta2, eps, step, scale=None, scalars=None, stream=None):
+        gq_adamw_step(self.handle, lr, beta1, beta2, eps, step, scale, scalars, stream)
+
+    def moments(self, m=None, v=None, stream=None):
+        gq_adamw_moments(self.handle, m, v, stream)
+
+    def close(self):
+        if self.handle:
+            gq_adamw_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def gq_status_string(status):

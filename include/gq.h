@@ -459,6 +459,156 @@ GQ_API gq_status_t gq_layer_norm_backward(int dtype, int param_dtype, int64_t ro
                                           int64_t dx_stride, float *dgamma, float *dbeta, int accumulate, void *workspace,
                                           size_t workspace_bytes, void *stream);
 
+/*
+ * Matrices in 8-bit floating point, and a linear layer's products from them.
+ *
+ * With y = x W^T + b the forward pass, the input's gradient dx = dy W and the weight's gradient
+ * dW = dy^T x are products of two matrices along their rows, when each operand is packed along the
+ * axis that the product sums over.  gq_fp8_pack packs a matrix along its rows, along its columns, or
+ * both in one pass; gq_fp8_matmul multiplies.  (gq_act_weight_grad computes dW from the checkpoint
+ * instead, whose 7 bits and groups of 32 keep more.)  There is no counterpart in the pages.
+ *
+ * The conventions of the section on activations hold (stateless; matrices, strides, alignment, overlap;
+ * fixed order of sums; NaN where a bounded wait gives up).
+ */
+
+/*
+ * Layout of the packed form of rows x cols values (host computation; outputs may be NULL).
+ * A block is 128 columns of a row (tile = 0), or of 128 rows (tile = 1); the last ones may be cut.
+ * codes_off = 0: rows of code bytes, each padded with 0 to whole blocks (pitch 128 * ceil(cols / 128)
+ * bytes).  exps_off (16-byte aligned): rows of exponent bytes, one a block, for every row (tile = 0) or
+ * every 128 rows (tile = 1), each padded with 0 to a multiple of four (pitch 4 * ceil(cols / 512)).
+ * Value of code c under exponent E: c * 2^(E - 127), c in the format's own value; E = 255: NaN.
+ *   GQ_FP8_E4M3  4 exponent and 3 mantissa bits, largest 448, smallest 2^-9, NaN 0x7f and 0xff;
+ *   GQ_FP8_E5M2  5 and 2, largest finite 57344, smallest 2^-16, infinities and NaN.
+ * E is the smallest with max |x| <= 1.75 * 2^(8 or 15) * 2^(E - 127) over the block, at least 10; codes
+ * are rounded to nearest, ties to even.  Every value is exact in bfloat16 and float32.  A block with a NaN
+ * or an infinity has E = 255 and codes 0x7f.
+ */
+typedef enum { GQ_FP8_E4M3 = 0, GQ_FP8_E5M2 = 1 } gq_fp8_t;
+GQ_API gq_status_t gq_fp8_layout(int tile, int64_t rows, int64_t cols, size_t *bytes, size_t *codes_off,
+                                 size_t *exps_off);
+
+/*
+ * x (rows x cols) -> its packed form, and the packed form of its transpose (cols x rows).
+ *   packed    device, gq_fp8_layout(tile, rows, cols) bytes, 16-byte aligned (NULL: not wanted);
+ *   packed_t  device, gq_fp8_layout(tile, cols, rows) bytes (NULL: not wanted; not both NULL);
+ *             rows <= GQ_ACT_MAX_COLS, and with rows = 0 packed_t must be NULL.
+ * The up to 15 bytes that round a region up to 16 are left as they were.
+ */
+GQ_API gq_status_t gq_fp8_pack(int dtype, int format, int tile, int64_t rows, int64_t cols, const void *x,
+                               int64_t x_stride, void *packed, void *packed_t, void *stream);
+/* Packed form -> x.  In float16 values are rounded and saturate at +-65504. */
+GQ_API gq_status_t gq_fp8_unpack(int dtype, int format, int tile, int64_t rows, int64_t cols, const void *packed, void *x,
+                                 int64_t x_stride, void *stream);
+
+/*
+ * y[i][j] = sum over c < k of a[i][c] * b[j][c]  + bias[j], i < m, j < n.
+ *   a, b       packed forms of m x k and n x k values, each with its own format and tile.
+ *   bias       n float32 values, 4-byte aligned (NULL: none).
+ *   y          m x n values of type dtype, rows y_stride apart; its element type's alignment is enough.
+ *   accumulate 1 adds to y (float32 only: GQ_ERR_UNSUPPORTED otherwise), 0 overwrites it.
+ *   workspace  device, at least gq_fp8_matmul_workspace bytes, 16-byte aligned; NULL if that is 0.  Its
+ *              contents do not outlive the call.
+ * m = 0 is a no-op; 1 <= n < 2^31, 1 <= k <= GQ_ACT_MAX_COLS.  Products are exact; sums are binary32, where
+ * the tensor cores cut off instead of rounding over runs of up to 1024 columns, and sums below 2^-126 may
+ * read as 0.  A row of y with a NaN block in its operands is NaN where the formula is.
+ */
+GQ_API gq_status_t gq_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes);
+GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int format_a, int tile_a, const void *a,
+                                 int format_b, int tile_b, const void *b, const float *bias, void *y, int64_t y_stride,
+                                 int accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * AdamW over many tensors at once: the step that takes the averaged gradient.
+ *
+ *   g = grad * scale                                      (scale: the clipping factor; 1 without one)
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr lr_scale weight_decay) - lr lr_scale / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in binary32, each operation rounded on its own; (1 - beta1), 1 / (1 - beta1^t) and 1 / sqrt(1 - beta2^t) are
+ * computed in binary64 and rounded once.
+ *
+ * Moments in 32 bits (state_bits = 32) are n float32 values each.  In 8 bits (state_bits = 8) each is
+ * gq_adamw_layout bytes, 16-byte aligned: a code byte an element, padded to whole blocks of 128, then one
+ * exponent byte a block, padded to a multiple of 16.  The step uses the moments as it computes them and
+ * keeps them as follows:
+ *   m  GQ_FP8_E4M3 codes and exponents exactly as gq_fp8_pack's blocks;
+ *   v  code 0: 0; code c > 0 under exponent E: (8 + c mod 8) * 2^(floor(c / 8) - 34 + E - 127).  E is the
+ *      smallest with max v <= 1.875 * 2^(E - 127) over the block, in [32, 254]; E = 255: NaN (codes 0).
+ *      v is rounded stochastically: up with the probability that its remainder has, from 16 random bits of
+ *      Philox4x32-10 (nearest values would keep v where it is for good: it decays by 0.1 % a step, a
+ *      code's step is 6 to 12 %).  Key: the seed.  Counter: (i / 8 low, high word; t; tensor's number in
+ *      the list + 2^31) for element i of its tensor; element i takes bits 16 (i mod 2) .. of word
+ *      (i mod 8) / 2, as a fraction of 2^16.  v > 0 keeps a code of at least 1.
+ * Zero bytes are moments of 0, as for a first step.
+ *
+ * The list of tensors is fixed by gq_adamw_create, which copies it to device memory that the optimizer owns
+ * (the only allocation); the tensors' memory stays the caller's and must outlive the optimizer.
+ *   param    n values of type param_dtype; grad: n values of grad_dtype, e.g. a slice of gq_fused_step's avg;
+ *   master   n float32 values that are updated in the parameters' place, param receiving them rounded;
+ *            NULL: none.  All tensors of a 16-bit type have one, or none has.
+ *   These, and moments in 32 bits, need their type's alignment only; 16 bytes are faster.
+ *   Tensors may share gradients; what a step writes may overlap nothing else that it reads or writes
+ *   (GQ_ERR_INVALID).  n = 0 is allowed; pointers may then be NULL.
+ * Calls on one optimizer must not overlap on the GPU, and must be made with its device current
+ * (GQ_ERR_INVALID).  Non-finite values pass through as in the formulas.
+ */
+typedef struct {
+    int32_t param_dtype, grad_dtype; /* gq_dtype_t */
+    int32_t state_bits;              /* 32 or 8 */
+    uint64_t seed;                   /* key of the random bits (state_bits = 8) */
+} gq_adamw_config_t;
+
+typedef struct {
+    void *param;
+    const void *grad;
+    float *master;
+    void *m, *v;
+    int64_t n;          /* 0 <= n < 2^40 */
+    float weight_decay; /* finite, >= 0 */
+    float lr_scale;     /* finite, >= 0; 1 for the step's own lr */
+} gq_adamw_tensor_t;
+
+typedef struct gq_adamw *gq_adamw_t; /* opaque; owned by the library */
+
+#define GQ_ADAMW_MAX_TENSORS (1 << 20)
+
+/* Bytes of a moment of n elements in 8 bits, and the offset of its exponents (outputs may be NULL). */
+GQ_API gq_status_t gq_adamw_layout(int64_t n, size_t *bytes, size_t *exps_off);
+
+GQ_API gq_status_t gq_adamw_create(const gq_adamw_config_t *cfg, const gq_adamw_tensor_t *tensors, int count,
+                                   gq_adamw_t *out);
+/* Frees the optimizer's own memory; waits for the device. */
+GQ_API gq_status_t gq_adamw_destroy(gq_adamw_t opt);
+
+/*
+ * out[0] = sqrt of the sum of grad^2 over all tensors, out[1] = min(1, max_norm / out[0]) (1 for a norm of 0; NaN
+ * if the norm is not finite), both summed in binary64 in a fixed order.  out: device, 2 floats, 4-byte aligned;
+ * max_norm > 0 (infinity: only the check that the gradients are finite).
+ */
+GQ_API gq_status_t gq_adamw_norm(gq_adamw_t opt, double max_norm, float *out, void *stream);
+
+/*
+ * One step.  t = step >= 1 (below 2^32); lr >= 0, eps >= 0 finite; 0 <= beta1, beta2 < 1.
+ *   scale    device, one float that multiplies the gradients, e.g. gq_adamw_norm's out + 1 (NULL: 1).  If it
+ *            is NaN the step changes nothing.
+ *   scalars  NULL, or device memory (16 bytes, 16-byte aligned) holding what gq_adamw_scalars gives, read when
+ *            the step runs in the place of lr and step: a captured step is replayed with new ones.
+ */
+typedef struct {
+    float lr;
+    float inv1;    /* 1 / (1 - beta1^t) */
+    float inv2;    /* 1 / sqrt(1 - beta2^t) */
+    uint32_t step; /* t */
+} gq_adamw_scalars_t;
+GQ_API gq_status_t gq_adamw_scalars(double lr, double beta1, double beta2, int64_t step, gq_adamw_scalars_t *out);
+GQ_API gq_status_t gq_adamw_step(gq_adamw_t opt, double lr, double beta1, double beta2, double eps, int64_t step,
+                                 const float *scale, const void *scalars, void *stream);
+
+/* The moments' values, all tensors one after another, in vectors of type dtype (device, 16-byte aligned; either
+ * may be NULL).  Moments in 8 bits are exact in bfloat16 and float32; float16 saturates at +-65504. */
+GQ_API gq_status_t gq_adamw_moments(gq_adamw_t opt, int dtype, void *m, void *v, void *stream);
+
 /* Static description of a status code. */
 GQ_API const char *gq_status_string(gq_status_t status);
 
