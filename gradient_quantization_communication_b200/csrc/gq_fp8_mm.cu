@@ -1,100 +1,728 @@
-// gq_fp8_mm.cu -- products of packed matrices of 8-bit floating point:
+// gq_fp8_mm.cu -- products of packed matrices of 8-bit floating point on the tensor cores:
 //   y[i][j] = sum over blocks b of 2^(Ea + Eb - 254) * sum over c in b of a[i][c] * b[j][c]  + bias[j].
 //
-// A block of 256 threads takes a tile of 64 x 64, 32 columns at a time, decoded to binary32 in shared memory; a
-// thread sums 4 x 4 of it on the ordinary cores.
+// The scales are powers of two, which tcgen05.mma (kind::mxf8f6f4, block_scale) takes as they are, one byte for every
+// 32 columns: a block's byte serves four MMAs, and the loop has no arithmetic besides them.  The M side of an MMA is
+// b (j, the features: a warp's 32 TMEM lanes are then adjacent columns of y), the N side is a (i, the tokens).  A
+// stage is 128 columns of both, K-major rows of 128 bytes with the 128-byte swizzle, fetched by TMA.  The exponents
+// of four stages (512 columns) are one word a row; four warps put them into TMEM, where row r's word belongs into
+// lane r mod 32 of column r / 32, once in each quarter of the lanes.
 #include "gq_act.cuh"
 #include "gq_device.cuh"
 #include "gq_fp8.cuh"
 #include "gq_fp8.h"
+#include "gq_internal.h"
+#include "gq_tc.cuh"
 
 namespace gq {
 namespace {
 
-struct Operand {
-    const uint8_t *codes, *exps;
-    int64_t rows, code_pitch, exp_pitch;
-    int format, shift;  // rows that share an exponent: 1 << shift
+// How a tile is made: by `group` CTAs (two share their operands), 128 * group features x tn tokens.
+template <int GROUP, int TN>
+struct Shape {
+    static constexpr int kGroup = GROUP, kTokens = TN, kFeatures = 128 * GROUP;
+    static constexpr int kUnits = 148 / GROUP;               // that run at once
+    static constexpr int kWBytes = 128 * 128, kXRows = TN / GROUP, kXBytes = kXRows * 128;
+    static constexpr int kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+    // TMEM: two accumulators of TN columns, then two buffers of exponents (4 columns for 128 features, TN / 32 but
+    // at least 4 for the tokens).  With 256 tokens they do not all fit into 512 columns, and the accumulators share 32.
+    static constexpr int kExpCols = 4 + (TN > 128 ? TN / 32 : 4);
+    static constexpr int kShared = TN > 128 ? 32 : 0;
+    static constexpr int kSecond = TN - kShared;             // the second accumulator's first column
+    static constexpr int kExps = kSecond + TN;
+};
+static_assert(Shape<2, 256>::kExps + 2 * Shape<2, 256>::kExpCols <= 512, "TMEM");
+
+constexpr int kThreads = 512;  // warps: 4 of control (copies, MMA, relay, idle), 8 of epilogue, 4 of exponents
+constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsEpi = 192, kRegsExp = 72;
+static_assert(4 * kRegsCtl + 8 * kRegsEpi + 4 * kRegsExp <= 16 * kRegsLaunch, "setmaxnreg: the shares come from the launch's registers");
+constexpr int kMaxUnits = 148;
+
+// How the tiles are spread over the units: whole rounds of a tile a unit first; the stages of the last, partial round's
+// tiles are one line, cut into `ranges` equal ranges, one a unit.  A range's part of a tile goes to the workspace, where a
+// second kernel joins them, unless it is the whole tile.
+struct Schedule {
+    int tiles_w, tiles_x;
+    int64_t whole;         // tiles of the whole rounds
+    int cut, ranges;       // tiles of the last one, and the ranges that they are cut into
+    int units, blocks;     // units launched; stages of a tile
+    int64_t start[kMaxUnits + 1];
+    uint8_t tile[kMaxUnits], from[kMaxUnits], to[kMaxUnits];
+};
+
+Schedule schedule(int units, int64_t features, int64_t tokens, int tw, int tx, int64_t k)
+{
+    Schedule s;
+    s.tiles_w = (int)((features + tw - 1) / tw);
+    s.tiles_x = (int)((tokens + tx - 1) / tx);
+    s.blocks = (int)((k + 127) / 128);
+    const int64_t tiles = (int64_t)s.tiles_w * s.tiles_x;
+    s.cut = (int)(tiles % units);
+    s.whole = tiles - s.cut;
+    s.ranges = s.cut;
+    if (s.cut) {
+        // A tile a unit, as many equal parts of every tile as there are units for, or equal ranges for all units.
+        const int64_t total = (int64_t)s.cut * s.blocks, most = total / 4 < units ? total / 4 : units;
+        double best = (double)s.blocks;
+        for (int64_t r = 2 * s.cut; r < most + s.cut; r += s.cut) {
+            if (r > most) r = most;
+            if (r <= s.cut) break;
+            const double parts = r % s.cut == 0 ? (double)r : (double)(s.cut + r - 1);
+            const double cost = (double)((total + r - 1) / r) + 0.1 * parts * tx / 256 + 4.0;
+            if (cost < best) {
+                best = cost;
+                s.ranges = (int)r;
+            }
+            if (r == most) break;
+        }
+    }
+    s.units = s.whole ? units : s.ranges;
+    const int64_t total = (int64_t)s.cut * s.blocks;
+    for (int p = 0; p <= s.ranges; ++p) s.start[p] = s.ranges ? total * p / s.ranges : 0;
+    for (int p = 0; p < s.ranges; ++p) s.tile[p] = (uint8_t)(s.start[p] / s.blocks);
+    for (int c = 0, p = 0; c < s.cut; ++c) {
+        while (s.start[p + 1] <= (int64_t)c * s.blocks) ++p;
+        s.from[c] = (uint8_t)p;
+        while (s.start[p + 1] < (int64_t)(c + 1) * s.blocks) ++p;
+        s.to[c] = (uint8_t)p;
+    }
+    return s;
+}
+// Partial tiles that the workspace holds: range p's part of tile c at c + p.
+int64_t part_tiles(const Schedule &s) { return s.ranges > s.cut ? s.cut + s.ranges - 1 : 0; }
+
+// An operand's exponents.
+struct Exps {
+    const uint8_t *p;
+    int64_t rows, pitch;
+    int shift;  // 1 << shift rows share one
 };
 
 struct Params {
-    Operand a, b;
-    int64_t k, sy;
+    CUtensorMap w, x;
+    Schedule s;
+    Exps ew, ex;
+    uint32_t idesc;     // without the exponents' byte numbers
+    int run;            // stages summed in TMEM before their sums are added to registers
+    int64_t tokens, features;
     const float *bias;
     void *y;
-    int accumulate, dtype;
-    int64_t tiles_n;
+    int64_t sy;
+    int accumulate;
+    float *parts;
+    long long limit;    // cycles after which a wait gives up
 };
 
-__device__ __forceinline__ float value(const Operand &o, int64_t row, int64_t c)
+struct Item {
+    int tw, tx;        // tile
+    int first, last;   // its stages
+    int part;          // partial tile in the workspace, -1: the whole tile
+};
+
+// Bands of 8 feature tiles, walked along the tokens: units that run together share their operands in L2.
+__device__ __forceinline__ void tile_place(const Schedule &s, int64_t tile, Item &it)
 {
-    if (row >= o.rows || c >= o.code_pitch) return 0.0f;
-    const uint32_t q = o.codes[row * o.code_pitch + c], E = o.exps[(row >> o.shift) * o.exp_pitch + (c >> 7)];
-    return (o.format == GQ_FP8_E4M3 ? fp8_values<GQ_FP8_E4M3>(q).x : fp8_values<GQ_FP8_E5M2>(q).x) * fp8_scale(E);
+    const int64_t band = (int64_t)8 * s.tiles_x;
+    const int64_t g = tile / band;
+    const int rest = (int)(tile - g * band);
+    const int wide = min(8, s.tiles_w - (int)g * 8);
+    it.tx = rest / wide;
+    it.tw = (int)g * 8 + rest - it.tx * wide;
 }
 
-__global__ void __launch_bounds__(256) k_simple(const __grid_constant__ Params p)
+__device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
 {
-    __shared__ float sa[64][33], sb[64][33];
-    const int64_t i0 = blockIdx.x / p.tiles_n * 64, j0 = blockIdx.x % p.tiles_n * 64;
-    const int ti = (threadIdx.x >> 4) * 4, tj = (threadIdx.x & 15) * 4;
-    float acc[4][4] = {};
-    for (int64_t c0 = 0; c0 < p.k; c0 += 32) {
-        for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-            sa[e >> 5][e & 31] = value(p.a, i0 + (e >> 5), c0 + (e & 31));
-            sb[e >> 5][e & 31] = value(p.b, j0 + (e >> 5), c0 + (e & 31));
-        }
-        __syncthreads();
-        for (int c = 0; c < 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(sa[ti + i][c], sb[tj + j][c], acc[i][j]);
-        __syncthreads();
+    int64_t tile;
+    if (i < s.whole) {
+        tile = i;
+        it.first = 0;
+        it.last = s.blocks;
+        it.part = -1;
+    } else {
+        // part m of unit p's range, which lies in the m-th tile that the range touches
+        const uint32_t j = (uint32_t)(i - s.whole), m = j / (uint32_t)s.units, p = j - m * (uint32_t)s.units;
+        if (p >= (uint32_t)s.ranges) return false;
+        const int64_t lo = s.start[p], hi = s.start[p + 1];
+        const int c = (int)(s.tile[p] + m);
+        const int64_t at = (int64_t)c * s.blocks;
+        it.first = (int)((lo > at ? lo : at) - at);
+        it.last = (int)((hi < at + s.blocks ? hi : at + s.blocks) - at);
+        if (it.first >= it.last) return false;
+        it.part = it.first == 0 && it.last == s.blocks ? -1 : c + (int)p;
+        tile = s.whole + c;
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t row = i0 + ti + i, col = j0 + tj + j;
-            if (row >= p.a.rows || col >= p.b.rows) continue;
-            float v = acc[i][j];
-            if (p.bias) v += p.bias[col];
-            const int64_t at = row * p.sy + col;
-            if (p.dtype == GQ_FLOAT32) {
-                float *y = static_cast<float *>(p.y) + at;
-                *y = p.accumulate ? *y + v : v;
-            } else if (p.dtype == GQ_BFLOAT16) {
-                static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
-            } else {
-                static_cast<__half *>(p.y)[at] = __float2half_rn(v);
+    tile_place(s, tile, it);
+    return true;
+}
+
+// Position in the ring of stages.  Every role sees every use of every stage, so a phase's parity names it.
+template <int N>
+struct Ring {
+    int st = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == N) {
+            st = 0;
+            ++turn;
+        }
+    }
+    __device__ __forceinline__ uint32_t parity() const { return turn & 1u; }
+    __device__ __forceinline__ uint32_t parity_before() const { return (turn & 1u) ^ 1u; }
+};
+
+// K-major rows of 128 bytes, 128-byte swizzle: groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::mxf8f6f4, D binary32, both operands K-major, exponents ue8m0.
+constexpr uint32_t instr_desc(int fw, int fx, int m, int n)
+{
+    return (uint32_t)fw << 7 | (uint32_t)fx << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(m >> 7) << 27;
+}
+// The byte of the exponents' words that counts.
+__device__ __forceinline__ uint32_t exp_byte(uint32_t b) { return b << 4 | b << 29; }
+
+template <int GROUP>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t ea, uint32_t eb, bool add)
+{
+    if constexpr (GROUP == 2)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d), "l"(a), "l"(b),
+            "r"(idesc), "r"(ea), "r"(eb), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d), "l"(a), "l"(b),
+            "r"(idesc), "r"(ea), "r"(eb), "r"((uint32_t)add)
+            : "memory");
+}
+// Arrives on the barrier (of both CTAs of a pair) once the MMAs issued so far are done.
+template <int GROUP>
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    if constexpr (GROUP == 2) commit_pair(bar);
+    else asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_store4(uint32_t addr, const uint32_t *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(addr)
+                 : "memory");
+}
+
+struct Shared {
+    unsigned long long full[8];       // this CTA's operands have arrived
+    unsigned long long peer_full[8];  // the other CTA's have (the leader's is used)
+    unsigned long long empty[8];      // the MMAs have read both
+    unsigned long long exp_full[2];   // the exponents of four stages are in TMEM, of both CTAs (the leader's)
+    unsigned long long exp_empty[2];  // the MMAs have read them
+    unsigned long long acc_full[2];   // a run's sums are complete
+    unsigned long long acc_empty[2];  // both CTAs have read them (the leader's)
+    unsigned long long edge[2];       // both CTAs have read the columns that the other accumulator shares (the leader's)
+    uint32_t tmem;
+};
+
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+// Where a lane's column of a tile goes: its feature of `count` tokens from token x0 of the tile on.
+template <typename T, class S>
+struct Out {
+    T *y;
+    float *part;      // the workspace, nullptr: y
+    int64_t sy;
+    int n;            // tokens that exist
+    float bias;
+    bool add, ok;
+
+    __device__ __forceinline__ Out(const Params &p, const Item &it, int x0, int count, int row, bool ok_) : sy(p.sy), ok(ok_)
+    {
+        const int64_t feature = (int64_t)it.tw * S::kFeatures + row, token = (int64_t)it.tx * S::kTokens + x0;
+        const int64_t left = p.tokens - token;
+        const bool in = feature < p.features;
+        part = it.part < 0 ? nullptr : p.parts + ((int64_t)it.part * S::kTokens + x0) * S::kFeatures + row;
+        n = in ? (int)(left < 0 ? 0 : left < count ? left : count) : 0;
+        y = static_cast<T *>(p.y) + token * sy + feature;
+        bias = p.bias && in && !part ? p.bias[feature] : 0.0f;
+        add = p.accumulate != 0;
+    }
+    // Tokens c .. c + 15; a wait that gave up (ok false) leaves NaN.
+    __device__ __forceinline__ void put16(float (&v)[16], int c) const
+    {
+        if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7fffffffu);
+        }
+        if (part) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < n) part[(c + j) * S::kFeatures] = v[j];
+            return;
+        }
+        T *const o = y + c * sy;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += bias;
+        if constexpr (sizeof(T) == 4) {
+            if (add) {
+                float old[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) old[j] = c + j < n ? o[j * sy] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += old[j];
             }
         }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (c + j < n) o[j * sy] = rounded<T>(v[j]);
+    }
+};
+
+// SUMS: runs' sums are added up in registers, rounded to nearest; else a tile is one run.
+template <typename T, int GROUP, int TN, bool SUMS>
+__global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Params p)
+{
+    using S = Shape<GROUP, TN>;
+    extern __shared__ unsigned char raw_smem[];
+    __shared__ Shared sh;
+    const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t rank = GROUP == 2 ? cluster_rank() : 0u;
+    const int64_t unit = blockIdx.x / GROUP, units = p.s.units;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.peer_full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.exp_full[i], 4 * GROUP);
+            mbar_init(&sh.exp_empty[i], 1);
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 8 * GROUP);
+            mbar_init(&sh.edge[i], 4 * GROUP);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        if constexpr (GROUP == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if constexpr (GROUP == 2) cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = sh.tmem;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        if (warp == 0 && lane == 0) {
+            // TMA: 128 features and this CTA's tokens of every stage
+            Ring<S::kStages> r;
+            bool ok = true;
+            Item it;
+            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
+                const int w0 = it.tw * S::kFeatures + (int)rank * 128, x0 = it.tx * S::kTokens + (int)rank * S::kXRows;
+                for (int b = it.first; b < it.last; ++b) {
+                    if (r.turn > 0 && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t base = stages + r.st * S::kStageBytes, bar = smem_u32(&sh.full[r.st]);
+                    mbar_arrive_expect_tx(&sh.full[r.st], S::kStageBytes);
+                    tma_load_2d(base, &p.w, b * 128, w0, bar);
+                    tma_load_2d(base + S::kWBytes, &p.x, b * 128, x0, bar);
+                    r.next();
+                }
+            }
+            // what is still under way into this CTA's shared memory arrives before the CTA may leave: the MMAs'
+            // signals (after which the copies have been read), or, where a wait gave up, the copies
+            const int used = r.turn > 0 ? S::kStages : r.st;
+            for (int i = 0; i < used; ++i) {
+                if (r.st == 0) {
+                    r.st = S::kStages;
+                    --r.turn;
+                }
+                --r.st;
+                mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.parity(), p.limit);
+            }
+        } else if (warp == 1 && rank == 0) {
+            // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one lane
+            // issues
+            const bool one = elect_one();
+            Ring<S::kStages> r;
+            int64_t runs = 0, groups = 0;
+            bool ok = true;
+            Item it;
+            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
+                uint32_t ew = 0;
+                for (int b = it.first; ok && b < it.last; ++runs) {
+                    const int buf = (int)(runs & 1);
+                    if (runs >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit);
+                    if (S::kShared && ok && runs >= 1)
+                        ok = mbar_wait_cycles_warp(smem_u32(&sh.edge[buf ^ 1]), (uint32_t)((runs - 1) >> 1) & 1u, p.limit);
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t d = tmem + buf * S::kSecond;
+                    const int end = it.last - b < p.run ? it.last : b + p.run;
+                    for (bool add = false; b < end; ++b, add = true) {
+                        const int eb = (int)(groups & 1);
+                        if (b == it.first || (b & 3) == 0) {
+                            if (!mbar_wait_cycles_warp(smem_u32(&sh.exp_full[eb]), (uint32_t)(groups >> 1) & 1u, p.limit)) {
+                                ok = false;
+                                break;
+                            }
+                            ew = tmem + S::kExps + eb * S::kExpCols;
+                        }
+                        if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.parity(), p.limit) ||
+                            (GROUP == 2 && !mbar_wait_cycles_warp(smem_u32(&sh.peer_full[r.st]), r.parity(), p.limit))) {
+                            ok = false;
+                            break;
+                        }
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint32_t base = stages + r.st * S::kStageBytes;
+                        const uint64_t dw = operand_desc(base), dx = operand_desc(base + S::kWBytes);
+                        const uint32_t idesc = p.idesc | exp_byte((uint32_t)b & 3u);
+                        const bool last = (b & 3) == 3 || b + 1 == it.last;  // of the four stages' exponents
+                        if (one) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 columns each
+                                mma<GROUP>(d, dw + 2 * k, dx + 2 * k, idesc, ew, ew + 4, add || k > 0);
+                            commit<GROUP>(smem_u32(&sh.empty[r.st]));
+                            if (last) commit<GROUP>(smem_u32(&sh.exp_empty[eb]));
+                        }
+                        __syncwarp();
+                        if (last) ++groups;
+                        r.next();
+                    }
+                    if (ok && one) commit<GROUP>(smem_u32(&sh.acc_full[buf]));
+                    __syncwarp();
+                }
+            }
+        } else if (GROUP == 2 && warp == 2 && rank == 1) {
+            // tells the leader that this CTA's operands have arrived
+            const uint32_t to = in_cta(smem_u32(&sh.peer_full[0]), 0);
+            Ring<S::kStages> r;
+            bool ok = true;
+            Item it;
+            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units)
+                for (int b = it.first; b < it.last; ++b) {
+                    if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.parity(), p.limit)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) arrive_cluster(to + r.st * 8);
+                    __syncwarp();
+                    r.next();
+                }
+        }
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // Epilogue: TMEM lane = feature, column = token; four warps take the lower half of the tokens, four the upper.
+        // Columns that the two accumulators share (the first one's last, the second one's first) are read before all
+        // others, kHeld of them, so that the other accumulator's MMAs can go on.
+        constexpr int kHalf = TN / 2, kHeld = S::kShared ? 32 : 0, kRest = kHalf - kHeld;
+        static_assert(S::kShared <= 32 && kRest % 16 == 0, "columns");
+        const int quarter = warp & 3;  // the TMEM lanes this warp may read
+        const bool upper = warp >= 8;
+        const int held0 = upper ? kRest : 0, rest0 = upper ? 0 : kHeld;
+        const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), 0), edge = in_cta(smem_u32(&sh.edge[0]), 0);
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (upper ? kHalf : 0);
+        const int row = (int)rank * 128 + quarter * 32 + lane;
+        int64_t runs = 0;
+        bool ok = true;
+        Item it;
+        for (int64_t i = unit; item_of(p.s, i, it); i += units) {
+            float acc[SUMS ? kHalf : 1];
+            if constexpr (SUMS) {
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
+            }
+            for (int b = it.first; b < it.last; b += p.run, ++runs) {
+                const int buf = (int)(runs & 1);
+                ok = ok && mbar_wait_cycles_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t cols = lanes + buf * S::kSecond;
+                float held[kHeld ? kHeld : 1];
+                if constexpr (kHeld != 0) {
+#pragma unroll
+                    for (int c = 0; c < kHeld; c += 16) {
+                        float v[16];
+                        tmem_load16(cols + held0 + c, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) held[c + j] = SUMS ? acc[SUMS ? c + j : 0] + v[j] : v[j];
+                    }
+                    if (upper == (buf == 0)) {
+                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(edge + buf * 8);
+                    }
+                }
+                const bool end = b + p.run >= it.last;
+                if constexpr (SUMS) {
+                    if (!end || b > it.first) {
+#pragma unroll
+                        for (int c = 0; c < kRest; c += 16) {
+                            float v[16];
+                            tmem_load16(cols + rest0 + c, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[kHeld + c + j] += v[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < kHeld; ++j) acc[j] = held[j];
+                    }
+                    if (end && b > it.first) {
+                        // The tile's sums go back to TMEM, and from there to memory 16 at a time, in a loop that stays
+                        // in the instruction cache.
+#pragma unroll
+                        for (int c = 0; c < kRest; c += 16) tmem_store16(cols + rest0 + c, acc + kHeld + c);
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    }
+                }
+                if (end) {
+                    const int x0 = upper ? kHalf : 0;
+                    const Out<T, S> out(p, it, x0, kHalf, row, ok);
+#pragma unroll
+                    for (int c = 0; c < kHeld; c += 16) {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = held[c + j];
+                        out.put16(v, held0 + c);
+                    }
+#pragma unroll 1
+                    for (int c = rest0; c < rest0 + kRest; c += 16) {
+                        float v[16];
+                        tmem_load16(cols + c, v);
+                        out.put16(v, c);
+                    }
+                }
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_cluster(acc_empty + buf * 8);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExp));
+        // Exponents: each warp its quarter of the lanes, all four the same words, fetched one group ahead.
+        constexpr int kX = S::kExpCols - 4;
+        const uint32_t to = in_cta(smem_u32(&sh.exp_full[0]), 0);
+        const uint32_t lanes = tmem + S::kExps + ((uint32_t)((warp & 3) * 32) << 16);
+        int64_t groups = 0;
+        bool ok = true;
+        Item it;
+        for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
+            const uint8_t *rows[4 + kX];
+#pragma unroll
+            for (int c = 0; c < 4 + kX; ++c) {
+                const Exps &e = c < 4 ? p.ew : p.ex;
+                const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + rank * 128 + c * 32 + lane
+                                          : (int64_t)it.tx * S::kTokens + (c - 4) * 32 + lane;
+                const bool in = row < e.rows && (c < 4 || (c - 4) * 32 < TN);
+                rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
+            }
+            for (int g = it.first >> 2; g <= (it.last - 1) >> 2; ++g, ++groups) {
+                uint32_t v[4 + kX];
+#pragma unroll
+                for (int c = 0; c < 4 + kX; ++c) v[c] = rows[c] ? __ldg(reinterpret_cast<const uint32_t *>(rows[c]) + g) : 0u;
+                const int eb = (int)(groups & 1);
+                if (groups >= 2 && !mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((uint32_t)(groups >> 1) + 1u) & 1u, p.limit)) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < 4 + kX; c += 4) tmem_store4(lanes + eb * S::kExpCols + c, v + c);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_cluster(to + eb * 8);
+            }
+        }
+        // the MMAs' last signals arrive before the CTA may leave
+        for (int64_t g = groups >= 2 ? groups - 2 : 0; ok && g < groups; ++g)
+            ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[g & 1]), (uint32_t)(g >> 1) & 1u, p.limit);
+    }
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if constexpr (GROUP == 2) cluster_sync();
+    if (warp == 1) {
+        if constexpr (GROUP == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
 }
 
-Operand operand_of(const void *p, int format, int tile, int64_t rows, int64_t cols)
+// The cut tiles' sums, range by range in order, to y.  A block takes 4 tokens of 256 features (8 of 128), a thread 4
+// adjacent features of one.
+template <typename T, class S>
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
-    const Fp8Layout l = fp8_layout(tile, rows, cols);
-    const uint8_t *b = static_cast<const uint8_t *>(p);
-    return Operand{b, b + l.exps_off, rows, l.code_pitch, l.exp_pitch, format, tile ? 7 : 0};
+    constexpr int kAcross = S::kFeatures / 4, kRows = 256 / kAcross;
+    cudaGridDependencySynchronize();  // launched to start as k_mm drains
+    const int c = (int)(blockIdx.x / (S::kTokens / kRows));
+    const int x = (int)(blockIdx.x % (S::kTokens / kRows)) * kRows + (int)threadIdx.x / kAcross, w = (int)(threadIdx.x % kAcross) * 4;
+    const int lo = p.s.from[c], hi = p.s.to[c];
+    if (lo == hi) return;  // one range has the whole tile, and has stored it
+    Item it;
+    tile_place(p.s, p.s.whole + c, it);
+    const int64_t feature = (int64_t)it.tw * S::kFeatures + w, token = (int64_t)it.tx * S::kTokens + x;
+    if (feature >= p.features || token >= p.tokens) return;
+    const int n = (int)min((int64_t)4, p.features - feature);
+    const float *s = p.parts + ((int64_t)(c + lo) * S::kTokens + x) * S::kFeatures + w;
+    float v[4] = {};
+#pragma unroll 4
+    for (int r = 0; r <= hi - lo; ++r) {
+        // columns of features that do not exist were not written
+        float a[4];
+        if (n == 4) {
+            *reinterpret_cast<float4 *>(a) = *reinterpret_cast<const float4 *>(s + (int64_t)r * S::kTokens * S::kFeatures);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] = j < n ? s[(int64_t)r * S::kTokens * S::kFeatures + j] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += a[j];
+    }
+    T *const y = static_cast<T *>(p.y) + token * p.sy + feature;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < n) {
+            if (p.bias) v[j] += p.bias[feature + j];
+            if constexpr (sizeof(T) == 4) {
+                if (p.accumulate) v[j] += y[j];
+            }
+            y[j] = rounded<T>(v[j]);
+        }
+}
+
+// Which shape: tiles of 256 x 256 by CTA pairs, or, for up to 128 tokens, 128 features by single CTAs.
+enum Kind { kPair256, kOne128, kOne64, kOne32 };
+Kind kind_of(int64_t tokens) { return tokens > 128 ? kPair256 : tokens > 64 ? kOne128 : tokens > 32 ? kOne64 : kOne32; }
+
+template <class S>
+Schedule schedule_of(int64_t m, int64_t n, int64_t k) { return schedule(S::kUnits, n, m, S::kFeatures, S::kTokens, k); }
+template <class S>
+size_t workspace_of(int64_t m, int64_t n, int64_t k)
+{
+    return (size_t)part_tiles(schedule_of<S>(m, n, k)) * S::kTokens * S::kFeatures * sizeof(float);
+}
+
+bool encode_rows(CUtensorMap *map, const void *p, int64_t rows, int64_t pitch, int box_rows)
+{
+    const EncodeFn encode = encode_fn();
+    const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, ones[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Exps exps_of(const void *p, int tile, int64_t rows, const Fp8Layout &l)
+{
+    return Exps{static_cast<const uint8_t *>(p) + l.exps_off, rows, l.exp_pitch, tile ? 7 : 0};
+}
+
+template <typename T, class S, bool SUMS>
+cudaError_t launch_kernels(const Params &p, cudaStream_t stream)
+{
+    auto kern = k_mm<T, S::kGroup, S::kTokens, SUMS>;
+    int per_sm = 0, sms = 0;
+    cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, S::kSmemBytes, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    static const int regs = num_regs(kern);
+    if (regs < kRegsLaunch) return cudaErrorInvalidKernelImage;  // setmaxnreg would wait
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(S::kGroup * p.s.units));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S::kGroup;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess || !part_tiles(p.s)) return e;
+    cfg.gridDim = dim3((unsigned)(p.s.cut * (S::kTokens / (1024 / S::kFeatures))));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, k_join<T, S>, p);
+}
+
+template <class S>
+cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
+{
+    Params p;
+    const Fp8Layout lx = fp8_layout(g.tile_a, g.m, g.k), lw = fp8_layout(g.tile_b, g.n, g.k);
+    p.s = schedule_of<S>(g.m, g.n, g.k);
+    p.ew = exps_of(g.b, g.tile_b, g.n, lw);
+    p.ex = exps_of(g.a, g.tile_a, g.m, lx);
+    p.idesc = instr_desc(g.format_b, g.format_a, S::kFeatures, S::kTokens);
+    p.tokens = g.m;
+    p.features = g.n;
+    p.bias = g.bias;
+    p.y = g.y;
+    p.sy = g.m > 1 ? g.y_stride : 0;
+    p.accumulate = g.accumulate;
+    p.parts = reinterpret_cast<float *>(g.ws);
+    // two seconds at 1.97 GHz, three at the power cap's 1.39 GHz; the longest wait, for a tile, is some microseconds a
+    // thousand columns
+    p.limit = 4000000000ll;
+    if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) || !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kXRows))
+        return cudaErrorInvalidValue;
+    if (g.dtype == GQ_FLOAT32) {
+        p.run = 8;
+        return launch_kernels<float, S, true>(p, stream);
+    }
+    const bool sums = p.s.blocks > 128;
+    p.run = sums ? 32 : 128;
+    if (g.dtype == GQ_BFLOAT16)
+        return sums ? launch_kernels<__nv_bfloat16, S, true>(p, stream) : launch_kernels<__nv_bfloat16, S, false>(p, stream);
+    return sums ? launch_kernels<__half, S, true>(p, stream) : launch_kernels<__half, S, false>(p, stream);
 }
 
 }  // namespace
 
-size_t fp8_matmul_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k)
+{
+    if (m == 0) return 0;
+    switch (kind_of(m)) {
+    case kPair256: return workspace_of<Shape<2, 256>>(m, n, k);
+    case kOne128: return workspace_of<Shape<1, 128>>(m, n, k);
+    case kOne64: return workspace_of<Shape<1, 64>>(m, n, k);
+    default: return workspace_of<Shape<1, 32>>(m, n, k);
+    }
+}
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs &g, cudaStream_t stream)
 {
-    Params p;
-    p.a = operand_of(g.a, g.format_a, g.tile_a, g.m, g.k);
-    p.b = operand_of(g.b, g.format_b, g.tile_b, g.n, g.k);
-    p.k = g.k;
-    p.sy = g.m > 1 ? g.y_stride : 0;
-    p.bias = g.bias;
-    p.y = g.y;
-    p.accumulate = g.accumulate;
-    p.dtype = g.dtype;
-    p.tiles_n = (g.n + 63) / 64;
-    k_simple<<<(unsigned)((g.m + 63) / 64 * p.tiles_n), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    switch (kind_of(g.m)) {
+    case kPair256: return launch_shape<Shape<2, 256>>(g, stream);
+    case kOne128: return launch_shape<Shape<1, 128>>(g, stream);
+    case kOne64: return launch_shape<Shape<1, 64>>(g, stream);
+    default: return launch_shape<Shape<1, 32>>(g, stream);
+    }
 }
 
 }  // namespace gq
