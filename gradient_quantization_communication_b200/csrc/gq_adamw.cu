@@ -1,7 +1,7 @@
 // gq_adamw.cu -- AdamW over many tensors in one launch, the gradients' global norm, and the moments' values.
 //
-// A block takes 4096 elements of one tensor, found in a table that the optimizer keeps on the device; a lane takes
-// 8 consecutive ones, a warp 256 at a time: two blocks of 128 where the moments are in 8 bits, so that a block's
+// A block takes 4096 elements of one tensor at a time, found in a table that the optimizer keeps on the device; a lane
+// takes 8 consecutive ones, a warp 256: two blocks of 128 where the moments are in 8 bits, so that a block's
 // largest value is found by shuffles within 16 lanes and every state is read and written once.
 // Every operation rounds on its own (the formula's order, IEEE division and square root).
 #include <type_traits>
@@ -15,23 +15,67 @@ namespace gq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHalf = kThreads / 32 * kChunk;  // elements that a block takes at once
+static_assert(2 * kHalf == kAdamChunk, "two halves a chunk");
 
 struct Params {
     AdamStep s;
-    const AdamTensor *tensors;
     const AdamChunk *table;
+    int64_t chunks;
     uint32_t rk0[10], rk1[10];  // Philox round keys
 };
 
-// Largest of 8 values' absolute bits over a block of 128 (NaN above infinity).
+// Two values at a time: each operation rounds its two results alone.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// The sums are taken one by one: packed sums of packed products come out fused, rounded once.
+__device__ __forceinline__ void sum2(Two a, Two b, float &x, float &y)
+{
+    float a0, a1, b0, b1;
+    apart(a, a0, a1);
+    apart(b, b0, b1);
+    x = __fadd_rn(a0, b0);
+    y = __fadd_rn(a1, b1);
+}
+
+// The update's square root and quotient: rounded to nearest, or, where the moments are in 8 bits and instructions bound
+// the kernel (206 us against 179, 64 tensors of 1e6, bf16 parameters and fp32 gradients), off by up to 2 units in the
+// last place each.  Only the parameter's own change, lr times something near 1, carries that error.
+template <bool FAST>
+__device__ __forceinline__ float root(float x)
+{
+    if constexpr (!FAST) return __fsqrt_rn(x);
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <bool FAST>
+__device__ __forceinline__ float quotient(float a, float b)
+{
+    if constexpr (!FAST) return __fdiv_rn(a, b);
+    else return __fdividef(a, b);  // b is below 2^126 unless it is infinite: a root of binary32 times at most 2^14
+}
+
+// Bits of the largest |x| of a block of 128, which 16 lanes hold (a NaN's above infinity's).
 __device__ __forceinline__ uint32_t block_max(const float (&x)[8])
 {
-    uint32_t b = 0;
+    const float a = fmax3_nan(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), b = fmax3_nan(fabsf(x[3]), fabsf(x[4]), fabsf(x[5]));
+    uint32_t m = __float_as_uint(fmax3_nan(fmax_nan(a, b), fabsf(x[6]), fabsf(x[7])));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) b = max(b, __float_as_uint(x[j]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(kFull, b, o));
-    return b;
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    return m;
 }
 
 // The second moment's format (include/gq.h): 5 exponent and 3 mantissa bits of binary32, counted from 31 below E.
@@ -39,196 +83,289 @@ __device__ __forceinline__ uint32_t square_exp(uint32_t bits)
 {
     return bits >= kInfBits ? 255u : min(max((bits + 0xfffffu) >> 23, 32u), 254u);
 }
-__device__ __forceinline__ uint32_t square_code(float v, uint32_t noise16, uint32_t E)
+// Codes of 8 values, whose random halves are those of w: binary32 bits with the fraction's 16 random bits added under
+// the code's last, cut off there and counted from E's lowest.
+__device__ __forceinline__ uint2 square_codes(const float (&v)[8], const uint32_t (&w)[4], uint32_t E)
 {
-    const uint32_t bits = __float_as_uint(v);
-    const int c = (int)((bits + (noise16 << 4)) >> 20) - (int)((E - 31u) << 3);
-    return E == 255u || bits == 0u ? 0u : (uint32_t)min(max(c, 1), 255);
-}
-__device__ __forceinline__ float square_value(uint32_t c, uint32_t E)
-{
-    const float v = __uint_as_float((c + ((E - 31u) << 3)) << 20);
-    return E == 255u ? __uint_as_float(0x7fffffffu) : c == 0u ? 0.0f : v;
-}
-
-__device__ __forceinline__ uint2 load8(const uint8_t *p) { return *reinterpret_cast<const uint2 *>(p); }
-__device__ __forceinline__ uint32_t byte_of(uint2 q, int j) { return ((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 0xffu; }
-
-// One warp's 256 elements from `base` of a chunk of n elements that starts at element `first` of its tensor.
-template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
-__device__ __forceinline__ void update(const Params &p, const AdamTensor &t, const gq_adamw_scalars_t &now, float scale,
-                                       int64_t first, int n, int base, int lane)
-{
-    using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
-    S *const param = MASTER ? reinterpret_cast<S *>(t.master) + first : static_cast<S *>(t.param) + first;
-    const G *const grad = static_cast<const G *>(t.grad) + first;
-    // Unaligned loads take whole 16-byte pieces, with bytes that other warps may be writing: those are dropped.
-    Raw<S, AL> rp;
-    Raw<G, AL> rg;
-    float m[8], v[8];
-    chunk_load<S, AL, false, false>(rp, param, base, lane, n);
-    chunk_load<G, AL, false>(rg, grad, base, lane, n);
-    const int64_t at = first + base + lane * 8;  // of the tensor
-    uint8_t *const m8 = static_cast<uint8_t *>(t.m), *const v8 = static_cast<uint8_t *>(t.v);
-    const size_t exps = adam_exps_off(t.n);
-    const bool in = base + lane * 8 < n;
-    if constexpr (EIGHT) {
-        uint2 qm = make_uint2(0u, 0u), qv = qm;
-        uint32_t em = 0, ev = 32;
-        if (in) {
-            qm = load8(m8 + at);
-            qv = load8(v8 + at);
-            em = m8[exps + (at >> 7)];
-            ev = v8[exps + (at >> 7)];
-        }
-        fp8_decode8<GQ_FP8_E4M3>(qm, fp8_scale(em), m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = square_value(byte_of(qv, j), ev);
-    } else {
-        Raw<float, AL> r;
-        chunk_load<float, AL, false, false>(r, static_cast<float *>(t.m) + first, base, lane, n);
-        to_floats(in_place<float, AL>(r, static_cast<float *>(t.m) + first), m);
-        chunk_load<float, AL, false, false>(r, static_cast<float *>(t.v) + first, base, lane, n);
-        to_floats(in_place<float, AL>(r, static_cast<float *>(t.v) + first), v);
-    }
-    float x[8], g[8];
-    to_floats(in_place<S, AL>(rp, param), x);
-    to_floats(in_place<G, AL>(rg, grad), g);
-    const float lr = __fmul_rn(now.lr, t.lr_scale);
-    const float keep = __fsub_rn(1.0f, __fmul_rn(lr, t.decay)), size = __fmul_rn(lr, now.inv1);
+    const int base = (int)((E - 31u) << 3);
+    int q[8], least = 1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float gj = __fmul_rn(g[j], scale);
-        m[j] = __fadd_rn(__fmul_rn(m[j], p.s.beta1), __fmul_rn(gj, p.s.rest1));
-        v[j] = __fadd_rn(__fmul_rn(v[j], p.s.beta2), __fmul_rn(__fmul_rn(gj, gj), p.s.rest2));
-        const float below = __fadd_rn(__fmul_rn(__fsqrt_rn(v[j]), now.inv2), p.s.eps);
-        x[j] = __fsub_rn(__fmul_rn(x[j], keep), __fmul_rn(size, __fdiv_rn(m[j], below)));
+        const uint32_t noise = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+        q[j] = (int)((noise * 16u + __float_as_uint(v[j])) >> 20) - base;
+        least = min(least, q[j]);
+    }
+    if (least < 1 || E >= 254u) {  // values 2^31 below the largest, or 0; beyond binary32's largest powers of two; not finite
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = E == 255u || v[j] == 0.0f ? 0 : min(max(q[j], 1), 255);
+    }
+    return make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+}
+__device__ __forceinline__ bool zero_byte(uint32_t w) { return ((w - 0x01010101u) & ~w & 0x80808080u) != 0u; }
+__device__ __forceinline__ void square_values(uint2 q, uint32_t E, float (&v)[8])
+{
+    const uint32_t base = (E - 31u) << 23;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = __uint_as_float(__byte_perm(j < 4 ? q.x : q.y, 0u, 0x4440u | (uint32_t)(j & 3)) * (1u << 20) + base);
+    if (zero_byte(q.x) || zero_byte(q.y) || E == 255u) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t c = __byte_perm(j < 4 ? q.x : q.y, 0u, 0x4440u | (uint32_t)(j & 3));
+            v[j] = E == 255u ? __uint_as_float(0x7fffffffu) : c ? v[j] : 0.0f;
+        }
+    }
+}
+
+// What a lane has loaded of its 8 elements.
+template <typename S, typename G, bool EIGHT, bool AL>
+struct Loaded {
+    Raw<S, AL> x;  // the parameters, or their master copies
+    Raw<G, AL> g;
+    Raw<float, AL> m[EIGHT ? 1 : 2];  // and v
+};
+template <typename S, typename G, bool AL>
+struct Loaded<S, G, true, AL> {
+    Raw<S, AL> x;
+    Raw<G, AL> g;
+    uint2 m, v;
+    uint32_t em, ev;
+};
+
+template <typename S, bool MASTER>
+__device__ __forceinline__ S *updated(const AdamChunk &c)
+{
+    if constexpr (MASTER) return c.master;
+    else return static_cast<S *>(c.param);
+}
+
+// Unaligned loads take whole 16-byte pieces, with bytes that other warps may be writing: those are dropped.
+// FULL: all of the warp's elements exist (aligned tensors).
+template <typename S, typename G, bool MASTER, bool EIGHT, bool AL, bool FULL>
+__device__ __forceinline__ void load(Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base, int lane)
+{
+    const int n = c.n;
+    chunk_load<S, AL, FULL, false>(l.x, updated<S, MASTER>(c), base, lane, n);
+    chunk_load<G, AL, FULL>(l.g, static_cast<const G *>(c.grad), base, lane, n);
+    if constexpr (EIGHT) {
+        const int at = base + lane * 8;
+        if (!FULL) {
+            l.m = l.v = make_uint2(0u, 0u);
+            l.em = 0;
+            l.ev = 32;
+        }
+        if (FULL || at < n) {
+            l.m = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(c.m) + at);
+            l.v = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(c.v) + at);
+            l.em = c.em[at >> 7];
+            l.ev = c.ev[at >> 7];
+        }
+    } else {
+        chunk_load<float, AL, FULL, false>(l.m[0], static_cast<const float *>(c.m), base, lane, n);
+        chunk_load<float, AL, FULL, false>(l.m[1], static_cast<const float *>(c.v), base, lane, n);
+    }
+}
+
+// One warp's 256 elements from `base` of a chunk.
+template <typename P, typename S, typename G, bool MASTER, bool EIGHT, bool AL, bool FULL>
+__device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c,
+                                       const gq_adamw_scalars_t &now, float scale, int base, int lane)
+{
+    const int n = c.n, at = base + lane * 8;
+    S *const param = updated<S, MASTER>(c);
+    float x[8], g[8], m[8], v[8], beta1 = p.s.beta1;
+    to_floats(in_place<S, AL>(l.x, param), x);
+    to_floats(in_place<G, AL>(l.g, static_cast<const G *>(c.grad)), g);
+    if constexpr (EIGHT) {
+        // the scale joins beta1 below: a power of two, so their product is exact
+        fp8_decode8<GQ_FP8_E4M3>(l.m, 1.0f, m);
+        beta1 = __fmul_rn(fp8_scale(l.em), beta1);
+        square_values(l.v, l.ev, v);
+    } else {
+        to_floats(in_place<float, AL>(l.m[0], static_cast<const float *>(c.m)), m);
+        to_floats(in_place<float, AL>(l.m[1], static_cast<const float *>(c.v)), v);
+    }
+    const float lr = __fmul_rn(now.lr, c.lr_scale);
+    const float keep = __fsub_rn(1.0f, __fmul_rn(lr, c.decay)), size = __fmul_rn(lr, now.inv1);
+    const Two scale2 = two(scale, scale), beta1s = two(beta1, beta1), rest1s = two(p.s.rest1, p.s.rest1),
+              beta2s = two(p.s.beta2, p.s.beta2), rest2s = two(p.s.rest2, p.s.rest2), inv2s = two(now.inv2, now.inv2),
+              epss = two(p.s.eps, p.s.eps), keeps = two(keep, keep), sizes = two(-size, -size);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const Two gj = mul2(two(g[j], g[j + 1]), scale2);
+        sum2(mul2(two(m[j], m[j + 1]), beta1s), mul2(gj, rest1s), m[j], m[j + 1]);
+        sum2(mul2(two(v[j], v[j + 1]), beta2s), mul2(mul2(gj, gj), rest2s), v[j], v[j + 1]);
+        float a, b;
+        sum2(mul2(two(root<EIGHT>(v[j]), root<EIGHT>(v[j + 1])), inv2s), epss, a, b);
+        const Two u = two(quotient<EIGHT>(m[j], a), quotient<EIGHT>(m[j + 1], b));
+        sum2(mul2(two(x[j], x[j + 1]), keeps), mul2(sizes, u), x[j], x[j + 1]);
     }
     Words<S> ws;
     from_floats(ws, x);
-    chunk_store<S, AL>(ws, param, base, lane, n);
+    chunk_store<S, AL, FULL>(ws, param, base, lane, n);
     if constexpr (MASTER) {
-        P *const out = static_cast<P *>(t.param) + first;
         Words<P> wp;
         from_floats(wp, x);
-        chunk_store<P, AL>(wp, out, base, lane, n);
+        chunk_store<P, AL, FULL>(wp, static_cast<P *>(c.param), base, lane, n);
     }
     if constexpr (EIGHT) {
         // elements past the tensor's last are zeros
-        if (base + lane * 8 + 8 > n) {
+        if (!FULL && at + 8 > n) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (base + lane * 8 + j >= n) m[j] = v[j] = 0.0f;
+                if (at + j >= n) m[j] = v[j] = 0.0f;
         }
         const uint32_t em = fp8_exp<GQ_FP8_E4M3>(block_max(m)), ev = square_exp(block_max(v));
         const float inv = fp8_inverse(em);
         const uint2 qm = make_uint2(fp8_codes4<GQ_FP8_E4M3>(m[0], m[1], m[2], m[3], inv, em),
                                     fp8_codes4<GQ_FP8_E4M3>(m[4], m[5], m[6], m[7], inv, em));
         // Philox's counter (element / 8, step, tensor + 2^31)
-        const uint64_t group = (uint64_t)at >> 3;
+        const uint64_t group = (uint64_t)(c.group + (at >> 3));
         const uint32_t c0 = (uint32_t)group, c2 = now.step;
         const unsigned long long p0 = (unsigned long long)0xD2511F53u * c0, p1 = (unsigned long long)0xCD9E8D57u * c2;
         const uint4 d = philox_rounds_2_to_10((uint32_t)(p1 >> 32) ^ (uint32_t)(group >> 32) ^ p.rk0[0], (uint32_t)p1,
-                                              (uint32_t)(p0 >> 32) ^ (t.number | 0x80000000u) ^ p.rk1[0], (uint32_t)p0,
+                                              (uint32_t)(p0 >> 32) ^ (c.number | 0x80000000u) ^ p.rk1[0], (uint32_t)p0,
                                               p.rk0 + 1, p.rk1 + 1);
         const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-        uint32_t q[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = square_code(v[j], (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu, ev);
-        const uint2 qv = make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+        const uint2 qv = square_codes(v, w, ev);
         // whole blocks are written, the last one's codes past the tensor as 0
-        if (first + base + (lane & 16) * 8 < t.n) {
-            *reinterpret_cast<uint2 *>(m8 + at) = qm;
-            *reinterpret_cast<uint2 *>(v8 + at) = qv;
+        if (FULL || base + (lane & 16) * 8 < n) {
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(c.m) + at) = qm;
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(c.v) + at) = qv;
             if ((lane & 15) == 0) {
-                m8[exps + (at >> 7)] = (uint8_t)em;
-                v8[exps + (at >> 7)] = (uint8_t)ev;
+                c.em[at >> 7] = (uint8_t)em;
+                c.ev[at >> 7] = (uint8_t)ev;
             }
         }
     } else {
         Words<float> w;
         from_floats(w, m);
-        chunk_store<float, AL>(w, static_cast<float *>(t.m) + first, base, lane, n);
+        chunk_store<float, AL, FULL>(w, static_cast<float *>(c.m), base, lane, n);
         from_floats(w, v);
-        chunk_store<float, AL>(w, static_cast<float *>(t.v) + first, base, lane, n);
+        chunk_store<float, AL, FULL>(w, static_cast<float *>(c.v), base, lane, n);
     }
 }
 
-template <typename P, typename G, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Params p)
+// Blocks walk the table in strides of the grid.  Entries are fetched two chunks ahead, and with moments in 8 bits the
+// elements 256 x 8 ahead: the way from an entry to its elements and back, which a block would wait for twice a chunk,
+// is otherwise most of its time (374 us without either, 206 with, 64 tensors of 1e6, bf16 parameters).
+// Blocks an SM: three, but two where 8-bit moments leave room for a float32 parameter's and gradient's elements on the
+// way only so (195 us against 211; with a bf16 parameter 178 against 157).
+constexpr int blocks_of(bool eight, int updated, int grad) { return eight && updated + grad == 8 ? 2 : 3; }
+
+template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
+__global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof(P), sizeof(G))) k_adamw(const __grid_constant__ Params p)
 {
-    const AdamChunk c = p.table[blockIdx.x];
+    using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
+    constexpr int kWords = sizeof(AdamChunk) / 16;
+    __shared__ AdamChunk entry[3];
     const float scale = p.s.scale ? *p.s.scale : 1.0f;
     if (scale != scale) return;
     gq_adamw_scalars_t now = p.s.now;
     if (p.s.scalars) now = *p.s.scalars;
-    const AdamTensor t = p.tensors[c.tensor];
-    const int64_t first = (int64_t)c.part * kAdamChunk;
-    const int n = (int)min((int64_t)kAdamChunk, t.n - first), lane = threadIdx.x & 31;
-    for (int base = (int)(threadIdx.x >> 5) * kChunk; base < n; base += kThreads / 32 * kChunk) {
-        if (t.aligned) update<P, G, MASTER, EIGHT, true>(p, t, now, scale, first, n, base, lane);
-        else update<P, G, MASTER, EIGHT, false>(p, t, now, scale, first, n, base, lane);
+    const int lane = threadIdx.x & 31, first = (int)(threadIdx.x >> 5) * kChunk, tid = threadIdx.x;
+    const int64_t step = gridDim.x;
+    int64_t i = blockIdx.x;
+    auto fetch = [&](int64_t at) { return __ldg(reinterpret_cast<const uint4 *>(p.table + at) + tid); };
+    if (tid < kWords) {
+        reinterpret_cast<uint4 *>(&entry[0])[tid] = fetch(i);
+        if (i + step < p.chunks) reinterpret_cast<uint4 *>(&entry[1])[tid] = fetch(i + step);
+    }
+    __syncthreads();
+    Loaded<S, G, EIGHT, AL> a;
+    auto fetch_elements = [&](Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
+        if (AL && base + kChunk <= c.n) load<S, G, MASTER, EIGHT, AL, AL>(l, c, base, lane);
+        else if (base < c.n) load<S, G, MASTER, EIGHT, AL, false>(l, c, base, lane);
+    };
+    auto work = [&](const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
+        if (AL && base + kChunk <= c.n) update<P, S, G, MASTER, EIGHT, AL, AL>(p, l, c, now, scale, base, lane);
+        else if (base < c.n) update<P, S, G, MASTER, EIGHT, AL, false>(p, l, c, now, scale, base, lane);
+    };
+    if (EIGHT) fetch_elements(a, entry[0], first);
+    for (int k = 0; i < p.chunks; i += step) {
+        const int next = k == 2 ? 0 : k + 1, after = next == 2 ? 0 : next + 1;
+        const AdamChunk &c = entry[k];
+        uint4 ahead;
+        const bool more = i + 2 * step < p.chunks && tid < kWords;
+        if (more) ahead = fetch(i + 2 * step);
+        if constexpr (EIGHT) {
+            Loaded<S, G, EIGHT, AL> b;
+            fetch_elements(b, c, first + kHalf);
+            work(a, c, first);
+            if (i + step < p.chunks) fetch_elements(a, entry[next], first);
+            work(b, c, first + kHalf);
+        } else {
+#pragma unroll 1
+            for (int base = first; base < c.n; base += kHalf) {
+                fetch_elements(a, c, base);
+                work(a, c, base);
+            }
+        }
+        if (more) reinterpret_cast<uint4 *>(&entry[after])[tid] = ahead;
+        __syncthreads();
+        k = next;
     }
 }
 
 // ---------------------------------------------------------------------------------------------
 // The moments' values.
 // ---------------------------------------------------------------------------------------------
-template <typename T, bool AL>
-__device__ __forceinline__ void put_values(float (&x)[8], void *out, int64_t at, int n, int base, int lane)
+// What a lane has loaded of its 8 elements of a moment.  Those in 32 bits may start elsewhere than the output.
+template <bool EIGHT>
+struct Moment {
+    Raw<float, false> r;
+};
+template <>
+struct Moment<true> {
+    uint2 q;
+    uint32_t E;
+};
+template <bool EIGHT>
+__device__ __forceinline__ void load(Moment<EIGHT> &l, const void *x, const uint8_t *exps, int n, int base, int lane)
 {
+    if constexpr (EIGHT) {
+        const int at = base + lane * 8;
+        l.q = make_uint2(0u, 0u);
+        l.E = 32;
+        if (at < n) {
+            l.q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + at));
+            l.E = __ldg(exps + (at >> 7));
+        }
+    } else {
+        chunk_load<float, false>(l.r, static_cast<const float *>(x), base, lane, n);
+    }
+}
+template <typename T, bool EIGHT, bool AL>
+__device__ __forceinline__ void put(const Moment<EIGHT> &l, const AdamChunk &c, bool second, int base, int lane, void *m, void *v)
+{
+    void *const out = second ? v : m;
+    if (!out) return;
+    float x[8];
+    if constexpr (!EIGHT) to_floats(in_place<float, false>(l.r, static_cast<const float *>(second ? c.v : c.m)), x);
+    else if (second) square_values(l.q, l.E, x);
+    else fp8_decode8<GQ_FP8_E4M3>(l.q, fp8_scale(l.E), x);
     saturate<T>(x);
     Words<T> w;
     from_floats(w, x);
-    chunk_store<T, AL>(w, static_cast<T *>(out) + at, base, lane, n);
+    chunk_store<T, AL>(w, static_cast<T *>(out) + c.start, base, lane, c.n);
 }
 
-template <typename T, bool EIGHT, bool AL>
-__device__ __forceinline__ void moments(const AdamTensor &t, int64_t first, int n, int base, int lane, void *m, void *v)
-{
-    const int64_t at = first + base + lane * 8, to = t.start + first;
-    const bool in = base + lane * 8 < n;
-    float x[8];
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        void *const out = which ? v : m;
-        if (!out) continue;
-        if constexpr (EIGHT) {
-            const uint8_t *const src = static_cast<const uint8_t *>(which ? t.v : t.m);
-            uint2 q = make_uint2(0u, 0u);
-            uint32_t E = 32;
-            if (in) {
-                q = __ldg(reinterpret_cast<const uint2 *>(src + at));
-                E = __ldg(src + adam_exps_off(t.n) + (at >> 7));
-            }
-            if (which == 0) {
-                fp8_decode8<GQ_FP8_E4M3>(q, fp8_scale(E), x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = square_value(byte_of(q, j), E);
-            }
-        } else {
-            // the tensor's slices may start elsewhere than the output's
-            const float *const src = static_cast<const float *>(which ? t.v : t.m) + first;
-            Raw<float, false> r;
-            chunk_load<float, false>(r, src, base, lane, n);
-            to_floats(in_place<float, false>(r, src), x);
-        }
-        put_values<T, AL>(x, out, to, n, base, lane);
-    }
-}
-
+// Registers for as many warps as an SM holds: at 47 instead of 32 the 8-bit form takes 95 us instead of 75 (64 x 1e6).
 template <typename T, bool EIGHT>
-__global__ void __launch_bounds__(kThreads) k_moments(const __grid_constant__ Params p, void *m, void *v)
+__global__ void __launch_bounds__(kThreads, EIGHT ? 8 : 6) k_moments(const __grid_constant__ Params p, void *m, void *v)
 {
     const AdamChunk c = p.table[blockIdx.x];
-    const AdamTensor t = p.tensors[c.tensor];
-    const int64_t first = (int64_t)c.part * kAdamChunk;
-    const int n = (int)min((int64_t)kAdamChunk, t.n - first), lane = threadIdx.x & 31;
-    const bool al = t.start % (16 / (int)sizeof(T)) == 0;
-    for (int base = (int)(threadIdx.x >> 5) * kChunk; base < n; base += kThreads / 32 * kChunk) {
-        if (al) moments<T, EIGHT, true>(t, first, n, base, lane, m, v);
-        else moments<T, EIGHT, false>(t, first, n, base, lane, m, v);
+    const int lane = threadIdx.x & 31;
+    const bool al = c.start % (16 / (int)sizeof(T)) == 0;
+    for (int base = (int)(threadIdx.x >> 5) * kChunk; base < c.n; base += kHalf) {
+        Moment<EIGHT> l[2];
+        if (m) load<EIGHT>(l[0], c.m, c.em, c.n, base, lane);
+        if (v) load<EIGHT>(l[1], c.v, c.ev, c.n, base, lane);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (al) put<T, EIGHT, true>(l[w], c, w == 1, base, lane, m, v);
+            else put<T, EIGHT, false>(l[w], c, w == 1, base, lane, m, v);
+        }
     }
 }
 
@@ -250,33 +387,38 @@ __device__ __forceinline__ double block_sum(double s, double *shared)
 }
 
 template <typename G, bool AL>
-__device__ __forceinline__ double squares(const G *grad, int n, int base, int lane)
+__device__ __forceinline__ double squares(const G *grad, int n, int first, int lane)
 {
-    Raw<G, AL> r;
-    chunk_load<G, AL>(r, grad, base, lane, n);
-    float g[8];
-    to_floats(in_place<G, AL>(r, grad), g);
-    double s = 0.0;
+    Raw<G, AL> r[2];
+    chunk_load<G, AL>(r[0], grad, first, lane, n);
+    chunk_load<G, AL>(r[1], grad, first + kHalf, lane, n);
+    double s[2] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = __fma_rn((double)g[j], (double)g[j], s);
-    return s;
+    for (int h = 0; h < 2; ++h) {
+        float g[8];
+        to_floats(in_place<G, AL>(r[h], grad), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[h] = __fma_rn((double)g[j], (double)g[j], s[h]);
+    }
+    return s[0] + s[1];
 }
 
 template <typename G>
-__global__ void __launch_bounds__(kThreads) k_norm(const AdamTensor *tensors, const AdamChunk *table, int64_t chunks, double *parts)
+__global__ void __launch_bounds__(kThreads) k_norm(const AdamChunk *table, int64_t aligned, int64_t chunks, double *parts)
 {
     __shared__ double shared[kThreads / 32];
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, first = (int)(threadIdx.x >> 5) * kChunk;
     double s = 0.0;
+    const void *grad = table[blockIdx.x].grad;
+    int n = table[blockIdx.x].n;
     for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-        const AdamChunk c = table[i];
-        const AdamTensor &t = tensors[c.tensor];
-        const int64_t first = (int64_t)c.part * kAdamChunk;
-        const G *const grad = static_cast<const G *>(t.grad) + first;
-        const int n = (int)min((int64_t)kAdamChunk, t.n - first);
-        const bool al = t.aligned != 0;
-        for (int base = (int)(threadIdx.x >> 5) * kChunk; base < n; base += kThreads / 32 * kChunk)
-            s += al ? squares<G, true>(grad, n, base, lane) : squares<G, false>(grad, n, base, lane);
+        const G *const g = static_cast<const G *>(grad);
+        const int count = n;
+        if (i + gridDim.x < chunks) {  // the next entry is on its way meanwhile
+            grad = table[i + gridDim.x].grad;
+            n = table[i + gridDim.x].n;
+        }
+        s += i < aligned ? squares<G, true>(g, count, first, lane) : squares<G, false>(g, count, first, lane);
     }
     s = block_sum(s, shared);
     if (threadIdx.x == 0) parts[blockIdx.x] = s;
@@ -295,12 +437,31 @@ __global__ void __launch_bounds__(kThreads) k_norm_join(const double *parts, int
     }
 }
 
+template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
+cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
+{
+    if (chunks == 0) return cudaSuccess;
+    auto kern = k_adamw<P, G, MASTER, EIGHT, AL>;
+    int per_sm = 0, sms = 0;
+    const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    p.table += first;
+    p.chunks = chunks;
+    // 32 bits: a block a chunk, replaced by the next as it ends (268 us against 286 for a grid that stays, 64 x 1e6)
+    const int64_t most = EIGHT ? (int64_t)per_sm * sms : chunks;
+    kern<<<(unsigned)(chunks < most ? chunks : most), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+template <typename P, typename G, bool MASTER, bool EIGHT>
+cudaError_t launch_parts(const AdamArgs &a, const Params &p, cudaStream_t s)
+{
+    const cudaError_t e = launch_part<P, G, MASTER, EIGHT, true>(p, 0, a.aligned, s);
+    return e != cudaSuccess ? e : launch_part<P, G, MASTER, EIGHT, false>(p, a.aligned, a.chunks - a.aligned, s);
+}
 template <typename P, typename G, bool MASTER>
 cudaError_t launch_state(const AdamArgs &a, const Params &p, cudaStream_t s)
 {
-    if (a.state_bits == 8) k_adamw<P, G, MASTER, true><<<(unsigned)a.chunks, kThreads, 0, s>>>(p);
-    else k_adamw<P, G, MASTER, false><<<(unsigned)a.chunks, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return a.state_bits == 8 ? launch_parts<P, G, MASTER, true>(a, p, s) : launch_parts<P, G, MASTER, false>(a, p, s);
 }
 template <typename P, typename G>
 cudaError_t launch_master(const AdamArgs &a, const Params &p, cudaStream_t s)
@@ -328,8 +489,8 @@ cudaError_t launch_moments(const AdamArgs &a, const Params &p, void *m, void *v,
 Params params_of(const AdamArgs &a)
 {
     Params p = {};
-    p.tensors = a.tensors;
     p.table = a.table;
+    p.chunks = a.chunks;
     for (int i = 0; i < 10; ++i) {
         p.rk0[i] = (uint32_t)a.seed + (uint32_t)i * 0x9E3779B9u;
         p.rk1[i] = (uint32_t)(a.seed >> 32) + (uint32_t)i * 0xBB67AE85u;
@@ -360,9 +521,9 @@ cudaError_t launch_adamw_norm(const AdamArgs &a, double max_norm, double *parts,
 {
     const unsigned grid = (unsigned)(a.chunks < kNormParts ? a.chunks : kNormParts);
     if (grid) {
-        if (a.grad_dtype == GQ_FLOAT32) k_norm<float><<<grid, kThreads, 0, s>>>(a.tensors, a.table, a.chunks, parts);
-        else if (a.grad_dtype == GQ_BFLOAT16) k_norm<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a.tensors, a.table, a.chunks, parts);
-        else k_norm<__half><<<grid, kThreads, 0, s>>>(a.tensors, a.table, a.chunks, parts);
+        if (a.grad_dtype == GQ_FLOAT32) k_norm<float><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
+        else if (a.grad_dtype == GQ_BFLOAT16) k_norm<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
+        else k_norm<__half><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
     }
     k_norm_join<<<1, kThreads, 0, s>>>(parts, (int)grid, max_norm, out);
     return cudaGetLastError();

@@ -15,29 +15,26 @@ constexpr int kAdamChunk = 4096;  // elements of a tensor that one block updates
 __host__ __device__ inline size_t adam_exps_off(int64_t n) { return (size_t)((n + 127) / 128 * 128); }
 inline size_t adam_bytes(int64_t n) { return adam_exps_off(n) + (size_t)(((n + 127) / 128 + 15) / 16 * 16); }
 
-// A tensor as the kernels read it.
-struct AdamTensor {
+// A piece of a tensor, up to kAdamChunk elements, as the kernels read it: where each of its arrays starts.
+struct alignas(16) AdamChunk {
     void *param;
     const void *grad;
     float *master;
-    void *m, *v;
-    int64_t n;
-    int64_t start;      // elements of the tensors before it
+    void *m, *v;          // float32 values, or codes
+    uint8_t *em, *ev;     // the codes' exponents
+    int64_t group;        // of 8 elements of its tensor, its first one
+    int64_t start;        // elements of the pieces before it, in the order of the list
+    int32_t n;
+    uint32_t number;      // its tensor's, in the caller's list
     float decay, lr_scale;
-    uint32_t number;    // in the caller's list
-    int32_t aligned;    // all of it starts on 16 bytes
 };
-// What block i works on: elements kAdamChunk * part and up of a tensor.
-struct AdamChunk {
-    uint32_t tensor, part;
-};
+static_assert(sizeof(AdamChunk) % 16 == 0, "read by 16 bytes");
 
 struct AdamArgs {
     int param_dtype, grad_dtype, state_bits;
     bool master;
-    int64_t chunks;
-    const AdamTensor *tensors;  // device
-    const AdamChunk *table;     // device
+    int64_t aligned, chunks;  // pieces whose arrays all start on 16 bytes come first
+    const AdamChunk *table;   // device
     uint64_t seed;
 };
 
@@ -51,7 +48,7 @@ cudaError_t launch_adamw(const AdamArgs &a, const AdamStep &s, cudaStream_t stre
 cudaError_t launch_adamw_moments(const AdamArgs &a, int dtype, void *m, void *v, cudaStream_t stream);
 
 // Partial sums that the norm writes (binary64).
-constexpr int kNormParts = 148 * 4;
+constexpr int kNormParts = 148 * 8;
 cudaError_t launch_adamw_norm(const AdamArgs &a, double max_norm, double *parts, float *out, cudaStream_t stream);
 
 }  // namespace gq

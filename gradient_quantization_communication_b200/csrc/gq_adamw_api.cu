@@ -19,7 +19,7 @@ struct Span {
 struct gq_adamw {
     gq::AdamArgs a;
     std::vector<gq::Span> spans;  // the tensors' memory, by address
-    void *memory;   // device: the tensors, the table of chunks, the norm's partial sums
+    void *memory;   // device: the table of chunks, the norm's partial sums
     double *parts;
     int64_t total;  // elements
     int device;
@@ -104,53 +104,61 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
     std::vector<Span> spans;
     const gq_status_t st = check_tensors(c, list, count, spans);
     if (st != GQ_OK) return st;
-    std::vector<AdamTensor> tensors;
     std::vector<AdamChunk> table;
-    int64_t total = 0, chunks = 0;
+    int64_t total = 0, chunks = 0, aligned_chunks = 0;
     for (int i = 0; i < count; ++i) chunks += (list[i].n + kAdamChunk - 1) / kAdamChunk;
     if (chunks > (int64_t(1) << 31) - 1) return GQ_ERR_UNSUPPORTED;
     table.reserve((size_t)chunks);
     bool master = false;
-    for (int i = 0; i < count; ++i) {
-        const gq_adamw_tensor_t &x = list[i];
-        if (x.n == 0) continue;
-        AdamTensor t = {};
-        t.param = x.param;
-        t.grad = x.grad;
-        t.master = x.master;
-        t.m = x.m;
-        t.v = x.v;
-        t.n = x.n;
-        t.start = total;
-        t.decay = x.weight_decay;
-        t.lr_scale = x.lr_scale;
-        t.number = (uint32_t)i;
-        t.aligned = aligned(x.param, 16) && aligned(x.grad, 16) && aligned(x.master, 16) && aligned(x.m, 16) && aligned(x.v, 16);
-        master = master || x.master;
-        for (int64_t k = 0; k * kAdamChunk < x.n; ++k) table.push_back(AdamChunk{(uint32_t)tensors.size(), (uint32_t)k});
-        tensors.push_back(t);
-        total += x.n;
+    const int64_t ps = elem_size(c.param_dtype), gs = elem_size(c.grad_dtype), ss = c.state_bits == 8 ? 1 : 4;
+    for (int pass = 0; pass < 2; ++pass) {  // tensors that start on 16 bytes, then the others
+        total = 0;
+        for (int i = 0; i < count; ++i) {
+            const gq_adamw_tensor_t &x = list[i];
+            const bool al = aligned(x.param, 16) && aligned(x.grad, 16) && aligned(x.master, 16) && aligned(x.m, 16) && aligned(x.v, 16);
+            for (int64_t at = 0; at < x.n && al == (pass == 0); at += kAdamChunk) {
+                auto plus = [at](void *p, int64_t size) { return static_cast<void *>(static_cast<uint8_t *>(p) + at * size); };
+                uint8_t *const m = static_cast<uint8_t *>(x.m), *const v = static_cast<uint8_t *>(x.v);
+                AdamChunk t = {};
+                t.param = plus(x.param, ps);
+                t.grad = plus(const_cast<void *>(x.grad), gs);
+                t.master = x.master ? x.master + at : nullptr;
+                t.m = plus(x.m, ss);
+                t.v = plus(x.v, ss);
+                if (ss == 1) {
+                    t.em = m + adam_exps_off(x.n) + at / 128;
+                    t.ev = v + adam_exps_off(x.n) + at / 128;
+                }
+                t.group = at / 8;
+                t.start = total + at;
+                t.n = (int32_t)(x.n - at < kAdamChunk ? x.n - at : kAdamChunk);
+                t.number = (uint32_t)i;
+                t.decay = x.weight_decay;
+                t.lr_scale = x.lr_scale;
+                master = master || x.master;
+                table.push_back(t);
+            }
+            total += x.n;
+        }
+        if (pass == 0) aligned_chunks = (int64_t)table.size();
     }
     gq_adamw *o = new gq_adamw;
     o->spans.swap(spans);
     o->total = total;
     o->memory = nullptr;
-    const size_t tb = (tensors.size() * sizeof(AdamTensor) + 15) / 16 * 16, cb = (table.size() * sizeof(AdamChunk) + 15) / 16 * 16;
-    if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, tb + cb + kNormParts * sizeof(double)) != cudaSuccess) {
+    const size_t bytes = table.size() * sizeof(AdamChunk);
+    if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, bytes + kNormParts * sizeof(double)) != cudaSuccess) {
         delete o;
         return GQ_ERR_CUDA;
     }
     unsigned char *mem = static_cast<unsigned char *>(o->memory);
-    if (!tensors.empty() &&
-        (cudaMemcpy(mem, tensors.data(), tensors.size() * sizeof(AdamTensor), cudaMemcpyHostToDevice) != cudaSuccess ||
-         cudaMemcpy(mem + tb, table.data(), table.size() * sizeof(AdamChunk), cudaMemcpyHostToDevice) != cudaSuccess)) {
+    if (bytes && cudaMemcpy(mem, table.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess) {
         cudaFree(o->memory);
         delete o;
         return GQ_ERR_CUDA;
     }
-    o->a = AdamArgs{c.param_dtype, c.grad_dtype, c.state_bits, master, chunks, reinterpret_cast<AdamTensor *>(mem),
-                    reinterpret_cast<AdamChunk *>(mem + tb), c.seed};
-    o->parts = reinterpret_cast<double *>(mem + tb + cb);
+    o->a = AdamArgs{c.param_dtype, c.grad_dtype, c.state_bits, master, aligned_chunks, chunks, reinterpret_cast<AdamChunk *>(mem), c.seed};
+    o->parts = reinterpret_cast<double *>(mem + bytes);
     *out = o;
     return GQ_OK;
 }
