@@ -24,7 +24,7 @@ struct Shape {
     static constexpr int kUnits = 148 / GROUP;               // that run at once
     static constexpr int kWBytes = 128 * 128, kXRows = TN / GROUP, kXBytes = kXRows * 128;
     static constexpr int kStageBytes = kWBytes + kXBytes;
-    static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+    static constexpr int kStages = 229376 / kStageBytes < 8 ? 229376 / kStageBytes : 8;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     // TMEM: two accumulators of TN columns, then two buffers of exponents (4 columns for 128 features, TN / 32 but
     // at least 4 for the tokens).  With 256 tokens they do not all fit into 512 columns, and the accumulators share 32.
@@ -35,7 +35,7 @@ struct Shape {
 };
 static_assert(Shape<2, 256>::kExps + 2 * Shape<2, 256>::kExpCols <= 512, "TMEM");
 
-constexpr int kThreads = 512;  // warps: 4 of control (copies, MMA, relay, idle), 8 of epilogue, 4 of exponents
+constexpr int kThreads = 512;  // warps: 4 of control (copies, MMA, two idle), 8 of epilogue, 4 of exponents
 constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsEpi = 192, kRegsExp = 72;
 static_assert(4 * kRegsCtl + 8 * kRegsEpi + 4 * kRegsExp <= 16 * kRegsLaunch, "setmaxnreg: the shares come from the launch's registers");
 constexpr int kMaxUnits = 148;
@@ -215,10 +215,39 @@ __device__ __forceinline__ void tmem_store4(uint32_t addr, const uint32_t *v)
                  : "memory");
 }
 
+// A box of 128 bytes a row into this CTA's shared memory; of a pair, either CTA's copies complete on the leader's barrier.
+template <int GROUP>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    if constexpr (GROUP == 1)
+        tma_load_2d(dst, map, x, y, bar);
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 struct Shared {
-    unsigned long long full[8];       // this CTA's operands have arrived
-    unsigned long long peer_full[8];  // the other CTA's have (the leader's is used)
-    unsigned long long empty[8];      // the MMAs have read both
+    unsigned long long full[8];       // both CTAs' operands have arrived (the leader's)
+    unsigned long long empty[8];      // the MMAs have read them
     unsigned long long exp_full[2];   // the exponents of four stages are in TMEM, of both CTAs (the leader's)
     unsigned long long exp_empty[2];  // the MMAs have read them
     unsigned long long acc_full[2];   // a run's sums are complete
@@ -303,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.peer_full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -333,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
-            // TMA: 128 features and this CTA's tokens of every stage
+            // TMA: 128 features and this CTA's tokens of every stage.  The leader's barrier expects both CTAs' bytes; the
+            // other's may arrive first, but not in an earlier phase: that one had ended when its stage was free again.
+            const uint32_t full = in_cta(smem_u32(&sh.full[0]), 0);
             Ring<S::kStages> r;
             bool ok = true;
             Item it;
@@ -344,15 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                         ok = false;
                         break;
                     }
-                    const uint32_t base = stages + r.st * S::kStageBytes, bar = smem_u32(&sh.full[r.st]);
-                    mbar_arrive_expect_tx(&sh.full[r.st], S::kStageBytes);
-                    tma_load_2d(base, &p.w, b * 128, w0, bar);
-                    tma_load_2d(base + S::kWBytes, &p.x, b * 128, x0, bar);
+                    const uint32_t base = stages + r.st * S::kStageBytes, bar = full + r.st * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[r.st], GROUP * S::kStageBytes);
+                    load_box<GROUP>(base, &p.w, b * 128, w0, bar);
+                    load_box<GROUP>(base + S::kWBytes, &p.x, b * 128, x0, bar);
                     r.next();
                 }
             }
             // what is still under way into this CTA's shared memory arrives before the CTA may leave: the MMAs'
-            // signals (after which the copies have been read), or, where a wait gave up, the copies
+            // signals (after which the copies have been read), or, where a wait gave up, the copies, for which the
+            // leader waits (and the other for the leader, at the end)
             const int used = r.turn > 0 ? S::kStages : r.st;
             for (int i = 0; i < used; ++i) {
                 if (r.st == 0) {
@@ -360,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                     --r.turn;
                 }
                 --r.st;
-                mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.parity(), p.limit);
+                if (ok || rank == 0) mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.parity(), p.limit);
             }
         } else if (warp == 1 && rank == 0) {
             // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one lane
@@ -390,8 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                             }
                             ew = tmem + S::kExps + eb * S::kExpCols;
                         }
-                        if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.parity(), p.limit) ||
-                            (GROUP == 2 && !mbar_wait_cycles_warp(smem_u32(&sh.peer_full[r.st]), r.parity(), p.limit))) {
+                        if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.parity(), p.limit)) {
                             ok = false;
                             break;
                         }
@@ -415,22 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                     __syncwarp();
                 }
             }
-        } else if (GROUP == 2 && warp == 2 && rank == 1) {
-            // tells the leader that this CTA's operands have arrived
-            const uint32_t to = in_cta(smem_u32(&sh.peer_full[0]), 0);
-            Ring<S::kStages> r;
-            bool ok = true;
-            Item it;
-            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units)
-                for (int b = it.first; b < it.last; ++b) {
-                    if (!mbar_wait_cycles_warp(smem_u32(&sh.full[r.st]), r.parity(), p.limit)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) arrive_cluster(to + r.st * 8);
-                    __syncwarp();
-                    r.next();
-                }
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
@@ -438,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
         // Columns that the two accumulators share (the first one's last, the second one's first) are read before all
         // others, kHeld of them, so that the other accumulator's MMAs can go on.
         constexpr int kHalf = TN / 2, kHeld = S::kShared ? 32 : 0, kRest = kHalf - kHeld;
-        static_assert(S::kShared <= 32 && kRest % 16 == 0, "columns");
+        static_assert(S::kShared <= kHeld && (kHeld == 0 || kHeld == 32) && kRest % 16 == 0, "columns");
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
         const bool upper = warp >= 8;
         const int held0 = upper ? kRest : 0, rest0 = upper ? 0 : kHeld;
@@ -459,14 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                 ok = ok && mbar_wait_cycles_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t cols = lanes + buf * S::kSecond;
-                float held[kHeld ? kHeld : 1];
+                float held[32];
                 if constexpr (kHeld != 0) {
+                    tmem_load32(cols + held0, held);
+                    if constexpr (SUMS) {
 #pragma unroll
-                    for (int c = 0; c < kHeld; c += 16) {
-                        float v[16];
-                        tmem_load16(cols + held0 + c, v);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) held[c + j] = SUMS ? acc[SUMS ? c + j : 0] + v[j] : v[j];
+                        for (int j = 0; j < kHeld; ++j) held[j] += acc[j];
                     }
                     if (upper == (buf == 0)) {
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -478,11 +490,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                 if constexpr (SUMS) {
                     if (!end || b > it.first) {
 #pragma unroll
-                        for (int c = 0; c < kRest; c += 16) {
-                            float v[16];
-                            tmem_load16(cols + rest0 + c, v);
+                        for (int c = 0; c + 32 <= kRest; c += 32) {
+                            float v[32];
+                            tmem_load32(cols + rest0 + c, v);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[kHeld + c + j] += v[j];
+                            for (int j = 0; j < 32; ++j) acc[kHeld + c + j] += v[j];
+                        }
+                        if constexpr (kRest % 32 != 0) {
+                            float v[16];
+                            tmem_load16(cols + rest0 + kRest - 16, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[kHeld + kRest - 16 + j] += v[j];
                         }
 #pragma unroll
                         for (int j = 0; j < kHeld; ++j) acc[j] = held[j];
