@@ -17,14 +17,18 @@
 namespace gq {
 namespace {
 
-// How a tile is made: by `group` CTAs (two share their operands), 128 * group features x tn tokens.
+// How a tile is made: 128 * group features x tn tokens by `group` CTAs.
+//   2  a pair of CTAs shares the operands of a large tile, and walks over tiles;
+//   1  a CTA makes a tile of few tokens, or a part of it: clusters of CTAs cut the columns among them and add their
+//      sums up through each other's shared memory.
 template <int GROUP, int TN>
 struct Shape {
     static constexpr int kGroup = GROUP, kTokens = TN, kFeatures = 128 * GROUP;
-    static constexpr int kUnits = 148 / GROUP;               // that run at once
+    static constexpr int kPerSm = GROUP == 2 || TN > 64 ? 1 : 2;  // CTAs of an SM
+    static constexpr int kEpiWarps = GROUP == 2 ? 8 : 4, kThreads = (8 + kEpiWarps) * 32;
     static constexpr int kWBytes = 128 * 128, kXRows = TN / GROUP, kXBytes = kXRows * 128;
     static constexpr int kStageBytes = kWBytes + kXBytes;
-    static constexpr int kStages = 229376 / kStageBytes < 8 ? 229376 / kStageBytes : 8;
+    static constexpr int kStages = 229376 / kPerSm / kStageBytes < 8 ? 229376 / kPerSm / kStageBytes : 8;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     // TMEM: two accumulators of TN columns, then two buffers of exponents (4 columns for 128 features, TN / 32 but
     // at least 4 for the tokens).  With 256 tokens they do not all fit into 512 columns, and the accumulators share 32.
@@ -32,33 +36,52 @@ struct Shape {
     static constexpr int kShared = TN > 128 ? 32 : 0;
     static constexpr int kSecond = TN - kShared;             // the second accumulator's first column
     static constexpr int kExps = kSecond + TN;
+    static constexpr int kTmem = kExps + 2 * kExpCols <= 128 ? 128 : kExps + 2 * kExpCols <= 256 ? 256 : 512;
 };
 static_assert(Shape<2, 256>::kExps + 2 * Shape<2, 256>::kExpCols <= 512, "TMEM");
 
-constexpr int kThreads = 512;  // warps: 4 of control (copies, MMA, two idle), 8 of epilogue, 4 of exponents
+// Warps: 4 of control (copies, MMA, two idle), 4 of exponents, 8 or 4 of epilogue.  A pair's epilogue holds 128 sums in
+// each thread's registers, more than an even split gives.
 constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsEpi = 192, kRegsExp = 72;
 static_assert(4 * kRegsCtl + 8 * kRegsEpi + 4 * kRegsExp <= 16 * kRegsLaunch, "setmaxnreg: the shares come from the launch's registers");
-constexpr int kMaxUnits = 148;
+// Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums are cut off, not
+// rounded, after every 32 products: over 4096 columns of positive products they come out some 8e-7 small, no more than
+// a float32 product rounded step by step is off.
+constexpr int kRun = 32;
+constexpr int kPairs = 74;        // CTA pairs of the 148 SMs
+constexpr int kMaxSplits = 8;     // CTAs of a portable cluster
 
-// How the tiles are spread over the units: whole rounds of a tile a unit first; the stages of the last, partial round's
-// tiles are one line, cut into `ranges` equal ranges, one a unit.  A range's part of a tile goes to the workspace, where a
+// How the tiles are spread over the pairs: whole rounds of a tile a pair first; the stages of the last, partial round's
+// tiles are one line, cut into `ranges` equal ranges, one a pair.  A range's part of a tile goes to the workspace, where a
 // second kernel joins them, unless it is the whole tile.
 struct Schedule {
     int tiles_w, tiles_x;
+    int blocks;            // stages of a tile
+    int splits;            // single CTAs: parts of each tile; nothing of the following
     int64_t whole;         // tiles of the whole rounds
     int cut, ranges;       // tiles of the last one, and the ranges that they are cut into
-    int units, blocks;     // units launched; stages of a tile
-    int64_t start[kMaxUnits + 1];
-    uint8_t tile[kMaxUnits], from[kMaxUnits], to[kMaxUnits];
+    int units;             // pairs launched
+    int64_t start[kPairs + 1];
+    uint8_t tile[kPairs], from[kPairs], to[kPairs];
 };
 
-Schedule schedule(int units, int64_t features, int64_t tokens, int tw, int tx, int64_t k)
+template <class S>
+Schedule schedule(int64_t features, int64_t tokens, int64_t k)
 {
+    constexpr int tw = S::kFeatures, tx = S::kTokens, units = kPairs;
     Schedule s;
     s.tiles_w = (int)((features + tw - 1) / tw);
     s.tiles_x = (int)((tokens + tx - 1) / tx);
     s.blocks = (int)((k + 127) / 128);
     const int64_t tiles = (int64_t)s.tiles_w * s.tiles_x;
+    if (S::kGroup == 1) {
+        // as many parts as there is room for, of two stages at least
+        s.splits = 1;
+        while (s.splits < kMaxSplits && tiles * s.splits * 2 <= 148 * S::kPerSm && s.splits * 4 <= s.blocks) s.splits *= 2;
+        s.cut = s.ranges = 0;
+        return s;
+    }
+    s.splits = 1;
     s.cut = (int)(tiles % units);
     s.whole = tiles - s.cut;
     s.ranges = s.cut;
@@ -105,7 +128,6 @@ struct Params {
     Schedule s;
     Exps ew, ex;
     uint32_t idesc;     // without the exponents' byte numbers
-    int run;            // stages summed in TMEM before their sums are added to registers
     int64_t tokens, features;
     const float *bias;
     void *y;
@@ -132,8 +154,21 @@ __device__ __forceinline__ void tile_place(const Schedule &s, int64_t tile, Item
     it.tw = (int)g * 8 + rest - it.tx * wide;
 }
 
-__device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, Item &it)
+// The i-th item of a pair, or a single CTA's only one (i = 0).
+template <int GROUP>
+__device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, uint32_t rank, Item &it)
 {
+    if constexpr (GROUP == 1) {
+        if (i != 0) return false;
+        const uint32_t tile = blockIdx.x / (uint32_t)s.splits;
+        it.tx = (int)(tile / (uint32_t)s.tiles_w);
+        it.tw = (int)(tile - (uint32_t)it.tx * (uint32_t)s.tiles_w);
+        it.first = (int)((int64_t)s.blocks * rank / s.splits);
+        it.last = (int)((int64_t)s.blocks * (rank + 1) / s.splits);
+        it.part = s.splits > 1 ? 0 : -1;
+        return true;
+    }
+    i = (blockIdx.x >> 1) + i * s.units;
     int64_t tile;
     if (i < s.whole) {
         tile = i;
@@ -254,6 +289,7 @@ struct Shared {
     unsigned long long acc_empty[2];  // both CTAs have read them (the leader's)
     unsigned long long edge[2];       // both CTAs have read the columns that the other accumulator shares (the leader's)
     uint32_t tmem;
+    int failed;                       // a single CTA's wait gave up
 };
 
 template <typename T>
@@ -269,18 +305,18 @@ __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half
 template <typename T, class S>
 struct Out {
     T *y;
-    float *part;      // the workspace, nullptr: y
+    float *part;      // the workspace, or (single CTAs) shared memory; nullptr: y
     int64_t sy;
     int n;            // tokens that exist
     float bias;
     bool add, ok;
 
-    __device__ __forceinline__ Out(const Params &p, const Item &it, int x0, int count, int row, bool ok_) : sy(p.sy), ok(ok_)
+    __device__ __forceinline__ Out(const Params &p, const Item &it, float *shared, int x0, int count, int row, bool ok_) : sy(p.sy), ok(ok_)
     {
         const int64_t feature = (int64_t)it.tw * S::kFeatures + row, token = (int64_t)it.tx * S::kTokens + x0;
         const int64_t left = p.tokens - token;
         const bool in = feature < p.features;
-        part = it.part < 0 ? nullptr : p.parts + ((int64_t)it.part * S::kTokens + x0) * S::kFeatures + row;
+        part = it.part < 0 ? nullptr : (S::kGroup == 1 ? shared : p.parts + (int64_t)it.part * S::kTokens * S::kFeatures) + x0 * S::kFeatures + row;
         n = in ? (int)(left < 0 ? 0 : left < count ? left : count) : 0;
         y = static_cast<T *>(p.y) + token * sy + feature;
         bias = p.bias && in && !part ? p.bias[feature] : 0.0f;
@@ -317,19 +353,62 @@ struct Out {
     }
 };
 
+__device__ __forceinline__ uint32_t load_cluster(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The parts of a cluster's tile, one in each CTA's shared memory, in order to y: every CTA takes some of the tokens.
+template <typename T, class S>
+__device__ __forceinline__ void join_cluster(const Params &p, Shared &sh, float *shared, uint32_t rank)
+{
+    cluster_sync();
+    Item it;
+    item_of<1>(p.s, 0, rank, it);
+    const int splits = p.s.splits, f = (int)(threadIdx.x & 127);
+    const int64_t feature = (int64_t)it.tw * S::kFeatures + f, token = (int64_t)it.tx * S::kTokens;
+    const int n = (int)min((int64_t)S::kTokens, p.tokens - token);
+    uint32_t failed = 0;
+    for (int r = 0; r < splits; ++r) failed |= load_cluster(in_cta(smem_u32(&sh.failed), (uint32_t)r));
+    if (feature < p.features) {
+        const float bias = p.bias ? p.bias[feature] : 0.0f;
+        T *const y = static_cast<T *>(p.y) + token * p.sy + feature;
+        const uint32_t from = smem_u32(shared + f);
+        for (int x = (int)rank + splits * (int)(threadIdx.x >> 7); x < n; x += splits * (S::kThreads / 128)) {
+            float part[kMaxSplits];
+#pragma unroll
+            for (int r = 0; r < kMaxSplits; ++r)
+                part[r] = r < splits ? __uint_as_float(load_cluster(in_cta(from + x * S::kFeatures * 4, (uint32_t)r))) : 0.0f;
+            float v = part[0];
+#pragma unroll
+            for (int r = 1; r < kMaxSplits; ++r)
+                if (r < splits) v += part[r];
+            v += bias;
+            if constexpr (sizeof(T) == 4) {
+                if (p.accumulate) v += y[x * p.sy];
+            }
+            y[x * p.sy] = rounded<T>(failed ? __uint_as_float(0x7fffffffu) : v);
+        }
+    }
+    cluster_sync();  // until all have read
+}
+
 // SUMS: runs' sums are added up in registers, rounded to nearest; else a tile is one run.
 template <typename T, int GROUP, int TN, bool SUMS>
-__global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::kPerSm) k_mm(const __grid_constant__ Params p)
 {
     using S = Shape<GROUP, TN>;
     extern __shared__ unsigned char raw_smem[];
     __shared__ Shared sh;
     const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t rank = GROUP == 2 ? cluster_rank() : 0u;
-    const int64_t unit = blockIdx.x / GROUP, units = p.s.units;
+    const uint32_t rank = cluster_rank(), leader = GROUP == 2 ? 0u : rank;  // whose barriers the MMAs go by
+    const int pair_rank = GROUP == 2 ? (int)rank : 0;
 
     if (threadIdx.x == 0) {
+        sh.failed = 0;
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
@@ -338,17 +417,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
             mbar_init(&sh.exp_full[i], 4 * GROUP);
             mbar_init(&sh.exp_empty[i], 1);
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 8 * GROUP);
+            mbar_init(&sh.acc_empty[i], S::kEpiWarps * GROUP);
             mbar_init(&sh.edge[i], 4 * GROUP);
         }
         fence_barrier_init();
     }
     if (warp == 1) {
         if constexpr (GROUP == 2) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(S::kTmem) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(S::kTmem) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
@@ -359,23 +438,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
     const uint32_t tmem = sh.tmem;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
             // TMA: 128 features and this CTA's tokens of every stage.  The leader's barrier expects both CTAs' bytes; the
             // other's may arrive first, but not in an earlier phase: that one had ended when its stage was free again.
-            const uint32_t full = in_cta(smem_u32(&sh.full[0]), 0);
+            const uint32_t full = in_cta(smem_u32(&sh.full[0]), leader);
             Ring<S::kStages> r;
             bool ok = true;
             Item it;
-            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
-                const int w0 = it.tw * S::kFeatures + (int)rank * 128, x0 = it.tx * S::kTokens + (int)rank * S::kXRows;
+            for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
+                const int w0 = it.tw * S::kFeatures + pair_rank * 128, x0 = it.tx * S::kTokens + pair_rank * S::kXRows;
                 for (int b = it.first; b < it.last; ++b) {
                     if (r.turn > 0 && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
                         ok = false;
                         break;
                     }
                     const uint32_t base = stages + r.st * S::kStageBytes, bar = full + r.st * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[r.st], GROUP * S::kStageBytes);
+                    if (rank == leader) mbar_arrive_expect_tx(&sh.full[r.st], GROUP * S::kStageBytes);
                     load_box<GROUP>(base, &p.w, b * 128, w0, bar);
                     load_box<GROUP>(base + S::kWBytes, &p.x, b * 128, x0, bar);
                     r.next();
@@ -391,9 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                     --r.turn;
                 }
                 --r.st;
-                if (ok || rank == 0) mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.parity(), p.limit);
+                if (ok || rank == leader) mbar_wait_cycles(smem_u32(ok ? &sh.empty[r.st] : &sh.full[r.st]), r.parity(), p.limit);
             }
-        } else if (warp == 1 && rank == 0) {
+        } else if (warp == 1 && rank == leader) {
             // MMA, by the leader CTA: the warp stays together, so that descriptors are uniform values, and one lane
             // issues
             const bool one = elect_one();
@@ -401,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
             int64_t runs = 0, groups = 0;
             bool ok = true;
             Item it;
-            for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
+            for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
                 uint32_t ew = 0;
                 for (int b = it.first; ok && b < it.last; ++runs) {
                     const int buf = (int)(runs & 1);
@@ -411,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t d = tmem + buf * S::kSecond;
-                    const int end = it.last - b < p.run ? it.last : b + p.run;
+                    const int end = it.last - b < kRun ? it.last : b + kRun;
                     for (bool add = false; b < end; ++b, add = true) {
                         const int eb = (int)(groups & 1);
                         if (b == it.first || (b & 3) == 0) {
@@ -446,39 +525,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                 }
             }
         }
-    } else if (warp < 12) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-        // Epilogue: TMEM lane = feature, column = token; four warps take the lower half of the tokens, four the upper.
+    } else if (warp >= 8) {
+        if constexpr (GROUP == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // Epilogue: TMEM lane = feature, column = token; of a pair four warps take the lower half of the tokens, four the
+        // upper.
         // Columns that the two accumulators share (the first one's last, the second one's first) are read before all
         // others, kHeld of them, so that the other accumulator's MMAs can go on.
-        constexpr int kHalf = TN / 2, kHeld = S::kShared ? 32 : 0, kRest = kHalf - kHeld;
+        constexpr int kHalf = GROUP == 2 ? TN / 2 : TN, kHeld = S::kShared ? 32 : 0, kRest = kHalf - kHeld;
         static_assert(S::kShared <= kHeld && (kHeld == 0 || kHeld == 32) && kRest % 16 == 0, "columns");
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
-        const bool upper = warp >= 8;
+        const bool upper = warp >= 12;
         const int held0 = upper ? kRest : 0, rest0 = upper ? 0 : kHeld;
-        const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), 0), edge = in_cta(smem_u32(&sh.edge[0]), 0);
+        const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), leader), edge = in_cta(smem_u32(&sh.edge[0]), leader);
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (upper ? kHalf : 0);
-        const int row = (int)rank * 128 + quarter * 32 + lane;
+        const int row = pair_rank * 128 + quarter * 32 + lane;
         int64_t runs = 0;
         bool ok = true;
         Item it;
-        for (int64_t i = unit; item_of(p.s, i, it); i += units) {
+        for (int64_t i = 0; item_of<GROUP>(p.s, i, rank, it); ++i) {
             float acc[SUMS ? kHalf : 1];
             if constexpr (SUMS) {
 #pragma unroll
                 for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
             }
-            for (int b = it.first; b < it.last; b += p.run, ++runs) {
+            for (int b = it.first; b < it.last; b += kRun, ++runs) {
                 const int buf = (int)(runs & 1);
                 ok = ok && mbar_wait_cycles_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t cols = lanes + buf * S::kSecond;
-                float held[32];
+                const bool end = b + kRun >= it.last;
+                float held[SUMS ? 1 : 32];
                 if constexpr (kHeld != 0) {
-                    tmem_load32(cols + held0, held);
                     if constexpr (SUMS) {
 #pragma unroll
-                        for (int j = 0; j < kHeld; ++j) held[j] += acc[j];
+                        for (int c = 0; c < kHeld; c += 16) {
+                            float v[16];
+                            tmem_load16(cols + held0 + c, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+                        }
+                    } else {
+                        tmem_load32(cols + held0, held);
                     }
                     if (upper == (buf == 0)) {
                         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -486,26 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                         if (lane == 0) arrive_cluster(edge + buf * 8);
                     }
                 }
-                const bool end = b + p.run >= it.last;
                 if constexpr (SUMS) {
-                    if (!end || b > it.first) {
 #pragma unroll
-                        for (int c = 0; c + 32 <= kRest; c += 32) {
-                            float v[32];
-                            tmem_load32(cols + rest0 + c, v);
+                    for (int c = 0; c < kRest; c += 16) {
+                        float v[16];
+                        tmem_load16(cols + rest0 + c, v);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) acc[kHeld + c + j] += v[j];
-                        }
-                        if constexpr (kRest % 32 != 0) {
-                            float v[16];
-                            tmem_load16(cols + rest0 + kRest - 16, v);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[kHeld + kRest - 16 + j] += v[j];
-                        }
-#pragma unroll
-                        for (int j = 0; j < kHeld; ++j) acc[j] = held[j];
+                        for (int j = 0; j < 16; ++j) acc[kHeld + c + j] += v[j];
                     }
-                    if (end && b > it.first) {
+                    if (end) {
                         // The tile's sums go back to TMEM, and from there to memory 16 at a time, in a loop that stays
                         // in the instruction cache.
 #pragma unroll
@@ -515,12 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
                 }
                 if (end) {
                     const int x0 = upper ? kHalf : 0;
-                    const Out<T, S> out(p, it, x0, kHalf, row, ok);
+                    if (GROUP == 1 && !ok) sh.failed = 1;
+                    const Out<T, S> out(p, it, reinterpret_cast<float *>(raw_smem), x0, kHalf, row, ok);
 #pragma unroll
                     for (int c = 0; c < kHeld; c += 16) {
                         float v[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = held[c + j];
+                        for (int j = 0; j < 16; ++j) v[j] = SUMS ? acc[SUMS ? c + j : 0] : held[SUMS ? 0 : c + j];
                         out.put16(v, held0 + c);
                     }
 #pragma unroll 1
@@ -536,20 +613,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExp));
+        if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExp));
         // Exponents: each warp its quarter of the lanes, all four the same words, fetched one group ahead.
         constexpr int kX = S::kExpCols - 4;
-        const uint32_t to = in_cta(smem_u32(&sh.exp_full[0]), 0);
+        const uint32_t to = in_cta(smem_u32(&sh.exp_full[0]), leader);
         const uint32_t lanes = tmem + S::kExps + ((uint32_t)((warp & 3) * 32) << 16);
         int64_t groups = 0;
         bool ok = true;
         Item it;
-        for (int64_t i = unit; ok && item_of(p.s, i, it); i += units) {
+        for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
             const uint8_t *rows[4 + kX];
 #pragma unroll
             for (int c = 0; c < 4 + kX; ++c) {
                 const Exps &e = c < 4 ? p.ew : p.ex;
-                const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + rank * 128 + c * 32 + lane
+                const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + pair_rank * 128 + c * 32 + lane
                                           : (int64_t)it.tx * S::kTokens + (c - 4) * 32 + lane;
                 const bool in = row < e.rows && (c < 4 || (c - 4) * 32 < TN);
                 rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
@@ -580,9 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm(const __grid_constant__ Para
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if constexpr (GROUP == 2) cluster_sync();
+    else if (p.s.splits > 1) join_cluster<T, S>(p, sh, reinterpret_cast<float *>(raw_smem), rank);
     if (warp == 1) {
-        if constexpr (GROUP == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        if constexpr (GROUP == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem));
     }
 }
 
@@ -634,11 +712,9 @@ enum Kind { kPair256, kOne128, kOne64, kOne32 };
 Kind kind_of(int64_t tokens) { return tokens > 128 ? kPair256 : tokens > 64 ? kOne128 : tokens > 32 ? kOne64 : kOne32; }
 
 template <class S>
-Schedule schedule_of(int64_t m, int64_t n, int64_t k) { return schedule(S::kUnits, n, m, S::kFeatures, S::kTokens, k); }
-template <class S>
 size_t workspace_of(int64_t m, int64_t n, int64_t k)
 {
-    return (size_t)part_tiles(schedule_of<S>(m, n, k)) * S::kTokens * S::kFeatures * sizeof(float);
+    return (size_t)part_tiles(schedule<S>(n, m, k)) * S::kTokens * S::kFeatures * sizeof(float);
 }
 
 bool encode_rows(CUtensorMap *map, const void *p, int64_t rows, int64_t pitch, int box_rows)
@@ -662,24 +738,26 @@ cudaError_t launch_kernels(const Params &p, cudaStream_t stream)
 {
     auto kern = k_mm<T, S::kGroup, S::kTokens, SUMS>;
     int per_sm = 0, sms = 0;
-    cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, S::kSmemBytes, &per_sm, &sms);
+    cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), S::kThreads, S::kSmemBytes, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     static const int regs = num_regs(kern);
-    if (regs < kRegsLaunch) return cudaErrorInvalidKernelImage;  // setmaxnreg would wait
+    if (S::kGroup == 2 && regs < kRegsLaunch) return cudaErrorInvalidKernelImage;  // setmaxnreg would wait
+    const int64_t ctas = S::kGroup == 2 ? 2 * (int64_t)p.s.units : (int64_t)p.s.tiles_w * p.s.tiles_x * p.s.splits;
+    if (ctas > (int64_t(1) << 31) - 1) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(S::kGroup * p.s.units));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S::kGroup;
+    attr[0].val.clusterDim.x = (unsigned)(S::kGroup == 2 ? 2 : p.s.splits);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
-    if (e != cudaSuccess || !part_tiles(p.s)) return e;
+    if (S::kGroup == 1 || e != cudaSuccess || !part_tiles(p.s)) return e;
     cfg.gridDim = dim3((unsigned)(p.s.cut * (S::kTokens / (1024 / S::kFeatures))));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -693,7 +771,7 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
 {
     Params p;
     const Fp8Layout lx = fp8_layout(g.tile_a, g.m, g.k), lw = fp8_layout(g.tile_b, g.n, g.k);
-    p.s = schedule_of<S>(g.m, g.n, g.k);
+    p.s = schedule<S>(g.n, g.m, g.k);
     p.ew = exps_of(g.b, g.tile_b, g.n, lw);
     p.ex = exps_of(g.a, g.tile_a, g.m, lx);
     p.idesc = instr_desc(g.format_b, g.format_a, S::kFeatures, S::kTokens);
@@ -709,12 +787,8 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
     p.limit = 4000000000ll;
     if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) || !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kXRows))
         return cudaErrorInvalidValue;
-    if (g.dtype == GQ_FLOAT32) {
-        p.run = 8;
-        return launch_kernels<float, S, true>(p, stream);
-    }
-    const bool sums = p.s.blocks > 128;
-    p.run = sums ? 32 : 128;
+    const bool sums = p.s.blocks > kRun;
+    if (g.dtype == GQ_FLOAT32) return sums ? launch_kernels<float, S, true>(p, stream) : launch_kernels<float, S, false>(p, stream);
     if (g.dtype == GQ_BFLOAT16)
         return sums ? launch_kernels<__nv_bfloat16, S, true>(p, stream) : launch_kernels<__nv_bfloat16, S, false>(p, stream);
     return sums ? launch_kernels<__half, S, true>(p, stream) : launch_kernels<__half, S, false>(p, stream);
@@ -725,12 +799,7 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
 size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k)
 {
     if (m == 0) return 0;
-    switch (kind_of(m)) {
-    case kPair256: return workspace_of<Shape<2, 256>>(m, n, k);
-    case kOne128: return workspace_of<Shape<1, 128>>(m, n, k);
-    case kOne64: return workspace_of<Shape<1, 64>>(m, n, k);
-    default: return workspace_of<Shape<1, 32>>(m, n, k);
-    }
+    return kind_of(m) == kPair256 ? workspace_of<Shape<2, 256>>(m, n, k) : 0;
 }
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs &g, cudaStream_t stream)

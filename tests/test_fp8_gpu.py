@@ -152,9 +152,9 @@ def operand(rows, k, fmt, tile, seed, spread=1.0):
 
 def steps(k):
     """Half-steps of binary32 that a sum over k columns may be off by, relative to the sum of absolute products: two
-    steps for every 32 products while the tensor cores cut off (runs of 1024 at most), three roundings a run, and a few
+    steps for every 32 products while the tensor cores cut off (runs of 4096 at most), three roundings a run, and a few
     for joining parts, the bias and adding."""
-    return 2 * (1024 / 32 * 2 + 3 * (k / 1024 + 1) + 16)
+    return 2 * (min(k, 4096) / 32 * 2 + 3 * (k / 4096 + 1) + 16)
 
 
 def check_product(y, da, db, k, bias=None, before=None):
