@@ -25,21 +25,6 @@ struct Params {
     uint32_t rk0[10], rk1[10];  // Philox round keys
 };
 
-// Two values at a time: each operation rounds its two results alone.
-typedef unsigned long long Two;
-__device__ __forceinline__ Two two(float a, float b)
-{
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ Two mul2(Two a, Two b)
-{
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // The sums are taken one by one: packed sums of packed products come out fused, rounded once.
 __device__ __forceinline__ void sum2(Two a, Two b, float &x, float &y)
 {
@@ -216,9 +201,7 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
                 if (at + j >= n) m[j] = v[j] = 0.0f;
         }
         const uint32_t em = fp8_exp<GQ_FP8_E4M3>(block_max(m)), ev = square_exp(block_max(v));
-        const float inv = fp8_inverse(em);
-        const uint2 qm = make_uint2(fp8_codes4<GQ_FP8_E4M3>(m[0], m[1], m[2], m[3], inv, em),
-                                    fp8_codes4<GQ_FP8_E4M3>(m[4], m[5], m[6], m[7], inv, em));
+        const uint2 qm = fp8_codes8<GQ_FP8_E4M3>(m, em);
         // Philox's counter (element / 8, step, tensor + 2^31)
         const uint64_t group = (uint64_t)(c.group + (at >> 3));
         const uint32_t c0 = (uint32_t)group, c2 = now.step;

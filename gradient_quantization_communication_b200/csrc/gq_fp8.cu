@@ -23,7 +23,7 @@ Packed packed_of(void *p, int tile, int64_t rows, int64_t cols)
 struct Params {
     const void *x;
     int64_t sx, rows;
-    int cols, per_row;  // chunks of 256 columns a row
+    int cols, per_row;  // items a row
     Packed p, t;        // along the rows, along the columns
 };
 
@@ -59,11 +59,21 @@ __device__ __forceinline__ uint32_t row_max(const Words<T> &w)
     return float_bits<T>(sizeof(T) == 4 ? m : max(m & 0xffffu, m >> 16));
 }
 
-template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t E)
+// Columns 2 k and 2 k + 1 of a lane's 8.
+template <typename T>
+__device__ __forceinline__ void two_floats(const Words<T> &w, int k, float &a, float &b)
 {
-    const float inv = fp8_inverse(E);
-    return make_uint2(fp8_codes4<FMT>(v[0], v[1], v[2], v[3], inv, E), fp8_codes4<FMT>(v[4], v[5], v[6], v[7], inv, E));
+    if constexpr (sizeof(T) == 4) {
+        a = __uint_as_float(w.w[2 * k]);
+        b = __uint_as_float(w.w[2 * k + 1]);
+    } else if constexpr (__is_same(T, __half)) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w.w[k]));
+        a = f.x;
+        b = f.y;
+    } else {
+        a = __uint_as_float(w.w[k] << 16);
+        b = __uint_as_float(w.w[k] & 0xffff0000u);
+    }
 }
 
 // A lane's 8 codes of a row, its block's exponent, and, behind the row's last block, the exponents' padding.
@@ -83,44 +93,64 @@ __device__ __forceinline__ void store_row(const Packed &p, int64_t row, int64_t 
 }
 
 // ---------------------------------------------------------------------------------------------
-// Along the rows only: a warp takes 256 columns of a row at a time.
+// Along the rows only: a warp takes up to N chunks of 256 columns of a row at a time, all loaded before the first is
+// used.  One where there are no more chunks than warps that the device holds (16 x 4096 bf16: 2.0 us against 2.8 with
+// four), else four (16384 x 8192: 67 us against 92 with one).
 // ---------------------------------------------------------------------------------------------
-template <typename T, int FMT, bool AL>
+constexpr int kAhead = 4;
+constexpr int64_t kFewChunks = 148 * 16 * 2;
+
+template <typename T, int FMT, bool AL, bool FULL, int N>
+__device__ __forceinline__ void pack_item(const Params &p, int64_t row, int base, int lane)
+{
+    const T *const x = static_cast<const T *>(p.x) + row * p.sx;
+    Raw<T, AL> r[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (!FULL && u > 0 && base + u * kChunk >= p.cols) break;
+        chunk_load<T, AL, FULL>(r[u], x, base + u * kChunk, lane, p.cols);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (!FULL && u > 0 && base + u * kChunk >= p.cols) break;
+        const Words<T> w = in_place<T, AL>(r[u], x);
+        const uint32_t E = fp8_exp<FMT>(row_max<T>(w));
+        float v[8];
+        to_floats(w, v);
+        store_row(p.p, row, row, base + u * kChunk, lane, fp8_codes8<FMT>(v, E), E, true);
+    }
+}
+
+template <typename T, int FMT, bool AL, int N>
 __global__ void __launch_bounds__(256) k_pack_rows(const __grid_constant__ Params p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t n = p.rows * p.per_row, warps = (int64_t)gridDim.x * 8;
     for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += warps) {
         const int64_t row = id / p.per_row;
-        const int base = (int)(id - row * p.per_row) * kChunk;
-        const T *const x = static_cast<const T *>(p.x) + row * p.sx;
-        Raw<T, AL> r;
-        chunk_load<T, AL>(r, x, base, lane, p.cols);
-        const Words<T> w = in_place<T, AL>(r, x);
-        const uint32_t E = fp8_exp<FMT>(row_max<T>(w));
-        float v[8];
-        to_floats(w, v);
-        store_row(p.p, row, row, base, lane, codes8<FMT>(v, E), E, true);
+        const int base = (int)(id - row * p.per_row) * (N * kChunk);
+        if (AL && base + N * kChunk <= p.cols) pack_item<T, FMT, AL, AL, N>(p, row, base, lane);
+        else pack_item<T, FMT, AL, false, N>(p, row, base, lane);
     }
 }
 
 // ---------------------------------------------------------------------------------------------
-// 128 rows x 256 columns a block: along the columns, along both, and square tiles.  A warp takes 8 rows, a lane 8
-// columns of them, so that a lane's 8 codes of a column are one 8-byte piece of the transpose.
+// 128 rows x 128 columns a block: along the columns, along both, and square tiles.  Half a warp takes 8 rows, a lane 8
+// columns of them, so that a lane's 8 codes of a column are one 8-byte piece of the transpose.  A block loads, finds its
+// largest values, and stores, with barriers between: as many blocks an SM as registers allow hide that from one another
+// (16384 x 8192 bf16 both ways: 130 us with two blocks of 512 threads on 256 columns, 110 with four of these).
 // ---------------------------------------------------------------------------------------------
-constexpr int kTileWarps = 16;
+constexpr int kTileWarps = 8;
 
-template <typename T, int FMT, bool TILE, bool AL>
-__global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_constant__ Params p)
+template <typename T, int FMT, bool TILE, bool AL, bool FULL>
+__device__ __forceinline__ void pack_tile(const Params &p, uint8_t *codes, uint8_t *exps)
 {
     constexpr int W = 2 * (int)sizeof(T);  // words of a lane's 8 columns
-    __shared__ __align__(16) uint8_t codes[kChunk * kBlock];  // transposed codes; before that, the warps' largest values
-    __shared__ uint8_t exps[kChunk];                          // of every column (TILE: the first two, of the two tiles)
-    uint32_t *const most = reinterpret_cast<uint32_t *>(codes);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t *const most = reinterpret_cast<uint32_t *>(codes);  // the halves' largest values, before the codes
+    const int lane = threadIdx.x & 15, piece = threadIdx.x >> 4;  // of 8 rows
     const int64_t tile = blockIdx.x / p.per_row;
-    const int base = (int)(blockIdx.x - tile * p.per_row) * kChunk;
-    const int64_t row0 = tile * kBlock + warp * 8;
+    const int base = (int)(blockIdx.x - tile * p.per_row) * kBlock;
+    const int64_t row0 = tile * kBlock + piece * 8;
 
     Words<T> w[8];
     {
@@ -128,8 +158,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_c
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const T *const x = static_cast<const T *>(p.x) + (row0 + i) * p.sx;
-            if (row0 + i < p.rows) {
-                chunk_load<T, AL>(r[i], x, base, lane, p.cols);
+            if (FULL || row0 + i < p.rows) {
+                chunk_load<T, AL, FULL>(r[i], x, base, lane, p.cols);
             } else {
 #pragma unroll
                 for (int k = 0; k < (int)(sizeof(r[i].w) / 4); ++k) r[i].w[k] = 0u;
@@ -139,7 +169,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_c
         for (int i = 0; i < 8; ++i) w[i] = in_place<T, AL>(r[i], static_cast<const T *>(p.x) + (row0 + i) * p.sx);
     }
 
-    uint32_t col[W];  // largest of the warp's rows
+    uint32_t col[W];  // largest of the 8 rows
 #pragma unroll
     for (int k = 0; k < W; ++k) {
         col[k] = abs_word<T>(w[0].w[k]);
@@ -151,34 +181,33 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_c
 #pragma unroll
         for (int k = 0; k < W; ++k) c.w[k] = col[k];
         const uint32_t m = row_max<T>(c);
-        if ((lane & 15) == 0) most[warp * 2 + (lane >> 4)] = m;
+        if (lane == 0) most[piece] = m;
     } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) most[(warp * W + k) * 32 + lane] = col[k];
+        for (int k = 0; k < W; ++k) most[(piece * W + k) * 16 + lane] = col[k];
     }
     __syncthreads();
     uint32_t E = 0;
     if constexpr (TILE) {
-        if (threadIdx.x < 2) {
+        if (threadIdx.x == 0) {
             uint32_t m = 0;
-            for (int i = 0; i < kTileWarps; ++i) m = max(m, most[i * 2 + threadIdx.x]);
+            for (int i = 0; i < 2 * kTileWarps; ++i) m = max(m, most[i]);
             E = fp8_exp<FMT>(m);
         }
-    } else if (threadIdx.x < kChunk) {
-        // column 8 l + j of the chunk: word j (or half of word j / 2) of lane l
+    } else if (threadIdx.x < kBlock) {
+        // column 8 l + j: word j (or half of word j / 2) of lane l
         const int l = threadIdx.x >> 3, j = threadIdx.x & 7;
         uint32_t m = 0;
-        for (int i = 0; i < kTileWarps; ++i)
-            m = max_word<T>(m, most[(i * W + (sizeof(T) == 4 ? j : j >> 1)) * 32 + l]);
+        for (int i = 0; i < 2 * kTileWarps; ++i) m = max_word<T>(m, most[(i * W + (sizeof(T) == 4 ? j : j >> 1)) * 16 + l]);
         if (sizeof(T) == 2) m = (j & 1) ? m >> 16 : m & 0xffffu;
         E = fp8_exp<FMT>(float_bits<T>(m));
     }
-    if (threadIdx.x < (TILE ? 2 : kChunk)) {
+    if (threadIdx.x < (TILE ? 1 : kBlock)) {
         exps[threadIdx.x] = (uint8_t)E;
         if (p.t.codes) {
             // the transpose's row: the column (TILE: 128 of them), its block: this one's rows
-            const int64_t r = TILE ? base / kBlock + threadIdx.x : base + threadIdx.x;
-            if (r < (TILE ? (p.cols + kBlock - 1) / kBlock : p.cols)) {
+            const int64_t r = TILE ? base / kBlock : base + threadIdx.x;
+            if (TILE || r < p.cols) {
                 uint8_t *e = p.t.exps + r * p.t.exp_pitch;
                 e[tile] = (uint8_t)E;
                 if (tile + 1 == p.t.blocks)
@@ -188,37 +217,81 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) k_pack_tile(const __grid_c
     }
     __syncthreads();
 
-    float v[8][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) to_floats(w[i], v[i]);
     if (p.p.codes) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t e = TILE ? exps[lane >> 4] : fp8_exp<FMT>(row_max<T>(w[i]));
-            const uint2 q = codes8<FMT>(v[i], e);
-            if (row0 + i < p.rows) store_row(p.p, row0 + i, TILE ? tile : row0 + i, base, lane, q, e, !TILE || (warp == 0 && i == 0));
+            const uint32_t e = TILE ? exps[0] : fp8_exp<FMT>(row_max<T>(w[i]));
+            float v[8];
+            to_floats(w[i], v);
+            const uint2 q = fp8_codes8<FMT>(v, e);
+            if (FULL || row0 + i < p.rows)
+                store_row(p.p, row0 + i, TILE ? tile : row0 + i, base, lane, q, e, !TILE || (piece == 0 && i == 0));
         }
     }
     if (!p.t.codes) return;
-    // Piece `warp` (8 rows) of column c lies at piece warp ^ (c / 8 mod 16) of its 128 bytes: the 16 lanes of half a
-    // warp, 8 columns apart, then store to different banks.
+    // Piece i (8 rows) of column c lies at piece i ^ (c / 8 mod 16) of its 128 bytes: the 16 lanes that store a piece, 8
+    // columns apart, then store to different banks.
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = lane * 8 + j;
-        float x[8];
+    for (int k = 0; k < 4; ++k) {
+        float x[2][8];  // columns 2 k and 2 k + 1
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = v[i][j];
-        const uint32_t e = exps[TILE ? lane >> 4 : c];
-        *reinterpret_cast<uint2 *>(codes + c * kBlock + ((warp ^ (lane & 15)) << 3)) = codes8<FMT>(x, e);
+        for (int i = 0; i < 8; ++i) two_floats<T>(w[i], k, x[0][i], x[1][i]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = lane * 8 + 2 * k + h;
+            const uint32_t e = exps[TILE ? 0 : c];
+            *reinterpret_cast<uint2 *>(codes + c * kBlock + ((piece ^ lane) << 3)) = fp8_codes8<FMT>(x[h], e);
+        }
     }
     __syncthreads();
     // 16-byte pieces, two of 8, in order; a column's 128 bytes by 8 lanes
-    for (int i = threadIdx.x; i < kChunk * 8; i += kTileWarps * 32) {
-        const int c = i >> 3, f = (c >> 3) & 15, piece = (i & 7) * 2;
-        if (base + c >= p.cols) break;
-        uint4 q = *reinterpret_cast<const uint4 *>(codes + c * kBlock + (((piece ^ f) & 14) << 3));
+#pragma unroll
+    for (int i = threadIdx.x; i < kBlock * 8; i += kTileWarps * 32) {
+        const int c = i >> 3, f = (c >> 3) & 15, at = (i & 7) * 2;
+        if (!FULL && base + c >= p.cols) break;
+        uint4 q = *reinterpret_cast<const uint4 *>(codes + c * kBlock + (((at ^ f) & 14) << 3));
         if (f & 1) q = make_uint4(q.z, q.w, q.x, q.y);
-        *reinterpret_cast<uint4 *>(p.t.codes + (int64_t)(base + c) * p.t.code_pitch + tile * kBlock + piece * 8) = q;
+        *reinterpret_cast<uint4 *>(p.t.codes + (int64_t)(base + c) * p.t.code_pitch + tile * kBlock + at * 8) = q;
+    }
+}
+
+template <typename T, int FMT, bool TILE, bool AL>
+__global__ void __launch_bounds__(kTileWarps * 32, sizeof(T) == 4 ? 2 : 4) k_pack_tile(const __grid_constant__ Params p)
+{
+    __shared__ __align__(16) uint8_t codes[kBlock * kBlock];  // transposed
+    __shared__ uint8_t exps[kBlock];                          // of every column (TILE: the first, of all)
+    const int64_t tile = blockIdx.x / p.per_row;
+    const int base = (int)(blockIdx.x - tile * p.per_row) * kBlock;
+    if (AL && (tile + 1) * kBlock <= p.rows && base + kBlock <= p.cols) pack_tile<T, FMT, TILE, AL, AL>(p, codes, exps);
+    else pack_tile<T, FMT, TILE, AL, false>(p, codes, exps);
+}
+
+template <typename T, int FMT, bool TILE, bool AL, bool FULL>
+__device__ __forceinline__ void unpack_item(const Params &p, T *out, int64_t row, int base, int lane)
+{
+    const uint8_t *const codes = p.p.codes + row * p.p.code_pitch;
+    const uint8_t *const exps = p.p.exps + (TILE ? row / kBlock : row) * p.p.exp_pitch;
+    uint2 q[kAhead];
+    uint32_t E[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        const int c = base + u * kChunk + lane * 8;
+        q[u] = make_uint2(0u, 0u);
+        E[u] = 0;
+        if (FULL || c < p.cols) {
+            q[u] = __ldg(reinterpret_cast<const uint2 *>(codes + c));
+            E[u] = __ldg(exps + (c >> 7));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        if (!FULL && u > 0 && base + u * kChunk >= p.cols) break;
+        float v[8];
+        fp8_decode8<FMT>(q[u], fp8_scale(E[u]), v);
+        saturate<T>(v);
+        Words<T> w;
+        from_floats(w, v);
+        chunk_store<T, AL, FULL>(w, out + row * p.sx, base + u * kChunk, lane, p.cols);
     }
 }
 
@@ -229,24 +302,16 @@ __global__ void __launch_bounds__(256) k_unpack(const __grid_constant__ Params p
     const int64_t n = p.rows * p.per_row, warps = (int64_t)gridDim.x * 8;
     for (int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); id < n; id += warps) {
         const int64_t row = id / p.per_row;
-        const int base = (int)(id - row * p.per_row) * kChunk, c = base + lane * 8;
-        uint2 q = make_uint2(0u, 0u);
-        uint32_t E = 0;
-        if (c < p.cols) {
-            q = __ldg(reinterpret_cast<const uint2 *>(p.p.codes + row * p.p.code_pitch + c));
-            E = __ldg(p.p.exps + (TILE ? row / kBlock : row) * p.p.exp_pitch + (c >> 7));
-        }
-        float v[8];
-        fp8_decode8<FMT>(q, fp8_scale(E), v);
-        saturate<T>(v);
-        Words<T> w;
-        from_floats(w, v);
-        chunk_store<T, AL>(w, out + row * p.sx, base, lane, p.cols);
+        const int base = (int)(id - row * p.per_row) * (kAhead * kChunk);
+        if (base + kAhead * kChunk <= p.cols) unpack_item<T, FMT, TILE, AL, true>(p, out, row, base, lane);
+        else unpack_item<T, FMT, TILE, AL, false>(p, out, row, base, lane);
     }
 }
 
 template <typename T>
 bool rows_aligned(const Params &p) { return p.rows <= 1 || p.sx % (16 / (int64_t)sizeof(T)) == 0; }
+
+bool few_chunks(int64_t rows, int64_t cols) { return rows * ((cols + kChunk - 1) / kChunk) <= kFewChunks; }
 
 unsigned warp_grid(const Params &p)
 {
@@ -259,8 +324,13 @@ cudaError_t pack(const Params &p, int tile, cudaStream_t s)
 {
     const bool al = rows_aligned<T>(p);
     if (!tile && !p.t.codes) {
-        if (al) k_pack_rows<T, FMT, true><<<warp_grid(p), 256, 0, s>>>(p);
-        else k_pack_rows<T, FMT, false><<<warp_grid(p), 256, 0, s>>>(p);
+        if (few_chunks(p.rows, p.cols)) {
+            if (al) k_pack_rows<T, FMT, true, 1><<<warp_grid(p), 256, 0, s>>>(p);
+            else k_pack_rows<T, FMT, false, 1><<<warp_grid(p), 256, 0, s>>>(p);
+        } else {
+            if (al) k_pack_rows<T, FMT, true, kAhead><<<warp_grid(p), 256, 0, s>>>(p);
+            else k_pack_rows<T, FMT, false, kAhead><<<warp_grid(p), 256, 0, s>>>(p);
+        }
         return cudaGetLastError();
     }
     const int64_t blocks = (p.rows + kBlock - 1) / kBlock * p.per_row;
@@ -290,14 +360,15 @@ cudaError_t unpack(const Params &p, int tile, T *out, cudaStream_t s)
     return cudaGetLastError();
 }
 
-Params params_of(const Fp8PackArgs &a)
+// width: columns of an item
+Params params_of(const Fp8PackArgs &a, int width)
 {
     Params p = {};
     p.x = a.x.p;
     p.sx = a.rows > 1 ? a.x.stride : 0;
     p.rows = a.rows;
     p.cols = (int)a.cols;
-    p.per_row = (int)((a.cols + kChunk - 1) / kChunk);
+    p.per_row = (int)((a.cols + width - 1) / width);
     p.p = packed_of(a.packed, a.tile, a.rows, a.cols);
     p.t = packed_of(a.packed_t, a.tile, a.cols, a.rows);
     return p;
@@ -306,13 +377,13 @@ Params params_of(const Fp8PackArgs &a)
 template <typename T>
 cudaError_t pack_type(const Fp8PackArgs &a, cudaStream_t s)
 {
-    const Params p = params_of(a);
+    const Params p = params_of(a, a.tile || a.packed_t ? kBlock : few_chunks(a.rows, a.cols) ? kChunk : kAhead * kChunk);
     return a.format == GQ_FP8_E4M3 ? pack<T, GQ_FP8_E4M3>(p, a.tile, s) : pack<T, GQ_FP8_E5M2>(p, a.tile, s);
 }
 template <typename T>
 cudaError_t unpack_type(const Fp8PackArgs &a, cudaStream_t s)
 {
-    const Params p = params_of(a);
+    const Params p = params_of(a, kAhead * kChunk);
     T *const out = static_cast<T *>(const_cast<void *>(a.x.p));
     return a.format == GQ_FP8_E4M3 ? unpack<T, GQ_FP8_E4M3>(p, a.tile, out, s) : unpack<T, GQ_FP8_E5M2>(p, a.tile, out, s);
 }

@@ -19,6 +19,21 @@ namespace gq {
 constexpr int kBlock = 128;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// Two values at a time: each operation rounds its two results alone.
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(Two x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // E of a block whose largest |x| has these bits (a NaN's or infinity's bits give 255).
 template <int FMT>
 __device__ __forceinline__ uint32_t fp8_exp(uint32_t abs_bits)
@@ -33,7 +48,7 @@ __device__ __forceinline__ float fp8_inverse(uint32_t E) { return __uint_as_floa
 // 2^(E - 127); infinity for E = 255, whose codes are NaN.
 __device__ __forceinline__ float fp8_scale(uint32_t E) { return __uint_as_float(E << 23); }
 
-// The codes of two values scaled by fp8_inverse, a in the low byte: nearest, ties to even.
+// The codes of two values already scaled, a in the low byte: nearest, ties to even.
 template <int FMT>
 __device__ __forceinline__ uint32_t fp8_pair(float a, float b)
 {
@@ -42,12 +57,21 @@ __device__ __forceinline__ uint32_t fp8_pair(float a, float b)
     else asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// The codes of four values as one word; a block with E = 255 has codes 0x7f.
+// The codes of 8 values under E; a block with E = 255 has codes 0x7f.
 template <int FMT>
-__device__ __forceinline__ uint32_t fp8_codes4(float a, float b, float c, float d, float inv, uint32_t E)
+__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], uint32_t E)
 {
-    const uint32_t w = fp8_pair<FMT>(__fmul_rn(a, inv), __fmul_rn(b, inv)) | fp8_pair<FMT>(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16;
-    return E == 255u ? 0x7f7f7f7fu : w;
+    const float inv = fp8_inverse(E);
+    const Two scale = two(inv, inv);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        apart(mul2(two(v[2 * i], v[2 * i + 1]), scale), a, b);
+        q[i] = fp8_pair<FMT>(a, b);
+    }
+    if (E == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 // The values of two codes (low byte first), before the scale.
 template <int FMT>
