@@ -17,8 +17,10 @@
 namespace gq {
 namespace {
 
-// How a tile is made: 128 * group features x tn tokens by `group` CTAs.
-//   2  a pair of CTAs shares the operands of a large tile, and walks over tiles;
+// How a tile is made: 128 * group features x up to TN tokens by `group` CTAs.
+//   2  a pair of CTAs shares the operands of a large tile, and walks over tiles.  Their tokens are chosen by the call
+//      (schedule_pairs).  Two accumulators and the exponents leave room for 224; with 256 the accumulators share 32
+//      columns, which the epilogue reads first, and the MMAs of the next tile or run wait for that;
 //   1  a CTA makes a tile of few tokens, or a part of it: clusters of CTAs cut the columns among them and add their
 //      sums up through each other's shared memory.
 template <int GROUP, int TN>
@@ -30,24 +32,27 @@ struct Shape {
     static constexpr int kStageBytes = kWBytes + kXBytes;
     static constexpr int kStages = 229376 / kPerSm / kStageBytes < 8 ? 229376 / kPerSm / kStageBytes : 8;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-    // TMEM: two accumulators of TN columns, then two buffers of exponents (4 columns for 128 features, TN / 32 but
-    // at least 4 for the tokens).  With 256 tokens they do not all fit into 512 columns, and the accumulators share 32.
-    static constexpr int kExpCols = 4 + (TN > 128 ? TN / 32 : 4);
-    static constexpr int kShared = TN > 128 ? 32 : 0;
-    static constexpr int kSecond = TN - kShared;             // the second accumulator's first column
+    // TMEM: two accumulators, the second from column kSecond on (or at a tile's fewer tokens), then two buffers of
+    // exponents (4 columns for 128 features, TN / 32 but at least 4 for the tokens)
+    static constexpr int kExpCols = 4 + (TN > 128 ? 8 : 4);
+    static constexpr int kSecond = TN > 128 ? 224 : TN;
     static constexpr int kExps = kSecond + TN;
     static constexpr int kTmem = kExps + 2 * kExpCols <= 128 ? 128 : kExps + 2 * kExpCols <= 256 ? 256 : 512;
 };
-static_assert(Shape<2, 256>::kExps + 2 * Shape<2, 256>::kExpCols <= 512, "TMEM");
+constexpr int kMostTokens = 256;
+using Pair = Shape<2, kMostTokens>;
+static_assert(Pair::kExps + 2 * Pair::kExpCols <= 512, "TMEM");
+constexpr int kHeld = 32;  // columns that the epilogue reads first: those that two accumulators may share
+static_assert(Pair::kTokens - Pair::kSecond <= kHeld, "shared columns");
 
 // Warps: 4 of control (copies, MMA, two idle), 4 of exponents, 8 or 4 of epilogue.  A pair's epilogue holds 128 sums in
 // each thread's registers, more than an even split gives.
-constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsEpi = 192, kRegsExp = 72;
+constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsEpi = 184, kRegsExp = 96;
 static_assert(4 * kRegsCtl + 8 * kRegsEpi + 4 * kRegsExp <= 16 * kRegsLaunch, "setmaxnreg: the shares come from the launch's registers");
 // Stages summed in TMEM before their sums are added to registers.  The tensor cores' binary32 sums are cut off, not
 // rounded, after every 32 products: over 4096 columns of positive products they come out some 8e-7 small, no more than
-// a float32 product rounded step by step is off.
-constexpr int kRun = 32;
+// a float32 product rounded step by step is off; over 16384 3e-6, a thousandth of what rounding to 16 bits leaves.
+constexpr int kRunWide = 32, kRun16 = 128;
 constexpr int kPairs = 74;        // CTA pairs of the 148 SMs
 constexpr int kMaxSplits = 8;     // CTAs of a portable cluster
 
@@ -55,6 +60,7 @@ constexpr int kMaxSplits = 8;     // CTAs of a portable cluster
 // tiles are one line, cut into `ranges` equal ranges, one a pair.  A range's part of a tile goes to the workspace, where a
 // second kernel joins them, unless it is the whole tile.
 struct Schedule {
+    int tokens;            // of a tile
     int tiles_w, tiles_x;
     int blocks;            // stages of a tile
     int splits;            // single CTAs: parts of each tile; nothing of the following
@@ -65,43 +71,64 @@ struct Schedule {
     uint8_t tile[kPairs], from[kPairs], to[kPairs];
 };
 
+int run_of(int dtype) { return dtype == GQ_FLOAT32 ? kRunWide : kRun16; }
+
 template <class S>
-Schedule schedule(int64_t features, int64_t tokens, int64_t k)
+Schedule schedule_single(int64_t features, int64_t tokens, int64_t k)
 {
-    constexpr int tw = S::kFeatures, tx = S::kTokens, units = kPairs;
-    Schedule s;
-    s.tiles_w = (int)((features + tw - 1) / tw);
-    s.tiles_x = (int)((tokens + tx - 1) / tx);
+    Schedule s = {};
+    s.tokens = S::kTokens;
+    s.tiles_w = (int)((features + 127) / 128);
+    s.tiles_x = (int)((tokens + S::kTokens - 1) / S::kTokens);
     s.blocks = (int)((k + 127) / 128);
-    const int64_t tiles = (int64_t)s.tiles_w * s.tiles_x;
-    if (S::kGroup == 1) {
-        // as many parts as there is room for, of two stages at least
-        s.splits = 1;
-        while (s.splits < kMaxSplits && tiles * s.splits * 2 <= 148 * S::kPerSm && s.splits * 4 <= s.blocks) s.splits *= 2;
-        s.cut = s.ranges = 0;
-        return s;
-    }
+    // as many parts as there is room for, of two stages at least
     s.splits = 1;
-    s.cut = (int)(tiles % units);
-    s.whole = tiles - s.cut;
-    s.ranges = s.cut;
-    if (s.cut) {
-        // A tile a unit, as many equal parts of every tile as there are units for, or equal ranges for all units.
-        const int64_t total = (int64_t)s.cut * s.blocks, most = total / 4 < units ? total / 4 : units;
-        double best = (double)s.blocks;
-        for (int64_t r = 2 * s.cut; r < most + s.cut; r += s.cut) {
+    while (s.splits < kMaxSplits && (int64_t)s.tiles_w * s.tiles_x * s.splits * 2 <= 148 * S::kPerSm && s.splits * 4 <= s.blocks)
+        s.splits *= 2;
+    return s;
+}
+
+// The pairs' tiles: of the widths that TMEM holds the one that is done first, in cycles as measured.
+Schedule schedule_pairs(int64_t features, int64_t tokens, int64_t k)
+{
+    Schedule s = {};
+    s.splits = 1;
+    s.tiles_w = (int)((features + Pair::kFeatures - 1) / Pair::kFeatures);
+    s.blocks = (int)((k + 127) / 128);
+    double best = 1e300;
+    for (int tx = kMostTokens; tx >= 64; tx -= 32) {  // pairs take their N in steps of 32
+        const int64_t tiles_x = (tokens + tx - 1) / tx, tiles = s.tiles_w * tiles_x;
+        // a stage: 550 cycles with 128 tokens, 620 with 224, 650 with 256, for its way through L2 (13.5 TB/s in all)
+        const double stage = 430 + 0.85 * tx;
+        const int64_t cut = tiles % kPairs, rounds = tiles / kPairs;
+        if (tx > Pair::kSecond && s.blocks > kRunWide) continue;  // the MMAs would wait at every run: 890 us against 810
+        const double before = (double)rounds * s.blocks * stage;
+        auto take = [&](int64_t ranges, double cycles) {
+            if (cycles >= best) return;
+            best = cycles;
+            s.tokens = tx;
+            s.tiles_x = (int)tiles_x;
+            s.cut = (int)cut;
+            s.whole = tiles - cut;
+            s.ranges = (int)ranges;
+        };
+        if (!cut) {
+            take(0, before + 24.0 * tx);
+            continue;
+        }
+        // the last, partial round: a tile a pair, as many equal parts of every tile as there are pairs for, or equal ranges
+        // for all pairs.  The second kernel, and its parts' way through L2, cost some microseconds.
+        take(cut, before + s.blocks * stage + 24.0 * tx);
+        const int64_t total = cut * s.blocks, most = total / 4 < kPairs ? total / 4 : kPairs;
+        for (int64_t r = 2 * cut; r < most + cut; r += cut) {
             if (r > most) r = most;
-            if (r <= s.cut) break;
-            const double parts = r % s.cut == 0 ? (double)r : (double)(s.cut + r - 1);
-            const double cost = (double)((total + r - 1) / r) + 0.1 * parts * tx / 256 + 4.0;
-            if (cost < best) {
-                best = cost;
-                s.ranges = (int)r;
-            }
+            if (r <= cut) break;
+            const double parts = r % cut == 0 ? (double)r : (double)(cut + r - 1);
+            take(r, before + (double)((total + r - 1) / r) * stage + 24.0 * tx + 5000.0 + 0.25 * parts * tx);
             if (r == most) break;
         }
     }
-    s.units = s.whole ? units : s.ranges;
+    s.units = s.whole ? kPairs : s.ranges;
     const int64_t total = (int64_t)s.cut * s.blocks;
     for (int p = 0; p <= s.ranges; ++p) s.start[p] = s.ranges ? total * p / s.ranges : 0;
     for (int p = 0; p < s.ranges; ++p) s.tile[p] = (uint8_t)(s.start[p] / s.blocks);
@@ -112,6 +139,12 @@ Schedule schedule(int64_t features, int64_t tokens, int64_t k)
         s.to[c] = (uint8_t)p;
     }
     return s;
+}
+template <class S>
+Schedule schedule(int64_t features, int64_t tokens, int64_t k)
+{
+    if constexpr (S::kGroup == 1) return schedule_single<S>(features, tokens, k);
+    else return schedule_pairs(features, tokens, k);
 }
 // Partial tiles that the workspace holds: range p's part of tile c at c + p.
 int64_t part_tiles(const Schedule &s) { return s.ranges > s.cut ? s.cut + s.ranges - 1 : 0; }
@@ -128,11 +161,13 @@ struct Params {
     Schedule s;
     Exps ew, ex;
     uint32_t idesc;     // without the exponents' byte numbers
+    int run;            // kRunWide or kRun16
     int64_t tokens, features;
     const float *bias;
     void *y;
     int64_t sy;
     int accumulate;
+    bool quads;         // four adjacent features of y start on 8 bytes
     float *parts;
     long long limit;    // cycles after which a wait gives up
 };
@@ -264,20 +299,22 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
             : "memory");
 }
 
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
+// 16 columns, to be had after tmem_wait16.
+__device__ __forceinline__ void tmem_begin16(uint32_t addr, uint32_t (&r)[16])
 {
-    uint32_t r[32];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 struct Shared {
@@ -307,49 +344,108 @@ struct Out {
     T *y;
     float *part;      // the workspace, or (single CTAs) shared memory; nullptr: y
     int64_t sy;
-    int n;            // tokens that exist
+    int n;            // tokens that exist, of `count`
     float bias;
-    bool add, ok;
+    bool in, add, ok;     // in: the lane's feature exists
+    bool fast;            // the warp may store by put16_whole
+    uint32_t mine, other, first, second;  // byte selectors of the exchange
 
     __device__ __forceinline__ Out(const Params &p, const Item &it, float *shared, int x0, int count, int row, bool ok_) : sy(p.sy), ok(ok_)
     {
-        const int64_t feature = (int64_t)it.tw * S::kFeatures + row, token = (int64_t)it.tx * S::kTokens + x0;
+        const int64_t feature = (int64_t)it.tw * S::kFeatures + row, token = (int64_t)it.tx * p.s.tokens + x0;
         const int64_t left = p.tokens - token;
-        const bool in = feature < p.features;
+        in = feature < p.features;
         part = it.part < 0 ? nullptr : (S::kGroup == 1 ? shared : p.parts + (int64_t)it.part * S::kTokens * S::kFeatures) + x0 * S::kFeatures + row;
-        n = in ? (int)(left < 0 ? 0 : left < count ? left : count) : 0;
+        n = (int)(left < 0 ? 0 : left < count ? left : count);
         y = static_cast<T *>(p.y) + token * sy + feature;
         bias = p.bias && in && !part ? p.bias[feature] : 0.0f;
         add = p.accumulate != 0;
+        // four lanes that share stores exist together, or not at all
+        const bool four = p.features % 4 == 0 || __all_sync(kFull, in);
+        fast = ok && (sizeof(T) == 4 || part || (p.quads && four));
+        const bool odd = threadIdx.x & 1;
+        mine = odd ? 0x7632 : 0x5410;
+        other = odd ? 0x5410 : 0x7632;
+        first = odd ? 0x1054 : 0x5410;
+        second = odd ? 0x3276 : 0x7632;
     }
-    // Tokens c .. c + 15; a wait that gave up (ok false) leaves NaN.
-    __device__ __forceinline__ void put16(float (&v)[16], int c) const
+    // Tokens c .. c + 15, some of which may not exist; a wait that gave up (ok false) leaves NaN.
+    __device__ __forceinline__ void put16(const uint32_t (&r)[16], int c) const
     {
-        if (!ok) {
+        const int m = in ? n - c : 0;
+        T *o = y + c * sy;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7fffffffu);
+        for (int j = 0; j < 16; ++j, o += sy) {
+            if (j >= m) continue;
+            float v = ok ? __uint_as_float(r[j]) : __uint_as_float(0x7fffffffu);
+            if (part) {
+                part[(c + j) * S::kFeatures] = v;
+                continue;
+            }
+            v += bias;
+            if constexpr (sizeof(T) == 4) {
+                if (add) v += *o;
+            }
+            *o = rounded<T>(v);
         }
+    }
+    // Whichever of the two it takes.
+    __device__ __forceinline__ void put(const uint32_t (&r)[16], int c) const
+    {
+        if (fast && c + 16 <= n) put16_whole(r, c);
+        else if (c < n) put16(r, c);
+    }
+    // The same where all 16 tokens exist, and where `fast`.  16-bit values go four features of a token at a time: of four tokens the lanes 4 q .. 4 q + 3
+    // exchange theirs, and lane 4 q + i stores token i's.
+    __device__ __forceinline__ void put16_whole(const uint32_t (&r)[16], int c) const
+    {
         if (part) {
+            float *o = part + c * S::kFeatures;
+            if (in) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (c + j < n) part[(c + j) * S::kFeatures] = v[j];
+                for (int j = 0; j < 16; ++j) o[j * S::kFeatures] = __uint_as_float(r[j]);
+            }
             return;
         }
-        T *const o = y + c * sy;
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += bias;
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) + bias;
         if constexpr (sizeof(T) == 4) {
+            T *o = y + c * sy;
+            if (!in) return;
             if (add) {
                 float old[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) old[j] = c + j < n ? o[j * sy] : 0.0f;
+                for (int j = 0; j < 16; ++j) old[j] = o[j * sy];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] += old[j];
             }
-        }
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c + j < n) o[j * sy] = rounded<T>(v[j]);
+            for (int j = 0; j < 16; ++j, o += sy) *o = v[j];
+        } else {
+            const int i = threadIdx.x & 3;
+            T *to = y + (c + i) * sy - i;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4, to += 4 * sy) {
+                const uint32_t ab = pair(v[j], v[j + 1]), cd = pair(v[j + 2], v[j + 3]);
+                // even lanes keep tokens 0 and 2, odd ones 1 and 3, of two features
+                const uint32_t a = __byte_perm(ab, cd, mine), b = __shfl_xor_sync(kFull, __byte_perm(ab, cd, other), 1);
+                const uint32_t x = __byte_perm(a, b, first), z = __byte_perm(a, b, second);
+                // lanes 0 and 1 keep the first of those, lanes 2 and 3 the second, of four features
+                const uint32_t got = __shfl_xor_sync(kFull, (i & 2) ? x : z, 2);
+                if (in) *reinterpret_cast<uint2 *>(to) = make_uint2((i & 2) ? got : x, (i & 2) ? z : got);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint32_t pair(float a, float b)
+    {
+        if constexpr (__is_same(T, __half)) {
+            const __half2 h = __floats2half2_rn(a, b);
+            return *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            return *reinterpret_cast<const uint32_t *>(&h);
+        }
     }
 };
 
@@ -406,7 +502,13 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank(), leader = GROUP == 2 ? 0u : rank;  // whose barriers the MMAs go by
     const int pair_rank = GROUP == 2 ? (int)rank : 0;
+    const int second = min(p.s.tokens, S::kSecond);
+    const bool shares = p.s.tokens > S::kSecond;
 
+    if (threadIdx.x == 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.w) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.x) : "memory");
+    }
     if (threadIdx.x == 0) {
         sh.failed = 0;
         for (int i = 0; i < S::kStages; ++i) {
@@ -436,6 +538,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     if constexpr (GROUP == 2) cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = sh.tmem;
+    cudaGridDependencySynchronize();  // up to here it runs as the kernel before it on the stream drains
 
     if (warp < 4) {
         if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -443,18 +546,20 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             // TMA: 128 features and this CTA's tokens of every stage.  The leader's barrier expects both CTAs' bytes; the
             // other's may arrive first, but not in an earlier phase: that one had ended when its stage was free again.
             const uint32_t full = in_cta(smem_u32(&sh.full[0]), leader);
+            const int xrows = GROUP == 2 ? p.s.tokens / 2 : TN;
+            const uint32_t bytes = GROUP * (S::kWBytes + xrows * 128);
             Ring<S::kStages> r;
             bool ok = true;
             Item it;
             for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
-                const int w0 = it.tw * S::kFeatures + pair_rank * 128, x0 = it.tx * S::kTokens + pair_rank * S::kXRows;
+                const int w0 = it.tw * S::kFeatures + pair_rank * 128, x0 = it.tx * p.s.tokens + pair_rank * xrows;
                 for (int b = it.first; b < it.last; ++b) {
                     if (r.turn > 0 && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
                         ok = false;
                         break;
                     }
                     const uint32_t base = stages + r.st * S::kStageBytes, bar = full + r.st * 8;
-                    if (rank == leader) mbar_arrive_expect_tx(&sh.full[r.st], GROUP * S::kStageBytes);
+                    if (rank == leader) mbar_arrive_expect_tx(&sh.full[r.st], bytes);
                     load_box<GROUP>(base, &p.w, b * 128, w0, bar);
                     load_box<GROUP>(base + S::kWBytes, &p.x, b * 128, x0, bar);
                     r.next();
@@ -485,12 +590,12 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
                 for (int b = it.first; ok && b < it.last; ++runs) {
                     const int buf = (int)(runs & 1);
                     if (runs >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.acc_empty[buf]), ((uint32_t)(runs >> 1) + 1u) & 1u, p.limit);
-                    if (S::kShared && ok && runs >= 1)
+                    if (shares && ok && runs >= 1)
                         ok = mbar_wait_cycles_warp(smem_u32(&sh.edge[buf ^ 1]), (uint32_t)((runs - 1) >> 1) & 1u, p.limit);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t d = tmem + buf * S::kSecond;
-                    const int end = it.last - b < kRun ? it.last : b + kRun;
+                    const uint32_t d = tmem + buf * second;
+                    const int end = it.last - b < p.run ? it.last : b + p.run;
                     for (bool add = false; b < end; ++b, add = true) {
                         const int eb = (int)(groups & 1);
                         if (b == it.first || (b & 3) == 0) {
@@ -529,124 +634,148 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
         if constexpr (GROUP == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         // Epilogue: TMEM lane = feature, column = token; of a pair four warps take the lower half of the tokens, four the
         // upper.
-        // Columns that the two accumulators share (the first one's last, the second one's first) are read before all
-        // others, kHeld of them, so that the other accumulator's MMAs can go on.
-        constexpr int kHalf = GROUP == 2 ? TN / 2 : TN, kHeld = S::kShared ? 32 : 0, kRest = kHalf - kHeld;
-        static_assert(S::kShared <= kHeld && (kHeld == 0 || kHeld == 32) && kRest % 16 == 0, "columns");
+        constexpr int kLower = TN > 128 ? 128 : TN, kFirst = GROUP == 2 && !SUMS ? kHeld : 0;
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
         const bool upper = warp >= 12;
-        const int held0 = upper ? kRest : 0, rest0 = upper ? 0 : kHeld;
+        const int x0 = upper ? kLower : 0;
+        const int count = GROUP == 2 ? min(max(p.s.tokens - x0, 0), kLower) : TN;  // a multiple of 32
         const uint32_t acc_empty = in_cta(smem_u32(&sh.acc_empty[0]), leader), edge = in_cta(smem_u32(&sh.edge[0]), leader);
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (upper ? kHalf : 0);
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + x0;
         const int row = pair_rank * 128 + quarter * 32 + lane;
+        // The columns are taken in this order: the first kFirst are those that the other accumulator may share, the first
+        // accumulator's last and the second one's first.  (Tiles of several runs are narrower and share none.)
+        const int turn = !SUMS && shares && upper ? kLower - kFirst : 0;
+        auto col = [&](int c) { return (c + turn) & (kLower - 1); };
+        auto release = [&](int buf) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_cluster(acc_empty + buf * 8);
+        };
         int64_t runs = 0;
         bool ok = true;
         Item it;
         for (int64_t i = 0; item_of<GROUP>(p.s, i, rank, it); ++i) {
-            float acc[SUMS ? kHalf : 1];
+            float acc[SUMS ? kLower : 1];
             if constexpr (SUMS) {
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) acc[j] = 0.0f;
+                for (int j = 0; j < kLower; ++j) acc[j] = 0.0f;
             }
-            for (int b = it.first; b < it.last; b += kRun, ++runs) {
-                const int buf = (int)(runs & 1);
+            uint32_t held[2][16], cols = 0;
+            int buf = 0;
+            // A tile of one run, or (SUMS) the sums of several; the last one's columns of TMEM are kept until all is stored
+            for (int b = it.first; b < it.last; b += p.run, ++runs) {
+                if (SUMS && b > it.first) release(buf);
+                buf = (int)(runs & 1);
                 ok = ok && mbar_wait_cycles_warp(smem_u32(&sh.acc_full[buf]), (uint32_t)(runs >> 1) & 1u, p.limit);
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t cols = lanes + buf * S::kSecond;
-                const bool end = b + kRun >= it.last;
-                float held[SUMS ? 1 : 32];
-                if constexpr (kHeld != 0) {
-                    if constexpr (SUMS) {
-#pragma unroll
-                        for (int c = 0; c < kHeld; c += 16) {
-                            float v[16];
-                            tmem_load16(cols + held0 + c, v);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
-                        }
-                    } else {
-                        tmem_load32(cols + held0, held);
-                    }
-                    if (upper == (buf == 0)) {
-                        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(edge + buf * 8);
-                    }
-                }
+                cols = lanes + buf * second;
                 if constexpr (SUMS) {
 #pragma unroll
-                    for (int c = 0; c < kRest; c += 16) {
-                        float v[16];
-                        tmem_load16(cols + rest0 + c, v);
+                    for (int c = 0; c < kLower; c += 16) {
+                        if (c >= count) break;
+                        tmem_begin16(cols + c, held[0]);
+                        tmem_wait16(held[0]);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[kHeld + c + j] += v[j];
-                    }
-                    if (end) {
-                        // The tile's sums go back to TMEM, and from there to memory 16 at a time, in a loop that stays
-                        // in the instruction cache.
-#pragma unroll
-                        for (int c = 0; c < kRest; c += 16) tmem_store16(cols + rest0 + c, acc + kHeld + c);
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(held[0][j]);
                     }
                 }
-                if (end) {
-                    const int x0 = upper ? kHalf : 0;
-                    if (GROUP == 1 && !ok) sh.failed = 1;
-                    const Out<T, S> out(p, it, reinterpret_cast<float *>(raw_smem), x0, kHalf, row, ok);
-#pragma unroll
-                    for (int c = 0; c < kHeld; c += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = SUMS ? acc[SUMS ? c + j : 0] : held[SUMS ? 0 : c + j];
-                        out.put16(v, held0 + c);
-                    }
-#pragma unroll 1
-                    for (int c = rest0; c < rest0 + kRest; c += 16) {
-                        float v[16];
-                        tmem_load16(cols + c, v);
-                        out.put16(v, c);
-                    }
-                }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) arrive_cluster(acc_empty + buf * 8);
             }
+            if constexpr (SUMS) {
+                // The tile's sums go back to TMEM, and from there to memory in a loop that stays in the instruction cache.
+#pragma unroll
+                for (int c = 0; c < kLower; c += 16) {
+                    if (c >= count) break;
+                    tmem_store16(cols + c, acc + c);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else if constexpr (kFirst != 0) {
+                if (count > 0) {
+                    tmem_begin16(cols + col(0), held[0]);
+                    tmem_begin16(cols + col(16), held[1]);
+                    tmem_wait16(held[0]);
+                    tmem_wait16(held[1]);
+                }
+                if (shares && upper == (buf == 0)) {
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(edge + buf * 8);
+                }
+            }
+            if (GROUP == 1 && !ok) sh.failed = 1;
+            if (count > 0) {
+                const Out<T, S> out(p, it, reinterpret_cast<float *>(raw_smem), x0, count, row, ok);
+                if (kFirst == 0) {
+                    tmem_begin16(cols, held[0]);
+                    tmem_wait16(held[0]);
+                }
+                // the next 16 columns on their way
+#pragma unroll 1
+                for (int c = 0; c < count; c += 32) {
+                    if (kFirst == 0 || c > 0) tmem_begin16(cols + col(c + 16), held[1]);
+                    out.put(held[0], col(c));
+                    if (kFirst == 0 || c > 0) tmem_wait16(held[1]);
+                    const bool more = c + 32 < count;
+                    if (more) tmem_begin16(cols + col(c + 32), held[0]);
+                    out.put(held[1], col(c + 16));
+                    if (more) tmem_wait16(held[0]);
+                }
+            }
+            release(buf);
         }
     } else {
         if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExp));
-        // Exponents: each warp its quarter of the lanes, all four the same words, fetched one group ahead.
-        constexpr int kX = S::kExpCols - 4;
+        // Exponents: each warp its quarter of the lanes, all four the same words.  A tile's first words come from memory
+        // (the next ones from the same sectors): they are fetched two groups ahead, across tiles.
+        constexpr int kN = S::kExpCols;
         const uint32_t to = in_cta(smem_u32(&sh.exp_full[0]), leader);
         const uint32_t lanes = tmem + S::kExps + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint8_t *rows[kN];
+        Item it;
+        int64_t next = 0;
+        int g = 0, end = 0;  // groups of the item that is fetched
+        auto fetch = [&](uint32_t (&v)[kN]) {
+            if (g == end) {
+                if (!item_of<GROUP>(p.s, next, rank, it)) return false;
+                ++next;
+                g = it.first >> 2;
+                end = ((it.last - 1) >> 2) + 1;
+#pragma unroll
+                for (int c = 0; c < kN; ++c) {
+                    const Exps &e = c < 4 ? p.ew : p.ex;
+                    const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + pair_rank * 128 + c * 32 + lane
+                                              : (int64_t)it.tx * p.s.tokens + (c - 4) * 32 + lane;
+                    const bool in = row < e.rows && (c < 4 || (c - 4) * 32 + lane < p.s.tokens);
+                    rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kN; ++c) v[c] = rows[c] ? __ldg(reinterpret_cast<const uint32_t *>(rows[c]) + g) : 0u;
+            ++g;
+            return true;
+        };
         int64_t groups = 0;
         bool ok = true;
-        Item it;
-        for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
-            const uint8_t *rows[4 + kX];
+        uint32_t v[3][kN];
+        bool has[3];
+        has[0] = fetch(v[0]);
+        has[1] = has[0] && fetch(v[1]);
+        while (ok && has[0]) {
 #pragma unroll
-            for (int c = 0; c < 4 + kX; ++c) {
-                const Exps &e = c < 4 ? p.ew : p.ex;
-                const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + pair_rank * 128 + c * 32 + lane
-                                          : (int64_t)it.tx * S::kTokens + (c - 4) * 32 + lane;
-                const bool in = row < e.rows && (c < 4 || (c - 4) * 32 < TN);
-                rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
-            }
-            for (int g = it.first >> 2; g <= (it.last - 1) >> 2; ++g, ++groups) {
-                uint32_t v[4 + kX];
-#pragma unroll
-                for (int c = 0; c < 4 + kX; ++c) v[c] = rows[c] ? __ldg(reinterpret_cast<const uint32_t *>(rows[c]) + g) : 0u;
+            for (int u = 0; u < 3; ++u) {
+                if (!ok || !has[u]) break;
+                has[(u + 2) % 3] = has[(u + 1) % 3] && fetch(v[(u + 2) % 3]);
                 const int eb = (int)(groups & 1);
-                if (groups >= 2 && !mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((uint32_t)(groups >> 1) + 1u) & 1u, p.limit)) {
-                    ok = false;
-                    break;
-                }
+                if (groups >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((uint32_t)(groups >> 1) + 1u) & 1u, p.limit);
+                if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-                for (int c = 0; c < 4 + kX; c += 4) tmem_store4(lanes + eb * S::kExpCols + c, v + c);
+                for (int c = 0; c < kN; c += 4) tmem_store4(lanes + eb * kN + c, v[u] + c);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_cluster(to + eb * 8);
+                ++groups;
+                has[u] = false;
             }
         }
         // the MMAs' last signals arrive before the CTA may leave
@@ -664,8 +793,8 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     }
 }
 
-// The cut tiles' sums, range by range in order, to y.  A block takes 4 tokens of 256 features (8 of 128), a thread 4
-// adjacent features of one.
+// The cut tiles' sums, range by range in order, to y.  A block takes 4 tokens of 256 features, a thread 4 adjacent
+// features of one.
 template <typename T, class S>
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
 {
@@ -677,8 +806,8 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
     if (lo == hi) return;  // one range has the whole tile, and has stored it
     Item it;
     tile_place(p.s, p.s.whole + c, it);
-    const int64_t feature = (int64_t)it.tw * S::kFeatures + w, token = (int64_t)it.tx * S::kTokens + x;
-    if (feature >= p.features || token >= p.tokens) return;
+    const int64_t feature = (int64_t)it.tw * S::kFeatures + w, token = (int64_t)it.tx * p.s.tokens + x;
+    if (feature >= p.features || x >= p.s.tokens || token >= p.tokens) return;
     const int n = (int)min((int64_t)4, p.features - feature);
     const float *s = p.parts + ((int64_t)(c + lo) * S::kTokens + x) * S::kFeatures + w;
     float v[4] = {};
@@ -707,9 +836,9 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
         }
 }
 
-// Which shape: tiles of 256 x 256 by CTA pairs, or, for up to 128 tokens, 128 features by single CTAs.
-enum Kind { kPair256, kOne128, kOne64, kOne32 };
-Kind kind_of(int64_t tokens) { return tokens > 128 ? kPair256 : tokens > 64 ? kOne128 : tokens > 32 ? kOne64 : kOne32; }
+// Which shape: tiles of 256 features by CTA pairs, or, for up to 128 tokens, 128 features by single CTAs.
+enum Kind { kByPairs, kOne128, kOne64, kOne32 };
+Kind kind_of(int64_t tokens) { return tokens > 128 ? kByPairs : tokens > 64 ? kOne128 : tokens > 32 ? kOne64 : kOne32; }
 
 template <class S>
 size_t workspace_of(int64_t m, int64_t n, int64_t k)
@@ -749,20 +878,21 @@ cudaError_t launch_kernels(const Params &p, cudaStream_t stream)
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)(S::kGroup == 2 ? 2 : p.s.splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)(S::kGroup == 2 ? 2 : p.s.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (S::kGroup == 1 || e != cudaSuccess || !part_tiles(p.s)) return e;
     cfg.gridDim = dim3((unsigned)(p.s.cut * (S::kTokens / (1024 / S::kFeatures))));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_join<T, S>, p);
 }
 
@@ -774,20 +904,22 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
     p.s = schedule<S>(g.n, g.m, g.k);
     p.ew = exps_of(g.b, g.tile_b, g.n, lw);
     p.ex = exps_of(g.a, g.tile_a, g.m, lx);
-    p.idesc = instr_desc(g.format_b, g.format_a, S::kFeatures, S::kTokens);
+    p.idesc = instr_desc(g.format_b, g.format_a, S::kFeatures, p.s.tokens);
     p.tokens = g.m;
     p.features = g.n;
     p.bias = g.bias;
     p.y = g.y;
     p.sy = g.m > 1 ? g.y_stride : 0;
     p.accumulate = g.accumulate;
+    p.quads = reinterpret_cast<uintptr_t>(g.y) % 8 == 0 && (g.m == 1 || g.y_stride % 4 == 0);
     p.parts = reinterpret_cast<float *>(g.ws);
     // two seconds at 1.97 GHz, three at the power cap's 1.39 GHz; the longest wait, for a tile, is some microseconds a
     // thousand columns
     p.limit = 4000000000ll;
-    if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) || !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kXRows))
+    if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) || !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kGroup == 2 ? p.s.tokens / 2 : S::kTokens))
         return cudaErrorInvalidValue;
-    const bool sums = p.s.blocks > kRun;
+    p.run = run_of(g.dtype);
+    const bool sums = p.s.blocks > p.run;
     if (g.dtype == GQ_FLOAT32) return sums ? launch_kernels<float, S, true>(p, stream) : launch_kernels<float, S, false>(p, stream);
     if (g.dtype == GQ_BFLOAT16)
         return sums ? launch_kernels<__nv_bfloat16, S, true>(p, stream) : launch_kernels<__nv_bfloat16, S, false>(p, stream);
@@ -799,13 +931,13 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
 size_t fp8_matmul_workspace(int64_t m, int64_t n, int64_t k)
 {
     if (m == 0) return 0;
-    return kind_of(m) == kPair256 ? workspace_of<Shape<2, 256>>(m, n, k) : 0;
+    return kind_of(m) == kByPairs ? workspace_of<Pair>(m, n, k) : 0;
 }
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs &g, cudaStream_t stream)
 {
     switch (kind_of(g.m)) {
-    case kPair256: return launch_shape<Shape<2, 256>>(g, stream);
+    case kByPairs: return launch_shape<Pair>(g, stream);
     case kOne128: return launch_shape<Shape<1, 128>>(g, stream);
     case kOne64: return launch_shape<Shape<1, 64>>(g, stream);
     default: return launch_shape<Shape<1, 32>>(g, stream);

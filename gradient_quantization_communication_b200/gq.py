@@ -5,6 +5,7 @@ torch's current CUDA stream.  There is no fallback: if ``libgq.so`` is missing t
 library fails with an error that says how to build it.
 """
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -511,6 +512,7 @@ def _format(fmt):
     return f
 
 
+@functools.lru_cache(maxsize=4096)
 def _fp8_bytes(tile, rows, cols):
     return ((rows * ((cols + 127) // 128 * 128) + 15) // 16 * 16
             + (((rows + 127) // 128 if tile else rows) * ((cols + 511) // 512 * 4) + 15) // 16 * 16)
@@ -521,7 +523,7 @@ def _packed(t, what, tile, rows, cols):
     if t is None:
         return None
     need = _fp8_bytes(tile, rows, cols)
-    if t.element_size() != 1 or t.dim() != 1 or t.shape[0] < need or not t.is_contiguous():
+    if t.numel() < need or t.element_size() != 1 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError("%s: a contiguous uint8 vector of at least %d bytes expected, got %s of shape %s"
                          % (what, need, t.dtype, tuple(t.shape)))
     return t.data_ptr()
@@ -553,6 +555,7 @@ def gq_fp8_unpack(packed, x, fmt="e4m3", tile=False, stream=None):
             _packed(packed, "packed", tile, rows, cols), px, sx)
 
 
+@functools.lru_cache(maxsize=4096)
 def _fp8_matmul_bytes(m, n, k):
     b = ctypes.c_size_t()
     _check(lib().gq_fp8_matmul_workspace(m, n, k, ctypes.byref(b)), "gq_fp8_matmul_workspace")
@@ -572,7 +575,9 @@ def gq_fp8_matmul(a, b, k, y, bias=None, fmt=("e4m3", "e4m3"), tile=(False, Fals
     m, n = y.shape
     ta, tb = int(bool(tile[0])), int(bool(tile[1]))
     if workspace is None:
-        workspace = _workspace(_fp8_matmul_bytes(m, n, k), y.device, stream)
+        need = _fp8_matmul_bytes(m, n, k)
+        if need:
+            workspace = _workspace(need, y.device, stream)
     pws, nws = _space(workspace, "gq_fp8_matmul")
     _launch(lib().gq_fp8_matmul, "gq_fp8_matmul", stream, (y, a, b, bias, workspace), _dtype(y, "y"), m, n, k,
             _format(fmt[0]), ta, _packed(a, "a", ta, m, k), _format(fmt[1]), tb, _packed(b, "b", tb, n, k),

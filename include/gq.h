@@ -511,8 +511,8 @@ GQ_API gq_status_t gq_fp8_unpack(int dtype, int format, int tile, int64_t rows, 
  *   workspace  device, at least gq_fp8_matmul_workspace bytes, 16-byte aligned; NULL if that is 0.  Its
  *              contents do not outlive the call.
  * m = 0 is a no-op; 1 <= n < 2^31, 1 <= k <= GQ_ACT_MAX_COLS.  Products are exact; sums are binary32, where
- * the tensor cores cut off instead of rounding over runs of up to 4096 columns, and sums below 2^-126 may
- * read as 0.  A row of y with a NaN block in its operands is NaN where the formula is.
+ * the tensor cores cut off instead of rounding over runs of up to 4096 columns (16384 where y has 16 bits,
+ * whose own rounding is far coarser), and sums below 2^-126 may read as 0.  A row of y with a NaN block in its operands is NaN where the formula is.
  */
 GQ_API gq_status_t gq_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes);
 GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int format_a, int tile_a, const void *a,

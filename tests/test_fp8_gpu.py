@@ -150,11 +150,12 @@ def operand(rows, k, fmt, tile, seed, spread=1.0):
     return buf, O.decode(codes[:rows * cp].reshape(rows, cp), codes[off:off + er * ep].reshape(er, ep), fmt, tile, k).cuda()
 
 
-def steps(k):
+def steps(k, dtype=torch.float32):
     """Half-steps of binary32 that a sum over k columns may be off by, relative to the sum of absolute products: two
-    steps for every 32 products while the tensor cores cut off (runs of 4096 at most), three roundings a run, and a few
-    for joining parts, the bias and adding."""
-    return 2 * (min(k, 4096) / 32 * 2 + 3 * (k / 4096 + 1) + 16)
+    steps for every 32 products while the tensor cores cut off (runs of 4096 columns at most, 16384 for a result of 16
+    bits), three roundings a run, and a few for joining parts, the bias and adding."""
+    run = 4096 if dtype == torch.float32 else 16384
+    return 2 * (min(k, run) / 32 * 2 + 3 * (k / run + 1) + 16)
 
 
 def check_product(y, da, db, k, bias=None, before=None):
@@ -166,7 +167,7 @@ def check_product(y, da, db, k, bias=None, before=None):
     if before is not None:
         want = want + before.double()
         size = size + before.double().abs()
-    tol = steps(k) * 2.0 ** -24 * size + O.HALF_STEP[y.dtype] * want.abs() * 1.01
+    tol = steps(k, y.dtype) * 2.0 ** -24 * size + O.HALF_STEP[y.dtype] * want.abs() * 1.01
     if y.dtype == torch.float16:
         tol = tol + 2.0 ** -25
     err = (y.double() - want).abs()
@@ -175,7 +176,7 @@ def check_product(y, da, db, k, bias=None, before=None):
 
 PRODUCTS = [(1, 1, 1), (1, 128, 128), (2, 7, 5), (16, 130, 500), (17, 257, 513), (33, 64, 1030), (64, 300, 4096),
             (65, 129, 640), (128, 256, 128), (129, 255, 384), (200, 1000, 1000), (300, 77, 2050), (515, 515, 515),
-            (1, 4096, 4096), (8, 1000, 8200), (1100, 900, 260)]
+            (1, 4096, 4096), (8, 1000, 8200), (1100, 900, 260), (300, 300, 8200), (70, 40, 20000), (260, 260, 20000)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
