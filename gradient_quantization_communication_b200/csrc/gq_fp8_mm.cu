@@ -64,7 +64,7 @@ struct Schedule {
     int tiles_w, tiles_x;
     int blocks;            // stages of a tile
     int splits;            // single CTAs: parts of each tile; nothing of the following
-    int64_t whole;         // tiles of the whole rounds
+    uint32_t whole;        // tiles of the whole rounds
     int cut, ranges;       // tiles of the last one, and the ranges that they are cut into
     int units;             // pairs launched
     int64_t start[kPairs + 1];
@@ -109,7 +109,7 @@ Schedule schedule_pairs(int64_t features, int64_t tokens, int64_t k)
             s.tokens = tx;
             s.tiles_x = (int)tiles_x;
             s.cut = (int)cut;
-            s.whole = tiles - cut;
+            s.whole = (uint32_t)(tiles - cut);
             s.ranges = (int)ranges;
         };
         if (!cut) {
@@ -179,19 +179,17 @@ struct Item {
 };
 
 // Bands of 8 feature tiles, walked along the tokens: units that run together share their operands in L2.
-__device__ __forceinline__ void tile_place(const Schedule &s, int64_t tile, Item &it)
+__device__ __forceinline__ void tile_place(const Schedule &s, uint32_t tile, Item &it)
 {
-    const int64_t band = (int64_t)8 * s.tiles_x;
-    const int64_t g = tile / band;
-    const int rest = (int)(tile - g * band);
-    const int wide = min(8, s.tiles_w - (int)g * 8);
-    it.tx = rest / wide;
-    it.tw = (int)g * 8 + rest - it.tx * wide;
+    const uint32_t band = 8u * (uint32_t)s.tiles_x, g = tile / band, rest = tile - g * band;
+    const uint32_t wide = min(8u, (uint32_t)s.tiles_w - g * 8u);
+    it.tx = (int)(rest / wide);
+    it.tw = (int)(g * 8u + rest - (uint32_t)it.tx * wide);
 }
 
 // The i-th item of a pair, or a single CTA's only one (i = 0).
 template <int GROUP>
-__device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, uint32_t rank, Item &it)
+__device__ __forceinline__ bool item_of(const Schedule &s, int i, uint32_t rank, Item &it)
 {
     if constexpr (GROUP == 1) {
         if (i != 0) return false;
@@ -203,25 +201,24 @@ __device__ __forceinline__ bool item_of(const Schedule &s, int64_t i, uint32_t r
         it.part = s.splits > 1 ? 0 : -1;
         return true;
     }
-    i = (blockIdx.x >> 1) + i * s.units;
-    int64_t tile;
-    if (i < s.whole) {
-        tile = i;
+    const uint32_t at = (blockIdx.x >> 1) + (uint32_t)i * (uint32_t)s.units;
+    uint32_t tile = at;
+    if (at < s.whole) {
         it.first = 0;
         it.last = s.blocks;
         it.part = -1;
     } else {
         // part m of unit p's range, which lies in the m-th tile that the range touches
-        const uint32_t j = (uint32_t)(i - s.whole), m = j / (uint32_t)s.units, p = j - m * (uint32_t)s.units;
+        const uint32_t j = at - s.whole, m = j / (uint32_t)s.units, p = j - m * (uint32_t)s.units;
         if (p >= (uint32_t)s.ranges) return false;
         const int64_t lo = s.start[p], hi = s.start[p + 1];
         const int c = (int)(s.tile[p] + m);
-        const int64_t at = (int64_t)c * s.blocks;
-        it.first = (int)((lo > at ? lo : at) - at);
-        it.last = (int)((hi < at + s.blocks ? hi : at + s.blocks) - at);
+        const int64_t from = (int64_t)c * s.blocks;
+        it.first = (int)((lo > from ? lo : from) - from);
+        it.last = (int)((hi < from + s.blocks ? hi : from + s.blocks) - from);
         if (it.first >= it.last) return false;
         it.part = it.first == 0 && it.last == s.blocks ? -1 : c + (int)p;
-        tile = s.whole + c;
+        tile = s.whole + (uint32_t)c;
     }
     tile_place(s, tile, it);
     return true;
@@ -338,6 +335,19 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// Two values of a 16-bit type as a word.
+template <typename T>
+__device__ __forceinline__ uint32_t pair16(float a, float b)
+{
+    if constexpr (__is_same(T, __half)) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
 // Where a lane's column of a tile goes: its feature of `count` tokens from token x0 of the tile on.
 template <typename T, class S>
 struct Out {
@@ -427,7 +437,7 @@ struct Out {
             T *to = y + (c + i) * sy - i;
 #pragma unroll
             for (int j = 0; j < 16; j += 4, to += 4 * sy) {
-                const uint32_t ab = pair(v[j], v[j + 1]), cd = pair(v[j + 2], v[j + 3]);
+                const uint32_t ab = pair16<T>(v[j], v[j + 1]), cd = pair16<T>(v[j + 2], v[j + 3]);
                 // even lanes keep tokens 0 and 2, odd ones 1 and 3, of two features
                 const uint32_t a = __byte_perm(ab, cd, mine), b = __shfl_xor_sync(kFull, __byte_perm(ab, cd, other), 1);
                 const uint32_t x = __byte_perm(a, b, first), z = __byte_perm(a, b, second);
@@ -435,16 +445,6 @@ struct Out {
                 const uint32_t got = __shfl_xor_sync(kFull, (i & 2) ? x : z, 2);
                 if (in) *reinterpret_cast<uint2 *>(to) = make_uint2((i & 2) ? got : x, (i & 2) ? z : got);
             }
-        }
-    }
-    static __device__ __forceinline__ uint32_t pair(float a, float b)
-    {
-        if constexpr (__is_same(T, __half)) {
-            const __half2 h = __floats2half2_rn(a, b);
-            return *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            return *reinterpret_cast<const uint32_t *>(&h);
         }
     }
 };
@@ -455,37 +455,52 @@ __device__ __forceinline__ uint32_t load_cluster(uint32_t addr)
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-
-// The parts of a cluster's tile, one in each CTA's shared memory, in order to y: every CTA takes some of the tokens.
-template <typename T, class S>
-__device__ __forceinline__ void join_cluster(const Params &p, Shared &sh, float *shared, uint32_t rank)
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr)
 {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// The parts of a cluster's tile, one in each CTA's shared memory, in order to y: a warp takes a token's 128 features, a
+// lane four of them, and all parts' are on their way at once (another CTA's shared memory answers after some 700 cycles).
+template <typename T, class S>
+__device__ __forceinline__ void join_cluster(const Params &p, const Item &it, Shared &sh, const float *shared, uint32_t rank)
+{
+    const int splits = p.s.splits, lane = threadIdx.x & 31;
+    const int64_t feature = (int64_t)it.tw * S::kFeatures + lane * 4, token = (int64_t)it.tx * S::kTokens;
+    const int n = (int)min((int64_t)S::kTokens, p.tokens - token), some = (int)max((int64_t)0, min((int64_t)4, p.features - feature));
+    float bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = p.bias && j < some ? p.bias[feature + j] : 0.0f;
     cluster_sync();
-    Item it;
-    item_of<1>(p.s, 0, rank, it);
-    const int splits = p.s.splits, f = (int)(threadIdx.x & 127);
-    const int64_t feature = (int64_t)it.tw * S::kFeatures + f, token = (int64_t)it.tx * S::kTokens;
-    const int n = (int)min((int64_t)S::kTokens, p.tokens - token);
-    uint32_t failed = 0;
-    for (int r = 0; r < splits; ++r) failed |= load_cluster(in_cta(smem_u32(&sh.failed), (uint32_t)r));
-    if (feature < p.features) {
-        const float bias = p.bias ? p.bias[feature] : 0.0f;
-        T *const y = static_cast<T *>(p.y) + token * p.sy + feature;
-        const uint32_t from = smem_u32(shared + f);
-        for (int x = (int)rank + splits * (int)(threadIdx.x >> 7); x < n; x += splits * (S::kThreads / 128)) {
-            float part[kMaxSplits];
+    const uint32_t from = smem_u32(shared + lane * 4);
+    const bool failed = __any_sync(kFull, lane < splits && load_cluster(in_cta(smem_u32(&sh.failed), (uint32_t)lane % splits)) != 0);
+    for (int x = (int)rank + splits * (int)(threadIdx.x >> 5); x < n; x += splits * (S::kThreads / 32)) {
+        float4 part[kMaxSplits];
 #pragma unroll
-            for (int r = 0; r < kMaxSplits; ++r)
-                part[r] = r < splits ? __uint_as_float(load_cluster(in_cta(from + x * S::kFeatures * 4, (uint32_t)r))) : 0.0f;
-            float v = part[0];
+        for (int r = 0; r < kMaxSplits; ++r)
+            if (r < splits) part[r] = load_cluster4(in_cta(from + x * S::kFeatures * 4, (uint32_t)r));
+        float4 sum = part[0];
 #pragma unroll
-            for (int r = 1; r < kMaxSplits; ++r)
-                if (r < splits) v += part[r];
-            v += bias;
-            if constexpr (sizeof(T) == 4) {
-                if (p.accumulate) v += y[x * p.sy];
+        for (int r = 1; r < kMaxSplits; ++r)
+            if (r < splits) sum = make_float4(sum.x + part[r].x, sum.y + part[r].y, sum.z + part[r].z, sum.w + part[r].w);
+        float v[4] = {sum.x + bias[0], sum.y + bias[1], sum.z + bias[2], sum.w + bias[3]};
+        T *const y = static_cast<T *>(p.y) + (token + x) * p.sy + feature;
+        if (failed) v[0] = v[1] = v[2] = v[3] = __uint_as_float(0x7fffffffu);
+        if constexpr (sizeof(T) == 2) {
+            if (p.quads && some == 4) {
+                *reinterpret_cast<uint2 *>(y) = make_uint2(pair16<T>(v[0], v[1]), pair16<T>(v[2], v[3]));
+                continue;
             }
-            y[x * p.sy] = rounded<T>(failed ? __uint_as_float(0x7fffffffu) : v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= some) continue;
+            if constexpr (sizeof(T) == 4) {
+                if (p.accumulate) v[j] += y[j];
+            }
+            y[j] = rounded<T>(v[j]);
         }
     }
     cluster_sync();  // until all have read
@@ -551,7 +566,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             Ring<S::kStages> r;
             bool ok = true;
             Item it;
-            for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
+            for (int i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
                 const int w0 = it.tw * S::kFeatures + pair_rank * 128, x0 = it.tx * p.s.tokens + pair_rank * xrows;
                 for (int b = it.first; b < it.last; ++b) {
                     if (r.turn > 0 && !mbar_wait_cycles(smem_u32(&sh.empty[r.st]), r.parity_before(), p.limit)) {
@@ -582,10 +597,10 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             // issues
             const bool one = elect_one();
             Ring<S::kStages> r;
-            int64_t runs = 0, groups = 0;
+            uint32_t runs = 0, groups = 0;
             bool ok = true;
             Item it;
-            for (int64_t i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
+            for (int i = 0; ok && item_of<GROUP>(p.s, i, rank, it); ++i) {
                 uint32_t ew = 0;
                 for (int b = it.first; ok && b < it.last; ++runs) {
                     const int buf = (int)(runs & 1);
@@ -651,10 +666,10 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             __syncwarp();
             if (lane == 0) arrive_cluster(acc_empty + buf * 8);
         };
-        int64_t runs = 0;
+        uint32_t runs = 0;
         bool ok = true;
         Item it;
-        for (int64_t i = 0; item_of<GROUP>(p.s, i, rank, it); ++i) {
+        for (int i = 0; item_of<GROUP>(p.s, i, rank, it); ++i) {
             float acc[SUMS ? kLower : 1];
             if constexpr (SUMS) {
 #pragma unroll
@@ -731,7 +746,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
         const uint32_t lanes = tmem + S::kExps + ((uint32_t)((warp & 3) * 32) << 16);
         const uint8_t *rows[kN];
         Item it;
-        int64_t next = 0;
+        int next = 0;
         int g = 0, end = 0;  // groups of the item that is fetched
         auto fetch = [&](uint32_t (&v)[kN]) {
             if (g == end) {
@@ -753,17 +768,17 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             ++g;
             return true;
         };
-        int64_t groups = 0;
+        uint32_t groups = 0;
         bool ok = true;
         uint32_t v[3][kN];
-        bool has[3];
-        has[0] = fetch(v[0]);
-        has[1] = has[0] && fetch(v[1]);
-        while (ok && has[0]) {
+        bool full[3];
+        full[0] = fetch(v[0]);
+        full[1] = full[0] && fetch(v[1]);
+        while (ok && full[0]) {
 #pragma unroll
             for (int u = 0; u < 3; ++u) {
-                if (!ok || !has[u]) break;
-                has[(u + 2) % 3] = has[(u + 1) % 3] && fetch(v[(u + 2) % 3]);
+                if (!ok || !full[u]) break;
+                full[(u + 2) % 3] = full[(u + 1) % 3] && fetch(v[(u + 2) % 3]);
                 const int eb = (int)(groups & 1);
                 if (groups >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((uint32_t)(groups >> 1) + 1u) & 1u, p.limit);
                 if (!ok) break;
@@ -775,18 +790,22 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
                 __syncwarp();
                 if (lane == 0) arrive_cluster(to + eb * 8);
                 ++groups;
-                has[u] = false;
+                full[u] = false;
             }
         }
         // the MMAs' last signals arrive before the CTA may leave
-        for (int64_t g = groups >= 2 ? groups - 2 : 0; ok && g < groups; ++g)
+        for (uint32_t g = groups >= 2 ? groups - 2 : 0; ok && g < groups; ++g)
             ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[g & 1]), (uint32_t)(g >> 1) & 1u, p.limit);
     }
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     if constexpr (GROUP == 2) cluster_sync();
-    else if (p.s.splits > 1) join_cluster<T, S>(p, sh, reinterpret_cast<float *>(raw_smem), rank);
+    else if (p.s.splits > 1) {
+        Item it;
+        item_of<GROUP>(p.s, 0, rank, it);
+        join_cluster<T, S>(p, it, sh, reinterpret_cast<float *>(raw_smem), rank);
+    }
     if (warp == 1) {
         if constexpr (GROUP == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem));
         else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem));
@@ -805,7 +824,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Params p)
     const int lo = p.s.from[c], hi = p.s.to[c];
     if (lo == hi) return;  // one range has the whole tile, and has stored it
     Item it;
-    tile_place(p.s, p.s.whole + c, it);
+    tile_place(p.s, p.s.whole + (uint32_t)c, it);
     const int64_t feature = (int64_t)it.tw * S::kFeatures + w, token = (int64_t)it.tx * p.s.tokens + x;
     if (feature >= p.features || x >= p.s.tokens || token >= p.tokens) return;
     const int n = (int)min((int64_t)4, p.features - feature);

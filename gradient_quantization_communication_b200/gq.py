@@ -283,17 +283,18 @@ def gq_elias_unpack(cfg, emsg, msg, stream=None):
 # ---------------------------------------------------------------------------------------------
 # activations kept in 8 bits: these take tensors, whose sizes, strides and types are the arguments
 # ---------------------------------------------------------------------------------------------
-_torch = _dtypes = _current_stream = None
+_torch = _dtypes = _current_stream = _current_device = None
 
 
 def _setup():
     """torch, looked up once: it is imported by the first call that takes tensors."""
-    global _torch, _dtypes, _current_stream
+    global _torch, _dtypes, _current_stream, _current_device
     import torch
     _dtypes = {torch.float32: GQ_FLOAT32, torch.bfloat16: GQ_BFLOAT16, torch.float16: GQ_FLOAT16}
     # the handle itself where torch offers it: building a Stream object around it takes a microsecond
     _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
 
 
@@ -353,7 +354,7 @@ def _launch(fn, what, stream, tensors, *args):
         stream = _current_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if _torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, stream)
     else:
         with _torch.cuda.device(dev):
@@ -638,11 +639,12 @@ def gq_adamw_create(params, grads, ms, vs, masters=None, weight_decay=0.0, lr_sc
         array[i] = gq_adamw_tensor_t(*ptr, n, per["weight_decay"][i], per["lr_scale"][i])
     cfg = gq_adamw_config_t(_dtype(params[0], "params") if count else GQ_FLOAT32,
                             _dtype(grads[0], "grads") if count else GQ_FLOAT32, bits, int(seed))
+    if _torch is None:
+        _setup()
     h = _AdamWHandle()
-    import torch
-    h.device = device.index if count else torch.cuda.current_device()
+    h.device = device.index if count else _torch.cuda.current_device()
     h.total = total
-    with torch.cuda.device(h.device):
+    with _torch.cuda.device(h.device):
         _check(lib().gq_adamw_create(ctypes.byref(cfg), array, count, ctypes.byref(h)), "gq_adamw_create")
     return h
 
@@ -652,20 +654,21 @@ def gq_adamw_destroy(opt):
 
 
 def _adamw_call(fn, what, opt, stream, tensors, *args):
-    import torch
+    dev = opt.device
     for t in tensors:
-        if t is not None and t.get_device() != opt.device:
-            raise ValueError("%s: tensors on cuda:%d expected, got %s" % (what, opt.device, t.device))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("%s: tensors on cuda:%d expected, got %s" % (what, dev, t.device))
     if stream is None:
-        stream = torch.cuda.current_stream(opt.device).cuda_stream
+        stream = _current_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == opt.device:
+    if _current_device() == dev:
         st = fn(opt, *args, stream)
     else:
-        with torch.cuda.device(opt.device):
+        with _torch.cuda.device(dev):
             st = fn(opt, *args, stream)
-    _check(st, what)
+    if st != GQ_OK:
+        raise GQError(st, what)
 
 
 def gq_adamw_norm(opt, max_norm, out, stream=None):
