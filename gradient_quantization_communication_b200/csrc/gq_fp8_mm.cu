@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     } else {
         if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExp));
         // Exponents: each warp its quarter of the lanes, all four the same words.  A tile's first words come from memory
-        // (the next ones from the same sectors): they are fetched two groups ahead, across tiles.
+        // (the next ones from the same sectors): they are fetched a group ahead, across tiles.
         constexpr int kN = S::kExpCols;
         const uint32_t to = in_cta(smem_u32(&sh.exp_full[0]), leader);
         const uint32_t lanes = tmem + S::kExps + ((uint32_t)((warp & 3) * 32) << 16);
@@ -748,50 +748,48 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
         Item it;
         int next = 0;
         int g = 0, end = 0;  // groups of the item that is fetched
-        auto fetch = [&](uint32_t (&v)[kN]) {
-            if (g == end) {
-                if (!item_of<GROUP>(p.s, next, rank, it)) return false;
+        uint32_t groups = 0;
+        bool ok = true, held = false;  // whether v[0] holds words; v[1] receives the next ones meanwhile
+        uint32_t v[2][kN] = {};
+#pragma unroll 1
+        for (bool more = true; ok && (more || held);) {
+            if (more && g == end) {
+                more = item_of<GROUP>(p.s, next, rank, it);
                 ++next;
-                g = it.first >> 2;
-                end = ((it.last - 1) >> 2) + 1;
+                if (more) {
+                    g = it.first >> 2;
+                    end = ((it.last - 1) >> 2) + 1;
 #pragma unroll
-                for (int c = 0; c < kN; ++c) {
-                    const Exps &e = c < 4 ? p.ew : p.ex;
-                    const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + pair_rank * 128 + c * 32 + lane
-                                              : (int64_t)it.tx * p.s.tokens + (c - 4) * 32 + lane;
-                    const bool in = row < e.rows && (c < 4 || (c - 4) * 32 + lane < p.s.tokens);
-                    rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
+                    for (int c = 0; c < kN; ++c) {
+                        const Exps &e = c < 4 ? p.ew : p.ex;
+                        const int64_t row = c < 4 ? (int64_t)it.tw * S::kFeatures + pair_rank * 128 + c * 32 + lane
+                                                  : (int64_t)it.tx * p.s.tokens + (c - 4) * 32 + lane;
+                        const bool in = row < e.rows && (c < 4 || (c - 4) * 32 + lane < p.s.tokens);
+                        rows[c] = in ? e.p + (row >> e.shift) * e.pitch : nullptr;
+                    }
                 }
             }
+            if (more) {
 #pragma unroll
-            for (int c = 0; c < kN; ++c) v[c] = rows[c] ? __ldg(reinterpret_cast<const uint32_t *>(rows[c]) + g) : 0u;
-            ++g;
-            return true;
-        };
-        uint32_t groups = 0;
-        bool ok = true;
-        uint32_t v[3][kN];
-        bool full[3];
-        full[0] = fetch(v[0]);
-        full[1] = full[0] && fetch(v[1]);
-        while (ok && full[0]) {
-#pragma unroll
-            for (int u = 0; u < 3; ++u) {
-                if (!ok || !full[u]) break;
-                full[(u + 2) % 3] = full[(u + 1) % 3] && fetch(v[(u + 2) % 3]);
+                for (int c = 0; c < kN; ++c) v[1][c] = rows[c] ? __ldg(reinterpret_cast<const uint32_t *>(rows[c]) + g) : 0u;
+                ++g;
+            }
+            if (held) {
                 const int eb = (int)(groups & 1);
-                if (groups >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((uint32_t)(groups >> 1) + 1u) & 1u, p.limit);
+                if (groups >= 2) ok = mbar_wait_cycles_warp(smem_u32(&sh.exp_empty[eb]), ((groups >> 1) + 1u) & 1u, p.limit);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-                for (int c = 0; c < kN; c += 4) tmem_store4(lanes + eb * kN + c, v[u] + c);
+                for (int c = 0; c < kN; c += 4) tmem_store4(lanes + eb * kN + c, v[0] + c);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) arrive_cluster(to + eb * 8);
                 ++groups;
-                full[u] = false;
             }
+            held = more;
+#pragma unroll
+            for (int c = 0; c < kN; ++c) v[0][c] = v[1][c];
         }
         // the MMAs' last signals arrive before the CTA may leave
         for (uint32_t g = groups >= 2 ? groups - 2 : 0; ok && g < groups; ++g)
