@@ -242,10 +242,6 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof
     using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
     constexpr int kWords = sizeof(AdamChunk) / 16;
     __shared__ AdamChunk entry[3];
-    const float scale = p.s.scale ? *p.s.scale : 1.0f;
-    if (scale != scale) return;
-    gq_adamw_scalars_t now = p.s.now;
-    if (p.s.scalars) now = *p.s.scalars;
     const int lane = threadIdx.x & 31, first = (int)(threadIdx.x >> 5) * kChunk, tid = threadIdx.x;
     const int64_t step = gridDim.x;
     int64_t i = blockIdx.x;
@@ -254,6 +250,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof
         reinterpret_cast<uint4 *>(&entry[0])[tid] = fetch(i);
         if (i + step < p.chunks) reinterpret_cast<uint4 *>(&entry[1])[tid] = fetch(i + step);
     }
+    cudaGridDependencySynchronize();  // the table never changes; all else may be written by the kernel before
+    const float scale = p.s.scale ? *p.s.scale : 1.0f;
+    if (scale != scale) return;
+    gq_adamw_scalars_t now = p.s.now;
+    if (p.s.scalars) now = *p.s.scalars;
     __syncthreads();
     Loaded<S, G, EIGHT, AL> a;
     auto fetch_elements = [&](Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
@@ -338,6 +339,7 @@ template <typename T, bool EIGHT>
 __global__ void __launch_bounds__(kThreads, EIGHT ? 8 : 6) k_moments(const __grid_constant__ Params p, void *m, void *v)
 {
     const AdamChunk c = p.table[blockIdx.x];
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31;
     const bool al = c.start % (16 / (int)sizeof(T)) == 0;
     for (int base = (int)(threadIdx.x >> 5) * kChunk; base < c.n; base += kHalf) {
@@ -394,6 +396,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(const AdamChunk *table, int64
     double s = 0.0;
     const void *grad = table[blockIdx.x].grad;
     int n = table[blockIdx.x].n;
+    cudaGridDependencySynchronize();
     for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
         const G *const g = static_cast<const G *>(grad);
         const int count = n;
@@ -410,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(const AdamChunk *table, int64
 __global__ void __launch_bounds__(kThreads) k_norm_join(const double *parts, int n, double max_norm, float *out)
 {
     __shared__ double shared[kThreads / 32];
+    cudaGridDependencySynchronize();
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += kThreads) s += parts[i];
     s = block_sum(s, shared);
@@ -418,6 +422,23 @@ __global__ void __launch_bounds__(kThreads) k_norm_join(const double *parts, int
         out[0] = (float)norm;
         out[1] = norm <= 1.7e308 ? (float)f : __uint_as_float(0x7fffffffu);
     }
+}
+
+// Launched to start as the kernel before it on the stream drains: these kernels follow one another, some of a few
+// microseconds, and each waits for the one before by itself.
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kern)(A...), unsigned grid, cudaStream_t s, B... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
@@ -432,8 +453,7 @@ cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
     p.chunks = chunks;
     // 32 bits: a block a chunk, replaced by the next as it ends (268 us against 286 for a grid that stays, 64 x 1e6)
     const int64_t most = EIGHT ? (int64_t)per_sm * sms : chunks;
-    kern<<<(unsigned)(chunks < most ? chunks : most), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(kern, (unsigned)(chunks < most ? chunks : most), s, p);
 }
 template <typename P, typename G, bool MASTER, bool EIGHT>
 cudaError_t launch_parts(const AdamArgs &a, const Params &p, cudaStream_t s)
@@ -464,9 +484,7 @@ cudaError_t launch_grad(const AdamArgs &a, const Params &p, cudaStream_t s)
 template <typename T>
 cudaError_t launch_moments(const AdamArgs &a, const Params &p, void *m, void *v, cudaStream_t s)
 {
-    if (a.state_bits == 8) k_moments<T, true><<<(unsigned)a.chunks, kThreads, 0, s>>>(p, m, v);
-    else k_moments<T, false><<<(unsigned)a.chunks, kThreads, 0, s>>>(p, m, v);
-    return cudaGetLastError();
+    return launch_after(a.state_bits == 8 ? k_moments<T, true> : k_moments<T, false>, (unsigned)a.chunks, s, p, m, v);
 }
 
 Params params_of(const AdamArgs &a)
@@ -504,12 +522,11 @@ cudaError_t launch_adamw_norm(const AdamArgs &a, double max_norm, double *parts,
 {
     const unsigned grid = (unsigned)(a.chunks < kNormParts ? a.chunks : kNormParts);
     if (grid) {
-        if (a.grad_dtype == GQ_FLOAT32) k_norm<float><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
-        else if (a.grad_dtype == GQ_BFLOAT16) k_norm<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
-        else k_norm<__half><<<grid, kThreads, 0, s>>>(a.table, a.aligned, a.chunks, parts);
+        auto kern = a.grad_dtype == GQ_FLOAT32 ? k_norm<float> : a.grad_dtype == GQ_BFLOAT16 ? k_norm<__nv_bfloat16> : k_norm<__half>;
+        const cudaError_t e = launch_after(kern, grid, s, a.table, a.aligned, a.chunks, parts);
+        if (e != cudaSuccess) return e;
     }
-    k_norm_join<<<1, kThreads, 0, s>>>(parts, (int)grid, max_norm, out);
-    return cudaGetLastError();
+    return launch_after(k_norm_join, 1, s, (const double *)parts, (int)grid, max_norm, out);
 }
 
 }  // namespace gq
