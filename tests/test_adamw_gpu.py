@@ -383,3 +383,95 @@ def test_elements_past_32_bits():
         assert np.array_equal(buf[off + first // 128:off + first // 128 + 4].cpu().numpy(), exps)
         assert int(buf[:first].max()) == 0
     assert int((p[:first] != 0).sum()) == 0 and int((p[first:] != 0).sum()) > 420
+
+
+def _run_gradients(values, bits, steps=2):
+    """A step or two on gradients of any size, from zero moments."""
+    n = values.numel()
+    c = Case([n], torch.float32, torch.float32, False, bits, zero=True)
+    c.flat["grad"][:n] = values.cuda()
+    for step in range(1, steps + 1):
+        before = c.snapshot()
+        c.opt.step(**HYPER, step=step)
+        yield c, before, step
+
+
+@pytest.mark.parametrize("lo,hi", [(-149, -100), (-80, -60), (-70, -63), (20, 40), (60, 68), (-149, 63)])
+def test_second_moments_of_every_size(lo, hi):
+    """8 bits: gradients whose squares are subnormal, vanish, come near binary32's largest value or pass it, and blocks
+    that span more than the codes do."""
+    rng = np.random.RandomState(5)
+    g = np.ldexp(rng.uniform(1, 2, 1280) * rng.choice([-1, 1], 1280), rng.randint(lo, hi, 1280)).astype(np.float32)
+    g[::7] = 0.0
+    g[256:384] = 0.0                                     # a block of nothing
+    g[400] = np.float32(2.0) ** (hi - 1)
+    for c, (before,), step in _run_gradients(torch.from_numpy(g), 8):
+        p, g64, m, v = before
+        h = dict(HYPER, lr=f32(HYPER["lr"]))
+        _, m32, v32 = O.adam_update(p, g64, m, v, **h, step=step, dtype=np.float32)
+        cm, em = O.pack(torch.from_numpy(m32.astype(np.float64)).view(10, 128), "e4m3", False)
+        cv, ev = O.squares_encode(v32.astype(np.float64).reshape(10, 128), O.noise(0, 1280, step, 0, 99).reshape(10, 128))
+        for buf, codes, exps in ((c.m[0], cm, em[:, 0]), (c.v[0], cv, ev)):
+            gc, ge = c.codes(buf, 1280)
+            assert np.array_equal(ge, exps) and np.array_equal(gc, codes)
+        gm, gv = c.moments(0)
+        # a second moment that is not 0 is kept above 0
+        assert (gv[np.isfinite(gv) & (v32 > 0)] > 0).all() and (gv[v32 == 0] == 0)[np.isfinite(gv[v32 == 0])].all()
+
+
+def test_two_optimizers_on_two_streams():
+    made = [Case([70000, 300, 8200], torch.bfloat16, torch.float32, True, 8, seed=7) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in made[1:]]
+    outs = [torch.empty(2, device="cuda") for _ in made]
+    torch.cuda.synchronize()
+    for step in (1, 2, 3):
+        for c, s, o in zip(made[1:], streams, outs[1:]):
+            c.opt.norm(0.3, o, stream=s)
+            c.opt.step(**HYPER, step=step, scale=o[1:], stream=s)
+        torch.cuda.synchronize()
+        made[0].opt.norm(0.3, outs[0])
+        torch.cuda.synchronize()
+        made[0].opt.step(**HYPER, step=step, scale=outs[0][1:])
+        torch.cuda.synchronize()
+        for c in made[1:]:
+            for k in c.flat:
+                assert torch.equal(c.flat[k], made[0].flat[k])
+            for x, y in zip(c.m + c.v, made[0].m + made[0].v):
+                assert torch.equal(x, y)
+
+
+def test_gradients_written_just_before():
+    """The norm and the step read what the kernel before them on the stream has just written."""
+    runs = []
+    for wait in (True, False):
+        c = Case([300000, 1000], torch.float32, torch.float32, False, 32, seed=8)
+        out = torch.empty(2, device="cuda")
+        g0 = c.flat["grad"].clone()
+        for step in range(1, 16):
+            torch.mul(g0, 1.0 / step, out=c.flat["grad"])
+            if wait:
+                torch.cuda.synchronize()
+            c.opt.norm(0.1, out)
+            if wait:
+                torch.cuda.synchronize()
+            c.opt.step(**HYPER, step=step, scale=out[1:])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        runs.append(c)
+    assert all(torch.equal(runs[0].flat[k], runs[1].flat[k]) for k in runs[0].flat)
+
+
+def test_shared_gradients_and_noncontiguous_order():
+    """Two parameters may take one gradient; tensors may lie in memory in any order."""
+    buf = torch.randn(4000, device="cuda")
+    g = 1e-2 * torch.randn(1000, device="cuda")
+    params = [buf[2000:3000], buf[:1000]]
+    ms, vs = ([torch.zeros(1000, device="cuda") for _ in range(2)] for _ in range(2))
+    before = [p.double().cpu().numpy() for p in params]
+    with G.AdamW(params, [g, g], ms, vs, weight_decay=0.0) as opt:
+        opt.step(**HYPER, step=1)
+    for p, b in zip(params, before):
+        wp, _, _ = O.adam_update(b, g.double().cpu().numpy(), np.zeros(1000), np.zeros(1000),
+                                 **dict(HYPER, lr=f32(HYPER["lr"])), step=1)
+        assert np.abs(p.double().cpu().numpy() - wp).max() <= 2.0 ** -22 * np.abs(b).max()
