@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <new>
+#include <memory>
 #include <vector>
 
 #include "gq_adamw.h"
@@ -18,7 +18,7 @@ struct Span {
 
 struct gq_adamw {
     gq::AdamArgs a;
-    std::vector<gq::Span> spans;  // the tensors' memory, by address
+    std::vector<gq::Span> all, written;  // the tensors' memory, and what a step writes of it: apart, by address
     void *memory;   // device: the table of chunks, the norm's partial sums
     double *parts;
     int64_t total;  // elements
@@ -51,16 +51,26 @@ bool any_shared(std::vector<Span> &s)
     return false;
 }
 
-// Whether `bytes` from p share a byte with the tensors' memory (`reads`: with what a step writes).
-bool in_tensors(const gq_adamw &o, const void *p, size_t bytes, bool reads)
+// The union of spans sorted by address (of the written ones among them), as spans that do not touch.
+std::vector<Span> merged(const std::vector<Span> &s, bool written)
+{
+    std::vector<Span> out;
+    for (const Span &x : s) {
+        if (written && !x.written) continue;
+        if (!out.empty() && x.from <= out.back().to) out.back().to = std::max(out.back().to, x.to);
+        else out.push_back(x);
+    }
+    return out;
+}
+
+// Whether `bytes` from p share a byte with one of them.
+bool meets(const std::vector<Span> &s, const void *p, size_t bytes)
 {
     if (!p || !bytes) return false;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    for (const Span &x : o.spans) {
-        if (x.from >= a + bytes) break;
-        if (x.to > a && (x.written || !reads)) return true;
-    }
-    return false;
+    // the first that ends behind p
+    auto x = std::upper_bound(s.begin(), s.end(), a, [](uintptr_t at, const Span &b) { return at < b.to; });
+    return x != s.end() && x->from < a + bytes;
 }
 
 bool factor_ok(float x) { return x >= 0.0f && x <= 3.0e38f; }
@@ -142,24 +152,22 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
         }
         if (pass == 0) aligned_chunks = (int64_t)table.size();
     }
-    gq_adamw *o = new gq_adamw;
-    o->spans.swap(spans);
+    std::unique_ptr<gq_adamw> o(new gq_adamw);
+    o->all = merged(spans, false);
+    o->written = merged(spans, true);
     o->total = total;
     o->memory = nullptr;
     const size_t bytes = table.size() * sizeof(AdamChunk);
-    if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, bytes + kNormParts * sizeof(double)) != cudaSuccess) {
-        delete o;
+    if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, bytes + kNormParts * sizeof(double)) != cudaSuccess)
         return GQ_ERR_CUDA;
-    }
     unsigned char *mem = static_cast<unsigned char *>(o->memory);
     if (bytes && cudaMemcpy(mem, table.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess) {
         cudaFree(o->memory);
-        delete o;
         return GQ_ERR_CUDA;
     }
     o->a = AdamArgs{c.param_dtype, c.grad_dtype, c.state_bits, master, aligned_chunks, chunks, reinterpret_cast<AdamChunk *>(mem), c.seed};
     o->parts = reinterpret_cast<double *>(mem + bytes);
-    *out = o;
+    *out = o.release();
     return GQ_OK;
 }
 
@@ -184,7 +192,7 @@ gq_status_t gq_adamw_create(const gq_adamw_config_t *cfg, const gq_adamw_tensor_
     if (count < 0 || count > GQ_ADAMW_MAX_TENSORS || (count && !tensors)) return GQ_ERR_INVALID;
     try {
         return create(*cfg, tensors, count, out);
-    } catch (const std::bad_alloc &) {
+    } catch (...) {  // std::bad_alloc, or a length that no vector takes
         return GQ_ERR_NOMEM;
     }
 }
@@ -203,7 +211,7 @@ gq_status_t gq_adamw_norm(gq_adamw_t opt, double max_norm, float *out, void *str
     if (!opt || !out || !aligned(out, 4) || !(max_norm > 0.0)) return GQ_ERR_INVALID;
     const gq_status_t st = check_device(*opt);
     if (st != GQ_OK) return st;
-    if (in_tensors(*opt, out, 8, false)) return GQ_ERR_INVALID;
+    if (meets(opt->all, out, 8)) return GQ_ERR_INVALID;
     return from_cuda(launch_adamw_norm(opt->a, max_norm, opt->parts, out, static_cast<cudaStream_t>(stream)));
 }
 
@@ -229,7 +237,7 @@ gq_status_t gq_adamw_step(gq_adamw_t opt, double lr, double beta1, double beta2,
     if (opt->a.chunks == 0) return GQ_OK;
     const gq_status_t st = check_device(*opt);
     if (st != GQ_OK) return st;
-    if (in_tensors(*opt, scale, 4, true) || in_tensors(*opt, scalars, 16, true)) return GQ_ERR_INVALID;
+    if (meets(opt->written, scale, 4) || meets(opt->written, scalars, 16)) return GQ_ERR_INVALID;
     s.beta1 = (float)beta1;
     s.rest1 = (float)(1.0 - beta1);
     s.beta2 = (float)beta2;
@@ -249,7 +257,7 @@ gq_status_t gq_adamw_moments(gq_adamw_t opt, int dtype, void *m, void *v, void *
     if (overlap(region(m, (size_t)opt->total * size), region(v, (size_t)opt->total * size))) return GQ_ERR_INVALID;
     const gq_status_t st = check_device(*opt);
     if (st != GQ_OK) return st;
-    if (in_tensors(*opt, m, (size_t)opt->total * size, false) || in_tensors(*opt, v, (size_t)opt->total * size, false))
+    if (meets(opt->all, m, (size_t)opt->total * size) || meets(opt->all, v, (size_t)opt->total * size))
         return GQ_ERR_INVALID;
     return from_cuda(launch_adamw_moments(opt->a, dtype, m, v, static_cast<cudaStream_t>(stream)));
 }
