@@ -35,22 +35,24 @@ __device__ __forceinline__ void sum2(Two a, Two b, float &x, float &y)
     y = __fadd_rn(a1, b1);
 }
 
-// The update's square root and quotient: rounded to nearest, or, where the moments are in 8 bits and instructions bound
-// the kernel (206 us against 179, 64 tensors of 1e6, bf16 parameters and fp32 gradients), off by up to 2 units in the
-// last place each.  Only the parameter's own change, lr times something near 1, carries that error.
+// The update's square root and quotient: rounded to nearest, or (FAST) off by up to 2 units in the last place each, and
+// subnormal second moments as 0.  Only the parameter's own change, lr times something near 1, carries that error.  FAST is
+// taken where the moments are in 8 bits and instructions bound the kernel (206 us against 172 when it was built, 64 tensors
+// of 1e6, bf16 parameters and fp32 gradients), and eps is so large that a subnormal moment's root (below 2^-63) vanishes
+// beside it.
 template <bool FAST>
 __device__ __forceinline__ float root(float x)
 {
     if constexpr (!FAST) return __fsqrt_rn(x);
     float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 template <bool FAST>
 __device__ __forceinline__ float quotient(float a, float b)
 {
     if constexpr (!FAST) return __fdiv_rn(a, b);
-    else return __fdividef(a, b);  // b is below 2^126 unless it is infinite: a root of binary32 times at most 2^14
+    else return __fmul_rn(a, rcp_approx(b));  // b is at least eps, and below 2^126 unless it is infinite
 }
 
 // Bits of the largest |x| of a block of 128, which 16 lanes hold (a NaN's above infinity's).
@@ -152,7 +154,7 @@ __device__ __forceinline__ void load(Loaded<S, G, EIGHT, AL> &l, const AdamChunk
 }
 
 // One warp's 256 elements from `base` of a chunk.
-template <typename P, typename S, typename G, bool MASTER, bool EIGHT, bool AL, bool FULL>
+template <typename P, typename S, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL, bool FULL>
 __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c,
                                        const gq_adamw_scalars_t &now, float scale, int base, int lane)
 {
@@ -181,8 +183,8 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
         sum2(mul2(two(m[j], m[j + 1]), beta1s), mul2(gj, rest1s), m[j], m[j + 1]);
         sum2(mul2(two(v[j], v[j + 1]), beta2s), mul2(mul2(gj, gj), rest2s), v[j], v[j + 1]);
         float a, b;
-        sum2(mul2(two(root<EIGHT>(v[j]), root<EIGHT>(v[j + 1])), inv2s), epss, a, b);
-        const Two u = two(quotient<EIGHT>(m[j], a), quotient<EIGHT>(m[j + 1], b));
+        sum2(mul2(two(root<FAST>(v[j]), root<FAST>(v[j + 1])), inv2s), epss, a, b);
+        const Two u = two(quotient<FAST>(m[j], a), quotient<FAST>(m[j + 1], b));
         sum2(mul2(two(x[j], x[j + 1]), keeps), mul2(sizes, u), x[j], x[j + 1]);
     }
     Words<S> ws;
@@ -236,7 +238,7 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
 // way only so (195 us against 211; with a bf16 parameter 178 against 157).
 constexpr int blocks_of(bool eight, int updated, int grad) { return eight && updated + grad == 8 ? 2 : 3; }
 
-template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
+template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL>
 __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof(P), sizeof(G))) k_adamw(const __grid_constant__ Params p)
 {
     using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof
         else if (base < c.n) load<S, G, MASTER, EIGHT, AL, false>(l, c, base, lane);
     };
     auto work = [&](const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (AL && base + kChunk <= c.n) update<P, S, G, MASTER, EIGHT, AL, AL>(p, l, c, now, scale, base, lane);
-        else if (base < c.n) update<P, S, G, MASTER, EIGHT, AL, false>(p, l, c, now, scale, base, lane);
+        if (AL && base + kChunk <= c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
+        else if (base < c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, false>(p, l, c, now, scale, base, lane);
     };
     if (EIGHT) fetch_elements(a, entry[0], first);
     for (int k = 0; i < p.chunks; i += step) {
@@ -441,11 +443,11 @@ cudaError_t launch_after(void (*kern)(A...), unsigned grid, cudaStream_t s, B...
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename P, typename G, bool MASTER, bool EIGHT, bool AL>
+template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL>
 cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
 {
     if (chunks == 0) return cudaSuccess;
-    auto kern = k_adamw<P, G, MASTER, EIGHT, AL>;
+    auto kern = k_adamw<P, G, MASTER, EIGHT, FAST, AL>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);
     if (e != cudaSuccess) return e;
@@ -455,16 +457,17 @@ cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
     const int64_t most = EIGHT ? (int64_t)per_sm * sms : chunks;
     return launch_after(kern, (unsigned)(chunks < most ? chunks : most), s, p);
 }
-template <typename P, typename G, bool MASTER, bool EIGHT>
+template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST>
 cudaError_t launch_parts(const AdamArgs &a, const Params &p, cudaStream_t s)
 {
-    const cudaError_t e = launch_part<P, G, MASTER, EIGHT, true>(p, 0, a.aligned, s);
-    return e != cudaSuccess ? e : launch_part<P, G, MASTER, EIGHT, false>(p, a.aligned, a.chunks - a.aligned, s);
+    const cudaError_t e = launch_part<P, G, MASTER, EIGHT, FAST, true>(p, 0, a.aligned, s);
+    return e != cudaSuccess ? e : launch_part<P, G, MASTER, EIGHT, FAST, false>(p, a.aligned, a.chunks - a.aligned, s);
 }
 template <typename P, typename G, bool MASTER>
 cudaError_t launch_state(const AdamArgs &a, const Params &p, cudaStream_t s)
 {
-    return a.state_bits == 8 ? launch_parts<P, G, MASTER, true>(a, p, s) : launch_parts<P, G, MASTER, false>(a, p, s);
+    if (a.state_bits != 8) return launch_parts<P, G, MASTER, false, false>(a, p, s);
+    return p.s.fast ? launch_parts<P, G, MASTER, true, true>(a, p, s) : launch_parts<P, G, MASTER, true, false>(a, p, s);
 }
 template <typename P, typename G>
 cudaError_t launch_master(const AdamArgs &a, const Params &p, cudaStream_t s)

@@ -41,6 +41,7 @@ struct AdamArgs {
 struct AdamStep {
     gq_adamw_scalars_t now;
     float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
+    bool fast;  // eps so large that the root of a subnormal second moment vanishes beside it
     const float *scale;
     const gq_adamw_scalars_t *scalars;
 };

@@ -243,6 +243,7 @@ gq_status_t gq_adamw_step(gq_adamw_t opt, double lr, double beta1, double beta2,
     s.beta2 = (float)beta2;
     s.rest2 = (float)(1.0 - beta2);
     s.eps = (float)eps;
+    s.fast = eps >= 0x1p-39 / std::sqrt(1.0 - beta2);  // 2^-63 times inv2 at its largest, t = 1, is below 2^-24 eps
     s.scale = scale;
     s.scalars = static_cast<const gq_adamw_scalars_t *>(scalars);
     return from_cuda(launch_adamw(opt->a, s, static_cast<cudaStream_t>(stream)));

@@ -138,9 +138,58 @@ __global__ void __launch_bounds__(256) k_pack_rows(const __grid_constant__ Param
 // 128 rows x 128 columns a block: along the columns, along both, and square tiles.  Half a warp takes 8 rows, a lane 8
 // columns of them, so that a lane's 8 codes of a column are one 8-byte piece of the transpose.  A block loads, finds its
 // largest values, and stores, with barriers between: as many blocks an SM as registers allow hide that from one another
-// (16384 x 8192 bf16 both ways: 130 us with two blocks of 512 threads on 256 columns, 110 with four of these).
+// (16384 x 8192 bf16 both ways: 130 us with two blocks of 512 threads on 256 columns, 97 with three of these; with four
+// 103, and 187 against 148 where rows start anywhere, their registers spilled).
 // ---------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 8;
+
+// Exponents of the 8 rows that 16 lanes hold 8 columns each of: byte i of the two words is row i's.  Lanes keep half of
+// the rows at each of the first steps, so that 5 exchanges (8 of binary32) find all largest values instead of 32, and an
+// exponent is formed once, not by all 16 lanes.
+template <typename T, int FMT>
+__device__ __forceinline__ void row_exps(const Words<T> (&w)[8], uint32_t (&e)[2])
+{
+    constexpr int W = 2 * (int)sizeof(T);
+    const int lane = threadIdx.x & 31;
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = abs_word<T>(w[i].w[0]);
+#pragma unroll
+        for (int k = 1; k < W; ++k) m[i] = max_word<T>(m[i], abs_word<T>(w[i].w[k]));
+    }
+    auto halve = [&](uint32_t a, uint32_t b, int bit) {  // lanes with the bit keep b
+        const uint32_t keep = (lane & bit) ? b : a, send = (lane & bit) ? a : b;
+        return max_word<T>(keep, __shfl_xor_sync(kFull, send, bit));
+    };
+    uint32_t E;
+    if constexpr (sizeof(T) == 2) {
+        uint32_t p[4];  // rows 2 k and 2 k + 1 in a word
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = max_u16x2(__byte_perm(m[2 * k], m[2 * k + 1], 0x5410), __byte_perm(m[2 * k], m[2 * k + 1], 0x7632));
+        uint32_t q = halve(halve(p[0], p[2], 8), halve(p[1], p[3], 8), 4);
+        q = max_u16x2(q, __shfl_xor_sync(kFull, q, 2));
+        q = max_u16x2(q, __shfl_xor_sync(kFull, q, 1));
+        E = fp8_exp<FMT>(float_bits<T>(q & 0xffffu)) | fp8_exp<FMT>(float_bits<T>(q >> 16)) << 8;
+        // lanes 8 (k / 2) + 4 (k mod 2) have rows 2 k and 2 k + 1
+        const int from = lane & 16;
+        e[0] = __shfl_sync(kFull, E, from) | __shfl_sync(kFull, E, from | 4) << 16;
+        e[1] = __shfl_sync(kFull, E, from | 8) | __shfl_sync(kFull, E, from | 12) << 16;
+    } else {
+        uint32_t a[4], b[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = halve(m[k], m[k + 4], 8);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[k] = halve(a[k], a[k + 2], 4);
+        uint32_t q = halve(b[0], b[1], 2);
+        q = max(q, __shfl_xor_sync(kFull, q, 1));
+        E = fp8_exp<FMT>(q);
+        // lanes 8 (i / 4) + 4 (i / 2 mod 2) + 2 (i mod 2) have row i
+        e[0] = e[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i >> 2] |= __shfl_sync(kFull, E, (lane & 16) | (i >> 2) << 3 | (i >> 1 & 1) << 2 | (i & 1) << 1) << (8 * (i & 3));
+    }
+}
 
 template <typename T, int FMT, bool TILE, bool AL, bool FULL>
 __device__ __forceinline__ void pack_tile(const Params &p, uint8_t *codes, uint8_t *exps)
@@ -218,9 +267,11 @@ __device__ __forceinline__ void pack_tile(const Params &p, uint8_t *codes, uint8
     __syncthreads();
 
     if (p.p.codes) {
+        uint32_t of_rows[2] = {};
+        if constexpr (!TILE) row_exps<T, FMT>(w, of_rows);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t e = TILE ? exps[0] : fp8_exp<FMT>(row_max<T>(w[i]));
+            const uint32_t e = TILE ? exps[0] : of_rows[i >> 2] >> (8 * (i & 3)) & 0xffu;
             float v[8];
             to_floats(w[i], v);
             const uint2 q = fp8_codes8<FMT>(v, e);
@@ -256,7 +307,7 @@ __device__ __forceinline__ void pack_tile(const Params &p, uint8_t *codes, uint8
 }
 
 template <typename T, int FMT, bool TILE, bool AL>
-__global__ void __launch_bounds__(kTileWarps * 32, sizeof(T) == 4 ? 2 : 4) k_pack_tile(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kTileWarps * 32, sizeof(T) == 4 ? 2 : 3) k_pack_tile(const __grid_constant__ Params p)
 {
     __shared__ __align__(16) uint8_t codes[kBlock * kBlock];  // transposed
     __shared__ uint8_t exps[kBlock];                          // of every column (TILE: the first, of all)

@@ -525,8 +525,9 @@ GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int
  *   g = grad * scale                                      (scale: the clipping factor; 1 without one)
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr lr_scale weight_decay) - lr lr_scale / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in binary32, each operation rounded on its own; (1 - beta1), 1 / (1 - beta1^t) and 1 / sqrt(1 - beta2^t) are
- * computed in binary64 and rounded once.
+ * in binary32, each operation rounded on its own (with moments in 8 bits the square root and the quotient may be off
+ * by 2 units in the last place); (1 - beta1), 1 / (1 - beta1^t) and 1 / sqrt(1 - beta2^t) are computed in binary64 and
+ * rounded once.
  *
  * Moments in 32 bits (state_bits = 32) are n float32 values each.  In 8 bits (state_bits = 8) each is
  * gq_adamw_layout bytes, 16-byte aligned: a code byte an element, padded to whole blocks of 128, then one
@@ -593,7 +594,7 @@ GQ_API gq_status_t gq_adamw_norm(gq_adamw_t opt, double max_norm, float *out, vo
  *   scale    device, one float that multiplies the gradients, e.g. gq_adamw_norm's out + 1 (NULL: 1).  If it
  *            is NaN the step changes nothing.
  *   scalars  NULL, or device memory (16 bytes, 16-byte aligned) holding what gq_adamw_scalars gives, read when
- *            the step runs in the place of lr and step: a captured step is replayed with new ones.
+ *            the step runs in the place of lr and step (for the same betas): a captured step is replayed with new ones.
  */
 typedef struct {
     float lr;

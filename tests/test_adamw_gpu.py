@@ -419,6 +419,27 @@ def test_second_moments_of_every_size(lo, hi):
         assert (gv[np.isfinite(gv) & (v32 > 0)] > 0).all() and (gv[v32 == 0] == 0)[np.isfinite(gv[v32 == 0])].all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-12, 1.0])
+def test_eps_of_every_size(bits, eps):
+    """Small second moments, subnormal ones among them, beside no eps and a large one."""
+    g = np.ldexp(np.random.RandomState(6).uniform(1, 2, 1280), np.random.RandomState(7).randint(-66, 0, 1280)).astype(np.float32)
+    c = Case([1280], torch.float32, torch.float32, bits == 0, bits, zero=True)
+    c.flat["grad"][:1280] = torch.from_numpy(g).cuda()
+    p, g64, m, v = c.snapshot()[0]
+    lr = f32(2e-3)
+    c.opt.step(lr, 0.9, 0.999, eps, 1)
+    e = f32(eps)
+    _, m32, v32 = O.adam_update(p, g64, m, v, lr, 0.9, 0.999, e, 1, dtype=np.float32)
+    # from the moments in binary32: what is asked for here is the update's own arithmetic
+    below = np.sqrt(v32.astype(np.float64)) / np.sqrt(1 - 0.999) + e
+    want = p - lr / (1 - 0.9) * m32.astype(np.float64) / below
+    upd = np.abs(lr / (1 - 0.9) * m32.astype(np.float64) / below)
+    got = c.params[0].double().cpu().numpy()
+    ok = v32 > 0
+    assert (np.abs(got - want)[ok] <= 16 * 2.0 ** -24 * upd[ok] + 4 * 2.0 ** -24 * np.abs(p[ok])).all()
+
+
 def test_two_optimizers_on_two_streams():
     made = [Case([70000, 300, 8200], torch.bfloat16, torch.float32, True, 8, seed=7) for _ in range(3)]
     streams = [torch.cuda.Stream() for _ in made[1:]]
