@@ -1,4 +1,9 @@
 // gq_fp8.cu -- packing matrices into 8-bit floating point along their rows and columns, and back.
+//
+// A block's exponent needs its largest value before its first code, so the 128 values wait in registers: along rows in
+// the 16 lanes that loaded them, along columns in a tile of 128 x 128 that a block holds, whose codes leave by way of
+// shared memory.  Bounded by bytes and by latency; 16384 x 8192 bf16, along rows 67 us, along columns 65, both 97, tiles
+// both ways 82, back 61, where the bytes take 62, 62, 83, 83 and 62.
 #include "gq_act.cuh"
 #include "gq_device.cuh"
 #include "gq_fp8.cuh"

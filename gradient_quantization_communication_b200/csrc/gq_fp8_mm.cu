@@ -7,6 +7,17 @@
 // stage is 128 columns of both, K-major rows of 128 bytes with the 128-byte swizzle, fetched by TMA.  The exponents
 // of four stages (512 columns) are one word a row; four warps put them into TMEM, where row r's word belongs into
 // lane r mod 32 of column r / 32, once in each quarter of the lanes.
+//
+// Two shapes (gq_fp8_tiles.h): CTA pairs on tiles of 256 features x up to 256 tokens, and, for up to 128 tokens, single
+// CTAs on 128 features whose clusters cut the columns.  In either, one thread fetches, one issues the MMAs, four warps
+// bring the exponents, and four or eight store tiles while the next ones are summed in a second accumulator.
+//
+// Bounded for many tokens by the SMs' way to L2 and then by power: a stage of a pair's CTA is 32 KB for 512 cycles of
+// MMAs, and arrives after 650 (13.5 TB/s over all SMs); the tensor pipe is active 72 % of the time.  Measured in graphs of
+// ten calls, bf16: 8192 tokens, 4096 x 4096 99 us (2.77 PFLOP/s), 16384 tokens, 4096 x 16384 759 us (2.90, 89 % of twice
+// the library's measured bf16 rate); in a long run of calls, under the power cap, some 2.3.  For few tokens by latency:
+// 16 tokens, 4096 x 4096 8.4 us, of which 1 us until the first copy is issued, 1.2 until it arrives, 1.1 for all stages, 1.2
+// for the sums' way out of TMEM and 2.7 for the cluster's join, where the weight's bytes would take 2.6.
 #include "gq_act.cuh"
 #include "gq_device.cuh"
 #include "gq_fp8.cuh"
@@ -191,7 +202,8 @@ struct Out {
         const int64_t feature = (int64_t)it.tw * S::kFeatures + row, token = (int64_t)it.tx * p.s.tokens + x0;
         const int64_t left = p.tokens - token;
         in = feature < p.features;
-        part = it.part < 0 ? nullptr : (S::kGroup == 1 ? shared : p.parts + (int64_t)it.part * S::kTokens * S::kFeatures) + x0 * S::kFeatures + row;
+        float *const tile = S::kGroup == 1 ? shared : p.parts + (int64_t)it.part * S::kTokens * S::kFeatures;
+        part = it.part < 0 ? nullptr : tile + x0 * S::kFeatures + row;
         n = (int)(left < 0 ? 0 : left < count ? left : count);
         y = static_cast<T *>(p.y) + token * sy + feature;
         bias = p.bias && in && !part ? p.bias[feature] : 0.0f;
@@ -231,8 +243,9 @@ struct Out {
         if (fast && c + 16 <= n) put16_whole(r, c);
         else if (c < n) put16(r, c);
     }
-    // The same where all 16 tokens exist, and where `fast`.  16-bit values go four features of a token at a time: of four tokens the lanes 4 q .. 4 q + 3
-    // exchange theirs, and lane 4 q + i stores token i's.
+    // The same where all 16 tokens exist, and where `fast`.  16-bit values go four features of a token at a time: of four
+    // tokens the lanes 4 q .. 4 q + 3 exchange theirs, and lane 4 q + i stores token i's (a store of 2 bytes by each lane
+    // takes four times as many; with a check for each of them a tile of 256 x 256 took 5.9 us, so it takes 3).
     __device__ __forceinline__ void put16_whole(const uint32_t (&r)[16], int c) const
     {
         if (part) {
@@ -365,6 +378,11 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
         }
         fence_barrier_init();
     }
+    __syncthreads();
+    if constexpr (GROUP == 2) cluster_sync();
+    // Up to here it runs as the kernel before it on the stream drains.  TMEM is not taken before: that kernel might still
+    // want it, and this one would wait for its end.
+    cudaGridDependencySynchronize();
     if (warp == 1) {
         if constexpr (GROUP == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "n"(S::kTmem) : "memory");
@@ -376,10 +394,8 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if constexpr (GROUP == 2) cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = sh.tmem;
-    cudaGridDependencySynchronize();  // up to here it runs as the kernel before it on the stream drains
 
     if (warp < 4) {
         if constexpr (GROUP == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
@@ -755,7 +771,8 @@ cudaError_t launch_shape(const Fp8MatmulArgs &g, cudaStream_t stream)
     // two seconds at 1.97 GHz, three at the power cap's 1.39 GHz; the longest wait, for a tile, is some microseconds a
     // thousand columns
     p.limit = 4000000000ll;
-    if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) || !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kGroup == 2 ? p.s.tokens / 2 : S::kTokens))
+    if (!encode_rows(&p.w, g.b, g.n, lw.code_pitch, 128) ||
+        !encode_rows(&p.x, g.a, g.m, lx.code_pitch, S::kGroup == 2 ? p.s.tokens / 2 : S::kTokens))
         return cudaErrorInvalidValue;
     p.run = run_of(g.dtype);
     const bool sums = p.s.blocks > p.run;

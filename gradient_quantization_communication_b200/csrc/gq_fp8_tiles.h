@@ -35,6 +35,9 @@ struct Shape {
     static constexpr int kSecond = TN > 128 ? 224 : TN;
     static constexpr int kExps = kSecond + TN;
     static constexpr int kTmem = kExps + 2 * kExpCols <= 128 ? 128 : kExps + 2 * kExpCols <= 256 ? 256 : 512;
+    // all CTAs that fit an SM get theirs at once, those of calls on other streams too: none waits for TMEM that another
+    // keeps until its cluster's join
+    static_assert(kPerSm * kTmem <= 512 && (kPerSm == 1 || 3 * kSmemBytes > 232448), "TMEM");
 };
 constexpr int kMostTokens = 256;
 using Pair = Shape<2, kMostTokens>;
