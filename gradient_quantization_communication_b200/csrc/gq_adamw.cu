@@ -8,7 +8,7 @@
 // Moments in 32 bits are bounded by bytes: 40 tensors of 25e6, bf16 parameters with float32 masters and bf16 gradients,
 // 1105 us with the moments' read-out where the bytes take 1147 at the rate of a plain copy.  In 8 bits by instructions and
 // latency: 64 tensors of 1e6, bf16 parameters and float32 gradients, 147 us where 770 MB take 118; 0.61 of the issue slots
-// are used, at 80 registers and 24 warps an SM.  The norm is bounded by bytes (48 us for 256 MB: 39).
+// are used, at 80 registers and 24 warps an SM.  The norm is bounded by bytes (41 us for 256 MB, which take 39).
 #include <type_traits>
 
 #include "gq_act.cuh"
@@ -379,40 +379,63 @@ __device__ __forceinline__ double block_sum(double s, double *shared)
 }
 
 template <typename G, bool AL>
-__device__ __forceinline__ double squares(const G *grad, int n, int first, int lane)
-{
+struct Grads {
     Raw<G, AL> r[2];
-    chunk_load<G, AL>(r[0], grad, first, lane, n);
-    chunk_load<G, AL>(r[1], grad, first + kHalf, lane, n);
-    double s[2] = {};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float g[8];
-        to_floats(in_place<G, AL>(r[h], grad), g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[h] = __fma_rn((double)g[j], (double)g[j], s[h]);
+    const G *at;
+    __device__ __forceinline__ void load(const AdamChunk &c, int first, int lane)
+    {
+        at = static_cast<const G *>(c.grad);
+        chunk_load<G, AL>(r[0], at, first, lane, c.n);
+        chunk_load<G, AL>(r[1], at, first + kHalf, lane, c.n);
     }
-    return s[0] + s[1];
+    __device__ __forceinline__ double squares() const
+    {
+        double s[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float g[8];
+            to_floats(in_place<G, AL>(r[h], at), g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[h] = __fma_rn((double)g[j], (double)g[j], s[h]);
+        }
+        return s[0] + s[1];
+    }
+};
+
+// The squares of the chunks i, i + gridDim.x, ... before `end`; i is left at the first behind.  A chunk's gradients are
+// on their way while the one before is summed, and its table entry an iteration longer (64 x 4194304: float32 178 us
+// without, 151 with, bf16 138 and 88).
+template <typename G, bool AL>
+__device__ __forceinline__ double walk(const AdamChunk *table, int64_t &i, int64_t end, int first, int lane)
+{
+    if (i >= end) return 0.0;
+    const int64_t step = gridDim.x;
+    double s = 0.0;
+    Grads<G, AL> now, next;
+    now.load(table[i], first, lane);
+    AdamChunk c = table[i + step < end ? i + step : i];
+    for (;;) {
+        i += step;
+        const bool more = i < end;
+        if (more) {
+            next.load(c, first, lane);
+            if (i + step < end) c = table[i + step];
+        }
+        s += now.squares();
+        if (!more) return s;
+        now = next;
+    }
 }
 
 template <typename G>
-__global__ void __launch_bounds__(kThreads) k_norm(const AdamChunk *table, int64_t aligned, int64_t chunks, double *parts)
+__global__ void __launch_bounds__(kThreads, kNormPerSm) k_norm(const AdamChunk *table, int64_t aligned, int64_t chunks, double *parts)
 {
     __shared__ double shared[kThreads / 32];
     const int lane = threadIdx.x & 31, first = (int)(threadIdx.x >> 5) * kChunk;
-    double s = 0.0;
-    const void *grad = table[blockIdx.x].grad;
-    int n = table[blockIdx.x].n;
     cudaGridDependencySynchronize();
-    for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-        const G *const g = static_cast<const G *>(grad);
-        const int count = n;
-        if (i + gridDim.x < chunks) {  // the next entry is on its way meanwhile
-            grad = table[i + gridDim.x].grad;
-            n = table[i + gridDim.x].n;
-        }
-        s += i < aligned ? squares<G, true>(g, count, first, lane) : squares<G, false>(g, count, first, lane);
-    }
+    int64_t i = blockIdx.x;
+    double s = walk<G, true>(table, i, aligned, first, lane);
+    s += walk<G, false>(table, i, chunks, first, lane);
     s = block_sum(s, shared);
     if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }

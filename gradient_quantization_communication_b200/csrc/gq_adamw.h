@@ -49,7 +49,7 @@ cudaError_t launch_adamw(const AdamArgs &a, const AdamStep &s, cudaStream_t stre
 cudaError_t launch_adamw_moments(const AdamArgs &a, int dtype, void *m, void *v, cudaStream_t stream);
 
 // Partial sums that the norm writes (binary64).
-constexpr int kNormParts = 148 * 8;
+constexpr int kNormPerSm = 4, kNormParts = 148 * kNormPerSm;
 cudaError_t launch_adamw_norm(const AdamArgs &a, double max_norm, double *parts, float *out, cudaStream_t stream);
 
 }  // namespace gq
