@@ -5,6 +5,8 @@ packing, decode and worker average) runs in the CUDA library ``libgq.so`` behind
 ``include/gq.h``; ``gq`` is its Python binding and ``synth`` draws seeded synthetic gradients.
 
 The gradients themselves can be made from activations kept in 8 bits: ``gq.gq_act_*`` (pack and
-unpack, activation functions, a linear layer's weight gradient) and ``gq.gq_layer_norm_*``.
+unpack, activation functions, a linear layer's weight gradient) and ``gq.gq_layer_norm_*``, or by
+products in 8-bit floating point, ``gq.gq_fp8_*`` (pack, unpack, the three products of a linear
+layer).  ``gq.AdamW`` takes the averaged gradient: its norm, and the step of all tensors at once.
 """
 from . import gq  # noqa: F401

@@ -5,10 +5,10 @@
 // largest value is found by shuffles within 16 lanes and every state is read and written once.
 // Every operation rounds on its own, in the formula's order; division and square root are IEEE's, but for `FAST` below.
 //
-// Moments in 32 bits are bounded by bytes: 40 tensors of 25e6, bf16 parameters with float32 masters and bf16 gradients,
-// 1105 us with the moments' read-out where the bytes take 1147 at the rate of a plain copy.  In 8 bits by instructions and
-// latency: 64 tensors of 1e6, bf16 parameters and float32 gradients, 147 us where 770 MB take 118; 0.61 of the issue slots
-// are used, at 80 registers and 24 warps an SM.  The norm is bounded by bytes (41 us for 256 MB, which take 39).
+// Moments in 32 bits are bounded by bytes: 64 tensors of 4194304, bf16 parameters with float32 masters and bf16
+// gradients, 1105 us, where the bytes take 1147 at the rate of a plain copy.  In 8 bits by instructions and latency: 64
+// tensors of 1e6, bf16 parameters and float32 gradients, 146 us, where 770 MB take 118; 61 % of the issue slots are used,
+// at 80 registers and 24 warps an SM.  The norm is bounded by bytes (41 us for 256 MB, which take 39).
 #include <type_traits>
 
 #include "gq_act.cuh"

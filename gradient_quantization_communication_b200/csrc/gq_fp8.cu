@@ -2,8 +2,9 @@
 //
 // A block's exponent needs its largest value before its first code, so the 128 values wait in registers: along rows in
 // the 16 lanes that loaded them, along columns in a tile of 128 x 128 that a block holds, whose codes leave by way of
-// shared memory.  Bounded by bytes and by latency; 16384 x 8192 bf16, along rows 67 us, along columns 65, both 97, tiles
-// both ways 82, back 61, where the bytes take 62, 62, 83, 83 and 62.
+// shared memory.  Bounded by bytes and by latency; 16384 x 8192 bf16, along rows 68 us, along columns 67, both 97, in
+// tiles both ways 85, back 64, where the bytes take 62, 62, 82, 82 and 62; a row of 16384 x 4095 whose start is not
+// aligned takes up to twice as long.
 #include "gq_act.cuh"
 #include "gq_device.cuh"
 #include "gq_fp8.cuh"
