@@ -161,7 +161,9 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
     if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, bytes + kNormParts * sizeof(double)) != cudaSuccess)
         return GQ_ERR_CUDA;
     unsigned char *mem = static_cast<unsigned char *>(o->memory);
-    if (bytes && cudaMemcpy(mem, table.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess) {
+    // a copy from pageable memory may return before its last bytes have arrived, and steps run on any stream
+    if (bytes && (cudaMemcpy(mem, table.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
+                  cudaStreamSynchronize(nullptr) != cudaSuccess)) {
         cudaFree(o->memory);
         return GQ_ERR_CUDA;
     }
@@ -243,7 +245,9 @@ gq_status_t gq_adamw_step(gq_adamw_t opt, double lr, double beta1, double beta2,
     s.beta2 = (float)beta2;
     s.rest2 = (float)(1.0 - beta2);
     s.eps = (float)eps;
-    s.fast = eps >= 0x1p-39 / std::sqrt(1.0 - beta2);  // 2^-63 times inv2 at its largest, t = 1, is below 2^-24 eps
+    // 2^-63 times inv2 at its largest, t = 1, is below 2^-24 eps; and with 2^64 times inv2 the divisor is below 2^126, whose
+    // reciprocal would be subnormal
+    s.fast = eps >= 0x1p-39 / std::sqrt(1.0 - beta2) && eps <= 0x1p64;
     s.scale = scale;
     s.scalars = static_cast<const gq_adamw_scalars_t *>(scalars);
     return from_cuda(launch_adamw(opt->a, s, static_cast<cudaStream_t>(stream)));

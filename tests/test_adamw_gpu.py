@@ -420,6 +420,24 @@ def test_second_moments_of_every_size(lo, hi):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [2.0 ** 64, 2.0 ** 65, 2.0 ** 125, 2.0 ** 126, 3e38])
+def test_eps_beyond_every_root(bits, eps):
+    """The update of parameters of 0 keeps its digits where the divisor's reciprocal is subnormal."""
+    g = np.random.RandomState(8).uniform(2.0 ** 59, 2.0 ** 60, 1280).astype(np.float32)
+    c = Case([1280], torch.float32, torch.float32, False, bits, zero=True)
+    c.flat["grad"][:1280] = torch.from_numpy(g).cuda()
+    c.params[0].zero_()
+    p, g64, m, v = c.snapshot()[0]
+    lr, e = 2.0 ** 60, f32(eps)
+    c.opt.step(lr, 0.9, 0.999, eps, 1)
+    _, m32, v32 = O.adam_update(p, g64, m, v, lr, 0.9, 0.999, e, 1, dtype=np.float32)
+    below = np.sqrt(v32.astype(np.float64)) / np.sqrt(1 - 0.999) + e
+    want = -lr / (1 - 0.9) * m32.astype(np.float64) / below
+    got = c.params[0].double().cpu().numpy()
+    assert (np.abs(got - want) <= 16 * 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-12, 1.0])
 def test_eps_of_every_size(bits, eps):
     """Small second moments, subnormal ones among them, beside no eps and a large one."""
