@@ -109,6 +109,33 @@ __device__ __forceinline__ void square_values(uint2 q, uint32_t E, float (&v)[8]
     }
 }
 
+// A lane's 8 elements, of which the first `head` of the piece are not the tensor's.
+template <typename T, bool AL, bool FULL, bool KEPT = true>
+__device__ __forceinline__ void piece_load(Raw<T, AL> &r, const T *row, int base, int lane, int head, int n)
+{
+    if constexpr (AL && !FULL) {
+        if (base + lane * 8 < head) {  // a piece's first lane
+#pragma unroll
+            for (int j = 0; j < 8; ++j) elem_set<T>(r.w, j, j >= head && j < n ? elem_bits(row[j]) : 0u);
+            return;
+        }
+    }
+    chunk_load<T, AL, FULL, KEPT>(r, row, base, lane, n);
+}
+template <typename T, bool AL, bool FULL>
+__device__ __forceinline__ void piece_store(const Words<T> &r, T *row, int base, int lane, int head, int n)
+{
+    if constexpr (AL && !FULL) {
+        if (base + lane * 8 < head) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j >= head && j < n) row[j] = elem_get<T>(r.w, j);
+            return;
+        }
+    }
+    chunk_store<T, AL, FULL>(r, row, base, lane, n);
+}
+
 // What a lane has loaded of its 8 elements.
 template <typename S, typename G, bool EIGHT, bool AL>
 struct Loaded {
@@ -136,9 +163,9 @@ __device__ __forceinline__ S *updated(const AdamChunk &c)
 template <typename S, typename G, bool MASTER, bool EIGHT, bool AL, bool FULL>
 __device__ __forceinline__ void load(Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base, int lane)
 {
-    const int n = c.n;
-    chunk_load<S, AL, FULL, false>(l.x, updated<S, MASTER>(c), base, lane, n);
-    chunk_load<G, AL, FULL>(l.g, static_cast<const G *>(c.grad), base, lane, n);
+    const int n = c.n, head = EIGHT ? 0 : c.head;
+    piece_load<S, AL, FULL, false>(l.x, updated<S, MASTER>(c), base, lane, head, n);
+    piece_load<G, AL, FULL>(l.g, static_cast<const G *>(c.grad), base, lane, head, n);
     if constexpr (EIGHT) {
         const int at = base + lane * 8;
         if (!FULL) {
@@ -153,8 +180,8 @@ __device__ __forceinline__ void load(Loaded<S, G, EIGHT, AL> &l, const AdamChunk
             l.ev = c.ev[at >> 7];
         }
     } else {
-        chunk_load<float, AL, FULL, false>(l.m[0], static_cast<const float *>(c.m), base, lane, n);
-        chunk_load<float, AL, FULL, false>(l.m[1], static_cast<const float *>(c.v), base, lane, n);
+        piece_load<float, AL, FULL, false>(l.m[0], static_cast<const float *>(c.m), base, lane, head, n);
+        piece_load<float, AL, FULL, false>(l.m[1], static_cast<const float *>(c.v), base, lane, head, n);
     }
 }
 
@@ -163,7 +190,7 @@ template <typename P, typename S, typename G, bool MASTER, bool EIGHT, bool FAST
 __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c,
                                        const gq_adamw_scalars_t &now, float scale, int base, int lane)
 {
-    const int n = c.n, at = base + lane * 8;
+    const int n = c.n, at = base + lane * 8, head = EIGHT ? 0 : c.head;
     S *const param = updated<S, MASTER>(c);
     float x[8], g[8], m[8], v[8], beta1 = p.s.beta1;
     to_floats(in_place<S, AL>(l.x, param), x);
@@ -194,11 +221,11 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
     }
     Words<S> ws;
     from_floats(ws, x);
-    chunk_store<S, AL, FULL>(ws, param, base, lane, n);
+    piece_store<S, AL, FULL>(ws, param, base, lane, head, n);
     if constexpr (MASTER) {
         Words<P> wp;
         from_floats(wp, x);
-        chunk_store<P, AL, FULL>(wp, static_cast<P *>(c.param), base, lane, n);
+        piece_store<P, AL, FULL>(wp, static_cast<P *>(c.param), base, lane, head, n);
     }
     if constexpr (EIGHT) {
         // elements past the tensor's last are zeros
@@ -230,9 +257,9 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
     } else {
         Words<float> w;
         from_floats(w, m);
-        chunk_store<float, AL, FULL>(w, static_cast<float *>(c.m), base, lane, n);
+        piece_store<float, AL, FULL>(w, static_cast<float *>(c.m), base, lane, head, n);
         from_floats(w, v);
-        chunk_store<float, AL, FULL>(w, static_cast<float *>(c.v), base, lane, n);
+        piece_store<float, AL, FULL>(w, static_cast<float *>(c.v), base, lane, head, n);
     }
 }
 
@@ -265,11 +292,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof
     __syncthreads();
     Loaded<S, G, EIGHT, AL> a;
     auto fetch_elements = [&](Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (AL && base + kChunk <= c.n) load<S, G, MASTER, EIGHT, AL, AL>(l, c, base, lane);
+        if (AL && base + kChunk <= c.n && (EIGHT || base >= c.head)) load<S, G, MASTER, EIGHT, AL, AL>(l, c, base, lane);
         else if (base < c.n) load<S, G, MASTER, EIGHT, AL, false>(l, c, base, lane);
     };
     auto work = [&](const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (AL && base + kChunk <= c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
+        if (AL && base + kChunk <= c.n && (EIGHT || base >= c.head)) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
         else if (base < c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, false>(p, l, c, now, scale, base, lane);
     };
     if (EIGHT) fetch_elements(a, entry[0], first);
@@ -345,7 +372,13 @@ __device__ __forceinline__ void put(const Moment<EIGHT> &l, const AdamChunk &c, 
 template <typename T, bool EIGHT>
 __global__ void __launch_bounds__(kThreads, EIGHT ? 8 : 6) k_moments(const __grid_constant__ Params p, void *m, void *v)
 {
-    const AdamChunk c = p.table[blockIdx.x];
+    AdamChunk c = p.table[blockIdx.x];
+    if constexpr (!EIGHT) {
+        c.m = static_cast<float *>(c.m) + c.head;
+        c.v = static_cast<float *>(c.v) + c.head;
+        c.n -= c.head;
+        c.start += c.head;
+    }
     cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31;
     const bool al = c.start % (16 / (int)sizeof(T)) == 0;
@@ -385,7 +418,7 @@ struct Grads {
     __device__ __forceinline__ void load(const AdamChunk &c, int first, int lane)
     {
         at = static_cast<const G *>(c.grad);
-        chunk_load<G, AL>(r[0], at, first, lane, c.n);
+        piece_load<G, AL, false>(r[0], at, first, lane, c.head, c.n);
         chunk_load<G, AL>(r[1], at, first + kHalf, lane, c.n);
     }
     __device__ __forceinline__ double squares() const

@@ -109,6 +109,16 @@ gq_status_t check_tensors(const gq_adamw_config_t &c, const gq_adamw_tensor_t *t
     return any_shared(spans) ? GQ_ERR_INVALID : GQ_OK;
 }
 
+// Elements before the tensor's first to where all its arrays lie on 16 bytes, below 8; -1: there is no such place.
+int head_of(const gq_adamw_tensor_t &x, uintptr_t ps, uintptr_t gs, bool eight)
+{
+    for (uintptr_t h = 0; h < (eight ? 1 : 8); ++h) {
+        auto on16 = [h](const void *p, uintptr_t size) { return !p || ((reinterpret_cast<uintptr_t>(p) - h * size) & 15) == 0; };
+        if (on16(x.param, ps) && on16(x.grad, gs) && on16(x.master, 4) && on16(x.m, 4) && on16(x.v, 4)) return (int)h;
+    }
+    return -1;
+}
+
 gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, int count, gq_adamw_t *out)
 {
     std::vector<Span> spans;
@@ -116,32 +126,35 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
     if (st != GQ_OK) return st;
     std::vector<AdamChunk> table;
     int64_t total = 0, chunks = 0, aligned_chunks = 0;
-    for (int i = 0; i < count; ++i) chunks += (list[i].n + kAdamChunk - 1) / kAdamChunk;
+    for (int i = 0; i < count; ++i) chunks += (list[i].n + 7 + kAdamChunk - 1) / kAdamChunk;
     if (chunks > (int64_t(1) << 31) - 1) return GQ_ERR_UNSUPPORTED;
     table.reserve((size_t)chunks);
     bool master = false;
     const int64_t ps = elem_size(c.param_dtype), gs = elem_size(c.grad_dtype), ss = c.state_bits == 8 ? 1 : 4;
-    for (int pass = 0; pass < 2; ++pass) {  // tensors that start on 16 bytes, then the others
+    for (int pass = 0; pass < 2; ++pass) {  // tensors whose arrays can be read by 16 bytes, then the others
         total = 0;
         for (int i = 0; i < count; ++i) {
             const gq_adamw_tensor_t &x = list[i];
-            const bool al = aligned(x.param, 16) && aligned(x.grad, 16) && aligned(x.master, 16) && aligned(x.m, 16) && aligned(x.v, 16);
-            for (int64_t at = 0; at < x.n && al == (pass == 0); at += kAdamChunk) {
-                auto plus = [at](void *p, int64_t size) { return static_cast<void *>(static_cast<uint8_t *>(p) + at * size); };
-                uint8_t *const m = static_cast<uint8_t *>(x.m), *const v = static_cast<uint8_t *>(x.v);
+            const int h = head_of(x, (uintptr_t)ps, (uintptr_t)gs, ss == 1), head = h < 0 ? 0 : h;
+            const int64_t end = x.n ? x.n + head : 0;
+            for (int64_t at = 0; at < end && (h >= 0) == (pass == 0); at += kAdamChunk) {
+                auto plus = [at, head](const void *p, int64_t size) {  // `head` elements back may be no place of the array
+                    return reinterpret_cast<void *>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)((at - head) * size));
+                };
                 AdamChunk t = {};
                 t.param = plus(x.param, ps);
-                t.grad = plus(const_cast<void *>(x.grad), gs);
-                t.master = x.master ? x.master + at : nullptr;
+                t.grad = plus(x.grad, gs);
+                t.master = x.master ? static_cast<float *>(plus(x.master, 4)) : nullptr;
                 t.m = plus(x.m, ss);
                 t.v = plus(x.v, ss);
                 if (ss == 1) {
-                    t.em = m + adam_exps_off(x.n) + at / 128;
-                    t.ev = v + adam_exps_off(x.n) + at / 128;
+                    t.em = static_cast<uint8_t *>(x.m) + adam_exps_off(x.n) + at / 128;
+                    t.ev = static_cast<uint8_t *>(x.v) + adam_exps_off(x.n) + at / 128;
                 }
                 t.group = at / 8;
-                t.start = total + at;
-                t.n = (int32_t)(x.n - at < kAdamChunk ? x.n - at : kAdamChunk);
+                t.start = total + at - head;
+                t.n = (int32_t)(end - at < kAdamChunk ? end - at : kAdamChunk);
+                t.head = at ? 0 : head;
                 t.number = (uint32_t)i;
                 t.decay = x.weight_decay;
                 t.lr_scale = x.lr_scale;
@@ -152,6 +165,7 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
         }
         if (pass == 0) aligned_chunks = (int64_t)table.size();
     }
+    chunks = (int64_t)table.size();
     std::unique_ptr<gq_adamw> o(new gq_adamw);
     o->all = merged(spans, false);
     o->written = merged(spans, true);

@@ -548,7 +548,8 @@ GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int
  *   param    n values of type param_dtype; grad: n values of grad_dtype, e.g. a slice of gq_fused_step's avg;
  *   master   n float32 values that are updated in the parameters' place, param receiving them rounded;
  *            NULL: none.  All tensors of a 16-bit type have one, or none has.
- *   These, and moments in 32 bits, need their type's alignment only; 16 bytes are faster.
+ *   These, and moments in 32 bits, need their type's alignment only.  Fastest are arrays that all begin equally far
+ *   behind 16-byte boundaries, in elements (slices of flat vectors at the same offset); with moments in 8 bits, on them.
  *   Tensors may share gradients; what a step writes may overlap nothing else that it reads or writes
  *   (GQ_ERR_INVALID).  n = 0 is allowed; pointers may then be NULL.
  * Calls on one optimizer must not overlap on the GPU, and must be made with its device current

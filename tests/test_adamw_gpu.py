@@ -17,7 +17,7 @@ HYPER = dict(lr=2e-3, beta1=0.9, beta2=0.999, eps=1e-8)
 class Case:
     """Tensors one after another in flat buffers, `gap` elements between them."""
 
-    def __init__(self, sizes, param, grad, master, bits, seed=1, gap=0, zero=False):
+    def __init__(self, sizes, param, grad, master, bits, seed=1, gap=0, zero=False, skew=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.sizes, self.bits = sizes, bits
         at, self.at = 0, []
@@ -31,6 +31,8 @@ class Case:
         if master:
             self.flat["master"] = 0.1 * r()
             self.flat["param"] = self.flat["master"].to(param)
+        if skew:  # the gradients begin elsewhere within 16 bytes
+            self.flat["grad"] = torch.cat([self.flat["grad"][:skew], self.flat["grad"]])[skew:]
         self.params, self.grads = self.views("param"), self.views("grad")
         self.masters = self.views("master") if master else None
         if bits == 32:
@@ -353,6 +355,37 @@ def test_refusals_that_need_an_optimizer():
         G.AdamW([x[::2] for x in c.params], c.grads, c.m, c.v, state_bits=8)
     with pytest.raises(G.GQError):
         G.AdamW([c.params[0], c.params[0]], [c.grads[0], c.grads[0]], [c.m[0], c.m[0]], [c.v[0], c.v[0]], state_bits=8)
+
+
+@pytest.mark.parametrize("param,grad,master", [(torch.float32, torch.float32, False), (torch.bfloat16, torch.bfloat16, True),
+                                               (torch.bfloat16, torch.float32, False), (torch.float32, torch.float16, False)])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_tensors_that_start_anywhere(param, grad, master, bits, skew):
+    """Every start within 32 bytes and every short length, pieces that end in a tensor's last elements, NaN between the
+    tensors: it reaches neither the norm nor the step, and what lies between stays as it is."""
+    sizes = [n for n in range(1, 20)] + [250, 251, 4093, 4096, 4099, 8189, 8192 + 5, 12000]
+    c = Case(sizes, param, grad, master, bits, seed=3 + skew, gap=3, skew=skew)
+    between = torch.ones(c.flat["param"].numel(), dtype=torch.bool, device="cuda")
+    for at, n in zip(c.at, sizes):
+        between[at:at + n] = False
+    for t in c.flat.values():
+        t[between] = float("nan")
+    out = torch.empty(2, device="cuda")
+    c.opt.norm(0.25, out)
+    norm = float(torch.cat([g.double() for g in c.grads]).square().sum().sqrt())
+    assert abs(float(out[0]) - norm) <= 2.0 ** -23 * norm
+    before, held = c.snapshot(), {k: t.clone() for k, t in c.flat.items()}
+    c.opt.step(**HYPER, step=5)
+    check_step(c, before, 5)
+    for k, t in c.flat.items():
+        assert torch.isnan(t[between]).all(), k
+    assert torch.equal(c.flat["grad"][~between], held["grad"][~between])
+    m, v = (torch.empty(sum(sizes), device="cuda") for _ in range(2))
+    c.opt.moments(m, v)
+    got = [c.moments(i) for i in range(len(sizes))]
+    for flat, k in ((m, 0), (v, 1)):
+        assert np.array_equal(flat.double().cpu().numpy(), np.concatenate([x[k] for x in got]))
 
 
 def test_elements_past_32_bits():
