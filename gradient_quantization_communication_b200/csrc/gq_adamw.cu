@@ -267,11 +267,12 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
 // elements 256 x 8 ahead: the way from an entry to its elements and back, which a block would wait for twice a chunk,
 // is otherwise most of its time (374 us without either, 206 with, 64 tensors of 1e6, bf16 parameters).
 // Blocks an SM: three, but two where 8-bit moments leave room for a float32 parameter's and gradient's elements on the
-// way only so (195 us against 211; with a bf16 parameter 178 against 157).
-constexpr int blocks_of(bool eight, int updated, int grad) { return eight && updated + grad == 8 ? 2 : 3; }
+// way only so (195 us against 211; with a bf16 parameter 178 against 157), or where loads that are shifted take more (64
+// x 1000001, bf16 parameters: 228 against 269).
+constexpr int blocks_of(bool eight, bool al, int updated, int grad) { return eight && (!al || updated + grad == 8) ? 2 : 3; }
 
 template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL>
-__global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof(P), sizeof(G))) k_adamw(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, AL, MASTER ? 4 : sizeof(P), sizeof(G))) k_adamw(const __grid_constant__ Params p)
 {
     using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
     constexpr int kWords = sizeof(AdamChunk) / 16;
@@ -291,12 +292,13 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, MASTER ? 4 : sizeof
     if (p.s.scalars) now = *p.s.scalars;
     __syncthreads();
     Loaded<S, G, EIGHT, AL> a;
+    auto whole = [](const AdamChunk &c, int base) { return AL && base + kChunk <= c.n && (EIGHT || base >= c.head); };
     auto fetch_elements = [&](Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (AL && base + kChunk <= c.n && (EIGHT || base >= c.head)) load<S, G, MASTER, EIGHT, AL, AL>(l, c, base, lane);
+        if (whole(c, base)) load<S, G, MASTER, EIGHT, AL, AL>(l, c, base, lane);
         else if (base < c.n) load<S, G, MASTER, EIGHT, AL, false>(l, c, base, lane);
     };
     auto work = [&](const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (AL && base + kChunk <= c.n && (EIGHT || base >= c.head)) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
+        if (whole(c, base)) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
         else if (base < c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, false>(p, l, c, now, scale, base, lane);
     };
     if (EIGHT) fetch_elements(a, entry[0], first);
