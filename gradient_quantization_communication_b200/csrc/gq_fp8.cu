@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(256) k_pack_rows(const __grid_constant__ Param
 // columns of them, so that a lane's 8 codes of a column are one 8-byte piece of the transpose.  A block loads, finds its
 // largest values, and stores, with barriers between: as many blocks an SM as registers allow hide that from one another
 // (16384 x 8192 bf16 both ways: 130 us with two blocks of 512 threads on 256 columns, 97 with three of these; with four
-// 103, and 187 against 148 where rows start anywhere, their registers spilled).
+// 103, their registers spilled).  Two where an element has 32 bits or rows start anywhere: a lane's loads take more
+// registers (16384 x 4095 bf16 in tiles both ways: 64 us with two, 77 with three).
 // ---------------------------------------------------------------------------------------------
 constexpr int kTileWarps = 8;
 
@@ -313,13 +314,14 @@ __device__ __forceinline__ void pack_tile(const Params &p, uint8_t *codes, uint8
 }
 
 template <typename T, int FMT, bool TILE, bool AL>
-__global__ void __launch_bounds__(kTileWarps * 32, sizeof(T) == 4 ? 2 : 3) k_pack_tile(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kTileWarps * 32, sizeof(T) == 4 || !AL ? 2 : 3) k_pack_tile(const __grid_constant__ Params p)
 {
     __shared__ __align__(16) uint8_t codes[kBlock * kBlock];  // transposed
     __shared__ uint8_t exps[kBlock];                          // of every column (TILE: the first, of all)
     const int64_t tile = blockIdx.x / p.per_row;
     const int base = (int)(blockIdx.x - tile * p.per_row) * kBlock;
-    if (AL && (tile + 1) * kBlock <= p.rows && base + kBlock <= p.cols) pack_tile<T, FMT, TILE, AL, AL>(p, codes, exps);
+    const bool whole = AL ? base + kBlock <= p.cols : base > 0 && base + kBlock + 8 <= p.cols;
+    if (whole && (tile + 1) * kBlock <= p.rows) pack_tile<T, FMT, TILE, AL, true>(p, codes, exps);
     else pack_tile<T, FMT, TILE, AL, false>(p, codes, exps);
 }
 
