@@ -34,7 +34,7 @@ constexpr int64_t kMaxElements = int64_t(1) << 40;
 gq_status_t check_device(const gq_adamw &o)
 {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
     return dev == o.device ? GQ_OK : GQ_ERR_INVALID;
 }
 
@@ -173,13 +173,13 @@ gq_status_t create(const gq_adamw_config_t &c, const gq_adamw_tensor_t *list, in
     o->memory = nullptr;
     const size_t bytes = table.size() * sizeof(AdamChunk);
     if (cudaGetDevice(&o->device) != cudaSuccess || cudaMalloc(&o->memory, bytes + kNormParts * sizeof(double)) != cudaSuccess)
-        return GQ_ERR_CUDA;
+        return cuda_failed();
     unsigned char *mem = static_cast<unsigned char *>(o->memory);
     // a copy from pageable memory may return before its last bytes have arrived, and steps run on any stream
     if (bytes && (cudaMemcpy(mem, table.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
                   cudaStreamSynchronize(nullptr) != cudaSuccess)) {
         cudaFree(o->memory);
-        return GQ_ERR_CUDA;
+        return cuda_failed();
     }
     o->a = AdamArgs{c.param_dtype, c.grad_dtype, c.state_bits, master, aligned_chunks, chunks, reinterpret_cast<AdamChunk *>(mem), c.seed};
     o->parts = reinterpret_cast<double *>(mem + bytes);

@@ -10,6 +10,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "gq_check.h"
 #include "gq_internal.h"
 
 struct gq_plan {
@@ -84,6 +85,9 @@ cudaError_t kernel_occupancy(const void *kern, int threads, size_t smem, int *pe
 }  // namespace gq
 
 namespace {
+
+using gq::cuda_failed;
+using gq::from_cuda;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -197,11 +201,9 @@ gq::KParams base_params(const gq_plan &pl, uint64_t step)
 gq_status_t check_device(const gq_plan &pl)
 {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
     return dev == pl.device ? GQ_OK : GQ_ERR_INVALID;
 }
-
-gq_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA; }
 
 // NVTX range around an entry point (free when no profiler is attached): shows the call on the
 // host timeline next to the kernels it enqueues.
@@ -260,7 +262,7 @@ gq_status_t gq_plan_create(const gq_config_t *cfg, gq_plan_t *out)
         if (pl->status) cudaFree(pl->status);
         if (pl->err_scratch) cudaFree(pl->err_scratch);
         delete pl;
-        return GQ_ERR_CUDA;
+        return cuda_failed();
     }
     *out = pl;
     return GQ_OK;
@@ -390,7 +392,7 @@ gq_status_t gq_quant_error(gq_plan_t plan, uint32_t worker, uint64_t step, const
     p.r[0] = const_cast<float *>(residual);  // read only in this mode
     double *part = plan->err_scratch;
     cudaError_t e = plan->cfg.bucket <= 512 ? gq::launch_warp_err(p, part, s) : gq::launch_cta_err(p, part, s);
-    if (e != cudaSuccess) return GQ_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_failed();
     return from_cuda(gq::launch_err_reduce(part, plan->nb, part + 3 * plan->nb, out, s));
 }
 
@@ -414,7 +416,7 @@ gq_status_t gq_plan_set_segments(gq_plan_t plan, const int64_t *offsets, int nse
         if (plan->seg_max) cudaFree(plan->seg_max);
         plan->seg_off = nullptr;
         plan->seg_max = nullptr;
-        return GQ_ERR_CUDA;
+        return cuda_failed();
     }
     plan->nseg = nseg;
     const int64_t cbytes = (plan->nb * (int64_t)plan->cfg.bucket * 2 / 8 + 15) / 16 * 16;
@@ -477,9 +479,9 @@ gq_status_t gq_plan_status(gq_plan_t plan, void *stream)
     if (!plan) return GQ_ERR_INVALID;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned int flags = 0;
-    if (cudaMemcpyAsync(&flags, plan->status, sizeof flags, cudaMemcpyDeviceToHost, s) != cudaSuccess) return GQ_ERR_CUDA;
-    if (cudaMemsetAsync(plan->status, 0, sizeof(unsigned int), s) != cudaSuccess) return GQ_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaMemcpyAsync(&flags, plan->status, sizeof flags, cudaMemcpyDeviceToHost, s) != cudaSuccess) return cuda_failed();
+    if (cudaMemsetAsync(plan->status, 0, sizeof(unsigned int), s) != cudaSuccess) return cuda_failed();
+    if (cudaStreamSynchronize(s) != cudaSuccess) return cuda_failed();
     if (flags & gq::kStatusTimeout) return GQ_ERR_TIMEOUT;
     if (flags & gq::kStatusNonFinite) return GQ_ERR_NONFINITE;
     return GQ_OK;

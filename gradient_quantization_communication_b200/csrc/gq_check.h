@@ -18,7 +18,14 @@ struct Range {
     ~Range() { nvtxRangePop(); }
 };
 
-inline gq_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA; }
+// A CUDA call's failure as a status.  The runtime keeps it as the thread's last error, which the next launch would report
+// as its own although its kernel runs: it is taken from there.
+inline gq_status_t cuda_failed()
+{
+    cudaGetLastError();
+    return GQ_ERR_CUDA;
+}
+inline gq_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? GQ_OK : cuda_failed(); }
 
 inline bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 

@@ -44,6 +44,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "gq_check.h"
 #include "gq_internal.h"
 
 namespace {
@@ -715,14 +716,14 @@ gq_status_t gq_elias_pack(const gq_config_t *cfg, const void *msg, void *emsg, v
     const size_t smem = sizeof(uint32_t) * kBktWarps * 32 * (size_t)(p.dw + 1);
     const int gc = bucket_grid(reinterpret_cast<const void *>(count), l.nb, smem);
     const int ge = bucket_grid(reinterpret_cast<const void *>(encode), l.nb, smem);
-    if (gc < 0 || ge < 0) return GQ_ERR_CUDA;
+    if (gc < 0 || ge < 0) return gq::cuda_failed();
     count<<<gc, kBktWarps * 32, smem, s>>>(p);
     k_tile_sums<<<(unsigned)p.ntiles, kScanThreads, 0, s>>>(p);
     k_scan_top<<<1, kScanThreads, 0, s>>>(p);
     k_scan_apply<<<(unsigned)p.ntiles, kScanThreads, 0, s>>>(p);
     const int64_t tab = l.nb * l.L;
     encode<<<ge, kBktWarps * 32, smem, s>>>(p, (int)(((tab + 3) & ~int64_t(3)) - tab));
-    return cudaGetLastError() == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return gq::from_cuda(cudaGetLastError());
 }
 
 gq_status_t gq_elias_unpack(const gq_config_t *cfg, const void *emsg, void *msg, void *stream)
@@ -744,7 +745,7 @@ gq_status_t gq_elias_unpack(const gq_config_t *cfg, const void *emsg, void *msg,
     auto decode = l.b == 2 ? k_decode<2> : l.b == 3 ? k_decode<3> : k_decode<4>;
     const size_t smem = sizeof(uint32_t) * kDecodeWarps * 32 * (size_t)(p.dw + 1);
     if (cudaFuncSetAttribute(decode, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return GQ_ERR_CUDA;
+        return gq::cuda_failed();
     int per_sm = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode, kDecodeWarps * 32, smem);
     if (per_sm < 1) per_sm = 1;
@@ -752,7 +753,7 @@ gq_status_t gq_elias_unpack(const gq_config_t *cfg, const void *emsg, void *msg,
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)sms * per_sm));
     decode<<<(unsigned)grid, kDecodeWarps * 32, smem, static_cast<cudaStream_t>(stream)>>>(
         p, reinterpret_cast<float *>(m + l.dense_levels_off), reinterpret_cast<uint32_t *>(m), pad);
-    return cudaGetLastError() == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return gq::from_cuda(cudaGetLastError());
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "gq_check.h"
 #include "gq_entropy.cuh"
 #include "gq_internal.h"
 
@@ -307,7 +308,7 @@ gq_status_t convert(const gq_config_t *cfg, const void *in, void *out, void *str
     case 9: e = pack ? launch<9, true>(p, cfg->bucket, s) : launch<9, false>(p, cfg->bucket, s); break;
     default: break;
     }
-    return e == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return gq::from_cuda(e);
 }
 
 struct Range {

@@ -26,6 +26,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "gq_check.h"
 #include "gq_internal.h"
 
 namespace {
@@ -59,15 +60,15 @@ gq_status_t current_context_id(unsigned long long *id)
         cudaDriverEntryPointQueryResult q1, q2;
         if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &f1, cudaEnableDefault, &q1) != cudaSuccess ||
             q1 != cudaDriverEntryPointSuccess || !f1)
-            return GQ_ERR_CUDA;
+            return gq::cuda_failed();
         if (cudaGetDriverEntryPoint("cuCtxGetId", &f2, cudaEnableDefault, &q2) != cudaSuccess ||
             q2 != cudaDriverEntryPointSuccess || !f2)
-            return GQ_ERR_CUDA;
+            return gq::cuda_failed();
         g_ctx_get_current = reinterpret_cast<CtxGetCurrentFn>(f1);
         g_ctx_get_id = reinterpret_cast<CtxGetIdFn>(f2);
     }
     CUcontext ctx = nullptr;
-    if (g_ctx_get_current(&ctx) != CUDA_SUCCESS || !ctx) return GQ_ERR_CUDA;
+    if (g_ctx_get_current(&ctx) != CUDA_SUCCESS || !ctx) return gq::cuda_failed();
     return g_ctx_get_id(ctx, id) == CUDA_SUCCESS ? GQ_OK : GQ_ERR_CUDA;
 }
 
@@ -85,7 +86,7 @@ gq_status_t scratch_address(int dev, unsigned char **out)
     if (st != GQ_OK) return st;
     if (g_scratch[dev].ctx_id != id || !g_scratch[dev].ptr) {
         void *p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return GQ_ERR_CUDA;
+        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return gq::cuda_failed();
         g_scratch[dev].ptr = static_cast<unsigned char *>(p);
         g_scratch[dev].ctx_id = id;
     }
@@ -112,19 +113,19 @@ extern "C" GQ_API gq_status_t gq_quant_error_noalloc(const gq_config_t *cfg, uin
     const int64_t nb = (c.n + c.bucket - 1) / c.bucket;
     if (nb > kMaxBuckets) return GQ_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (c.n == 0) return cudaMemsetAsync(out, 0, 3 * sizeof(double), s) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    if (c.n == 0) return gq::from_cuda(cudaMemsetAsync(out, 0, 3 * sizeof(double), s));
     if (!grad || !aligned16(grad)) return GQ_ERR_INVALID;
     if ((c.error_feedback != 0) != (residual != nullptr)) return GQ_ERR_INVALID;
     if (residual && !aligned16(residual)) return GQ_ERR_INVALID;
 
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return gq::cuda_failed();
     unsigned char *scratch = nullptr;
     const gq_status_t sa = scratch_address(dev, &scratch);
     if (sa != GQ_OK) return sa;
     unsigned int *status = reinterpret_cast<unsigned int *>(scratch);
     double *part = reinterpret_cast<double *>(scratch + kStatusBytes);
-    if (cudaMemsetAsync(status, 0, sizeof(unsigned int), s) != cudaSuccess) return GQ_ERR_CUDA;
+    if (cudaMemsetAsync(status, 0, sizeof(unsigned int), s) != cudaSuccess) return gq::cuda_failed();
 
     size_t msg_bytes = 0, codes_off = 0, levels_off = 0;
     if (gq_message_layout(&c, &msg_bytes, &codes_off, &levels_off) != GQ_OK) return GQ_ERR_INVALID;
@@ -161,8 +162,8 @@ extern "C" GQ_API gq_status_t gq_quant_error_noalloc(const gq_config_t *cfg, uin
     p.r[0] = const_cast<float *>(residual);  // read only in this mode
     p.status = status;
     cudaError_t e = c.bucket <= 512 ? gq::launch_warp_err(p, part, s) : gq::launch_cta_err(p, part, s);
-    if (e != cudaSuccess) return GQ_ERR_CUDA;
+    if (e != cudaSuccess) return gq::cuda_failed();
     // the reduction reads the status word: a kernel that stopped early (or saw a non-finite
     // value) makes all three outputs NaN
-    return gq::launch_err_reduce(part, nb, part + 3 * nb, out, s, status) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+    return gq::from_cuda(gq::launch_err_reduce(part, nb, part + 3 * nb, out, s, status));
 }
