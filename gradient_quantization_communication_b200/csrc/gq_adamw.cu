@@ -70,6 +70,29 @@ __device__ __forceinline__ uint32_t block_max(const float (&x)[8])
     return m;
 }
 
+// What a step does with moments in 8 bits: approximate root and quotient (FAST above) and, for beta1 above 17/18, the first
+// moment rounded stochastically.
+constexpr int kFast = 1, kSpread = 2;
+
+// Codes of 8 first moments under E, up with the probability that the remainder has: the 16 random bits of w's halves are a
+// fraction of a code's step.  From 2^-6 on the step is 2^-3 of the value's own power of two, and the sum's upper bits are the
+// code, as for the second moment below; under it the step is 2^-9, and values are counted in 2^-25.
+__device__ __forceinline__ uint2 spread_codes(const float (&m)[8], const uint32_t (&w)[4], uint32_t E)
+{
+    if (E == 255u) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    const float inv = fp8_inverse(E);
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t noise = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+        const float x = __fmul_rn(fabsf(m[j]), inv);
+        const uint32_t above = ((__float_as_uint(x) + noise * 16u) >> 20) - (120u << 3);
+        const uint32_t below = (__float2uint_rz(__fmul_rn(x, 0x1p25f)) + noise) >> 16;
+        q[j] = (x >= 0x1p-6f ? above : below) | (__float_as_uint(m[j]) >> 24 & 0x80u);
+    }
+    return make_uint2(pack_bytes(q[0], q[1], q[2], q[3]), pack_bytes(q[4], q[5], q[6], q[7]));
+}
+
 // The second moment's format (include/gq.h): 5 exponent and 3 mantissa bits of binary32, counted from 31 below E.
 __device__ __forceinline__ uint32_t square_exp(uint32_t bits)
 {
@@ -186,10 +209,11 @@ __device__ __forceinline__ void load(Loaded<S, G, EIGHT, AL> &l, const AdamChunk
 }
 
 // One warp's 256 elements from `base` of a chunk.
-template <typename P, typename S, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL, bool FULL>
+template <typename P, typename S, typename G, bool MASTER, bool EIGHT, int MODE, bool AL, bool FULL>
 __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c,
                                        const gq_adamw_scalars_t &now, float scale, int base, int lane)
 {
+    constexpr bool FAST = (MODE & kFast) != 0;
     const int n = c.n, at = base + lane * 8, head = EIGHT ? 0 : c.head;
     S *const param = updated<S, MASTER>(c);
     float x[8], g[8], m[8], v[8], beta1 = p.s.beta1;
@@ -235,15 +259,25 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
                 if (at + j >= n) m[j] = v[j] = 0.0f;
         }
         const uint32_t em = fp8_exp<GQ_FP8_E4M3>(block_max(m)), ev = square_exp(block_max(v));
-        const uint2 qm = fp8_codes8<GQ_FP8_E4M3>(m, em);
-        // Philox's counter (element / 8, step, tensor + 2^31)
+        // Philox's counter (element / 8, step, tensor + 2^31; for the first moment + 2^30 too)
         const uint64_t group = (uint64_t)(c.group + (at >> 3));
         const uint32_t c0 = (uint32_t)group, c2 = now.step;
         const unsigned long long p0 = (unsigned long long)0xD2511F53u * c0, p1 = (unsigned long long)0xCD9E8D57u * c2;
-        const uint4 d = philox_rounds_2_to_10((uint32_t)(p1 >> 32) ^ (uint32_t)(group >> 32) ^ p.rk0[0], (uint32_t)p1,
-                                              (uint32_t)(p0 >> 32) ^ (c.number | 0x80000000u) ^ p.rk1[0], (uint32_t)p0,
-                                              p.rk0 + 1, p.rk1 + 1);
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+        auto draw = [&](uint32_t which, uint32_t (&w)[4]) {
+            const uint4 d = philox_rounds_2_to_10((uint32_t)(p1 >> 32) ^ (uint32_t)(group >> 32) ^ p.rk0[0], (uint32_t)p1,
+                                                  (uint32_t)(p0 >> 32) ^ (c.number | which) ^ p.rk1[0], (uint32_t)p0,
+                                                  p.rk0 + 1, p.rk1 + 1);
+            w[0] = d.x; w[1] = d.y; w[2] = d.z; w[3] = d.w;
+        };
+        uint32_t w[4];
+        uint2 qm;
+        if constexpr ((MODE & kSpread) != 0) {
+            draw(0xc0000000u, w);
+            qm = spread_codes(m, w, em);
+        } else {
+            qm = fp8_codes8<GQ_FP8_E4M3>(m, em);
+        }
+        draw(0x80000000u, w);
         const uint2 qv = square_codes(v, w, ev);
         // whole blocks are written, the last one's codes past the tensor as 0
         if (FULL || base + (lane & 16) * 8 < n) {
@@ -271,7 +305,7 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
 // x 1000001, bf16 parameters: 228 against 269).
 constexpr int blocks_of(bool eight, bool al, int updated, int grad) { return eight && (!al || updated + grad == 8) ? 2 : 3; }
 
-template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL>
+template <typename P, typename G, bool MASTER, bool EIGHT, int MODE, bool AL>
 __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, AL, MASTER ? 4 : sizeof(P), sizeof(G))) k_adamw(const __grid_constant__ Params p)
 {
     using S = typename std::conditional<MASTER, float, P>::type;  // what is updated
@@ -298,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(EIGHT, AL, MASTER ? 4 : si
         else if (base < c.n) load<S, G, MASTER, EIGHT, AL, false>(l, c, base, lane);
     };
     auto work = [&](const Loaded<S, G, EIGHT, AL> &l, const AdamChunk &c, int base) {
-        if (whole(c, base)) update<P, S, G, MASTER, EIGHT, FAST, AL, AL>(p, l, c, now, scale, base, lane);
-        else if (base < c.n) update<P, S, G, MASTER, EIGHT, FAST, AL, false>(p, l, c, now, scale, base, lane);
+        if (whole(c, base)) update<P, S, G, MASTER, EIGHT, MODE, AL, AL>(p, l, c, now, scale, base, lane);
+        else if (base < c.n) update<P, S, G, MASTER, EIGHT, MODE, AL, false>(p, l, c, now, scale, base, lane);
     };
     if (EIGHT) fetch_elements(a, entry[0], first);
     for (int k = 0; i < p.chunks; i += step) {
@@ -506,11 +540,11 @@ cudaError_t launch_after(void (*kern)(A...), unsigned grid, cudaStream_t s, B...
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST, bool AL>
+template <typename P, typename G, bool MASTER, bool EIGHT, int MODE, bool AL>
 cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
 {
     if (chunks == 0) return cudaSuccess;
-    auto kern = k_adamw<P, G, MASTER, EIGHT, FAST, AL>;
+    auto kern = k_adamw<P, G, MASTER, EIGHT, MODE, AL>;
     int per_sm = 0, sms = 0;
     const cudaError_t e = kernel_occupancy(reinterpret_cast<const void *>(kern), kThreads, 0, &per_sm, &sms);
     if (e != cudaSuccess) return e;
@@ -520,17 +554,19 @@ cudaError_t launch_part(Params p, int64_t first, int64_t chunks, cudaStream_t s)
     const int64_t most = EIGHT ? (int64_t)per_sm * sms : chunks;
     return launch_after(kern, (unsigned)(chunks < most ? chunks : most), s, p);
 }
-template <typename P, typename G, bool MASTER, bool EIGHT, bool FAST>
+template <typename P, typename G, bool MASTER, bool EIGHT, int MODE>
 cudaError_t launch_parts(const AdamArgs &a, const Params &p, cudaStream_t s)
 {
-    const cudaError_t e = launch_part<P, G, MASTER, EIGHT, FAST, true>(p, 0, a.aligned, s);
-    return e != cudaSuccess ? e : launch_part<P, G, MASTER, EIGHT, FAST, false>(p, a.aligned, a.chunks - a.aligned, s);
+    const cudaError_t e = launch_part<P, G, MASTER, EIGHT, MODE, true>(p, 0, a.aligned, s);
+    return e != cudaSuccess ? e : launch_part<P, G, MASTER, EIGHT, MODE, false>(p, a.aligned, a.chunks - a.aligned, s);
 }
 template <typename P, typename G, bool MASTER>
 cudaError_t launch_state(const AdamArgs &a, const Params &p, cudaStream_t s)
 {
-    if (a.state_bits != 8) return launch_parts<P, G, MASTER, false, false>(a, p, s);
-    return p.s.fast ? launch_parts<P, G, MASTER, true, true>(a, p, s) : launch_parts<P, G, MASTER, true, false>(a, p, s);
+    if (a.state_bits != 8) return launch_parts<P, G, MASTER, false, 0>(a, p, s);
+    if (p.s.spread)
+        return p.s.fast ? launch_parts<P, G, MASTER, true, kSpread | kFast>(a, p, s) : launch_parts<P, G, MASTER, true, kSpread>(a, p, s);
+    return p.s.fast ? launch_parts<P, G, MASTER, true, kFast>(a, p, s) : launch_parts<P, G, MASTER, true, 0>(a, p, s);
 }
 template <typename P, typename G>
 cudaError_t launch_master(const AdamArgs &a, const Params &p, cudaStream_t s)

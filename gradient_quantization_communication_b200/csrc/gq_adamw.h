@@ -46,6 +46,7 @@ struct AdamStep {
     gq_adamw_scalars_t now;
     float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
     bool fast;  // eps so large that the root of a subnormal second moment vanishes beside it
+    bool spread;  // beta1 so near 1 that a first moment in 8 bits would stand still under rounding to nearest
     const float *scale;
     const gq_adamw_scalars_t *scalars;
 };

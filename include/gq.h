@@ -533,14 +533,19 @@ GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int
  * gq_adamw_layout bytes, 16-byte aligned: a code byte an element, padded to whole blocks of 128, then one
  * exponent byte a block, padded to a multiple of 16.  The step uses the moments as it computes them and
  * keeps them as follows:
- *   m  GQ_FP8_E4M3 codes and exponents exactly as gq_fp8_pack's blocks;
+ *   m  GQ_FP8_E4M3 codes and exponents as gq_fp8_pack's blocks.  For beta1 <= 17/18 it is rounded to nearest, exactly as
+ *      there: a gradient's change by less than half a code's step over 1 - beta1 may then not be seen by m where the
+ *      gradients have no noise.  For beta1 above 17/18 nearest values would keep m where it is for good (a step without a gradient takes
+ *      less off it than half a code's step, which is up to 1/18), and it is rounded stochastically: away from 0 with the probability
+ *      that its remainder has, sign kept;
  *   v  code 0: 0; code c > 0 under exponent E: (8 + c mod 8) * 2^(floor(c / 8) - 34 + E - 127).  E is the
  *      smallest with max v <= 1.875 * 2^(E - 127) over the block, in [32, 254]; E = 255: NaN (codes 0).
  *      v is rounded stochastically: up with the probability that its remainder has, from 16 random bits of
  *      Philox4x32-10 (nearest values would keep v where it is for good: it decays by 0.1 % a step, a
- *      code's step is 6 to 12 %).  Key: the seed.  Counter: (i / 8 low, high word; t; tensor's number in
- *      the list + 2^31) for element i of its tensor; element i takes bits 16 (i mod 2) .. of word
- *      (i mod 8) / 2, as a fraction of 2^16.  v > 0 keeps a code of at least 1.
+ *      code's step is 6 to 12 %).  v > 0 keeps a code of at least 1.
+ *   Random bits: key: the seed.  Counter: (i / 8 low, high word; t; tensor's number in the list + 2^31, for m
+ *   + 2^31 + 2^30) for element i of its tensor; element i takes bits 16 (i mod 2) .. of word (i mod 8) / 2, as a
+ *   fraction of 2^16 of its code's step; a remainder counts in whole 2^-16 of the step, cut off.
  * Zero bytes are moments of 0, as for a first step.
  *
  * The list of tensors is fixed by gq_adamw_create, which copies it to device memory that the optimizer owns
