@@ -44,7 +44,7 @@ __device__ __forceinline__ void sum2(Two a, Two b, float &x, float &y)
 // subnormal second moments as 0.  Only the parameter's own change, lr times something near 1, carries that error.  FAST is
 // taken where the moments are in 8 bits and instructions bound the kernel (206 us against 172 when it was built, 64 tensors
 // of 1e6, bf16 parameters and fp32 gradients), and eps is so large that a subnormal moment's root (below 2^-63) vanishes
-// beside it.
+// beside it, and beta1 no smaller than update() can join with a block's scale.
 template <bool FAST>
 __device__ __forceinline__ float root(float x)
 {
@@ -220,9 +220,9 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
     to_floats(in_place<S, AL>(l.x, param), x);
     to_floats(in_place<G, AL>(l.g, static_cast<const G *>(c.grad)), g);
     if constexpr (EIGHT) {
-        // the scale joins beta1 below: a power of two, so their product is exact
-        fp8_decode8<GQ_FP8_E4M3>(l.m, 1.0f, m);
-        beta1 = __fmul_rn(fp8_scale(l.em), beta1);
+        // FAST: the scale, a power of two and at least 2^-117, joins beta1, which is 0 or at least 2^-9: their product is exact
+        fp8_decode8<GQ_FP8_E4M3>(l.m, FAST ? 1.0f : fp8_scale(l.em), m);
+        if (FAST) beta1 = __fmul_rn(fp8_scale(l.em), beta1);
         square_values(l.v, l.ev, v);
     } else {
         to_floats(in_place<float, AL>(l.m[0], static_cast<const float *>(c.m)), m);

@@ -45,7 +45,7 @@ struct AdamArgs {
 struct AdamStep {
     gq_adamw_scalars_t now;
     float beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
-    bool fast;  // eps so large that the root of a subnormal second moment vanishes beside it
+    bool fast;  // eps so large that the root of a subnormal second moment vanishes beside it, beta1 0 or at least 2^-9
     bool spread;  // beta1 so near 1 that a first moment in 8 bits would stand still under rounding to nearest
     const float *scale;
     const gq_adamw_scalars_t *scalars;

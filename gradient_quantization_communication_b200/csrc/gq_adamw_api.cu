@@ -261,7 +261,7 @@ gq_status_t gq_adamw_step(gq_adamw_t opt, double lr, double beta1, double beta2,
     s.eps = (float)eps;
     // 2^-63 times inv2 at its largest, t = 1, is below 2^-24 eps; and with 2^64 times inv2 the divisor is below 2^126, whose
     // reciprocal would be subnormal
-    s.fast = eps >= 0x1p-39 / std::sqrt(1.0 - beta2) && eps <= 0x1p64;
+    s.fast = eps >= 0x1p-39 / std::sqrt(1.0 - beta2) && eps <= 0x1p64 && (s.beta1 == 0.0f || s.beta1 >= 0x1p-9f);
     // e4m3's widest step for its size: half of it is 1/18 of 1.125, which a tie at 17/18 still leaves for the even code below
     s.spread = (double)s.beta1 * 18.0 > 17.0;
     s.scale = scale;

@@ -190,3 +190,24 @@ def test_sparse_gradients(beta1):
         c.opt.moments(out)
         stored += float(out.double().sum())
     assert abs(stored / total - 1) <= 5 * sigma(steps, g.double().cpu().numpy()) + steps * 2.0 ** -19
+
+
+@pytest.mark.parametrize("eps", [1e-8, 0.5])
+@pytest.mark.parametrize("beta1", [0.0, 1.1 * 2.0 ** -20, 1.1 * 2.0 ** -12, 2.0 ** -9, 0.9])
+def test_small_beta1_on_the_smallest_moments(beta1, eps):
+    """m beta1 rounds once in binary32 where a block's scale times beta1 would be subnormal: parameters of 0 show m."""
+    n, nb = 1280, 10
+    c = Case([n], torch.float32, torch.float32, False, 8, zero=True)
+    codes = np.random.RandomState(3).randint(0, 127, n).astype(np.uint8)
+    exps = np.zeros(16, np.uint8)
+    exps[:nb] = 10 + np.arange(nb)
+    c.m[0].copy_(torch.from_numpy(np.concatenate([codes, exps])))
+    c.flat["grad"].zero_(), c.flat["param"].zero_()
+    p, g, m, v = c.snapshot()[0]
+    lr = 2.0 ** 120
+    c.opt.step(lr, beta1, 0.999, eps, 2)
+    _, m32, _ = O.adam_update(p, g, m, v, lr, beta1, 0.999, eps, 2, dtype=np.float32)
+    # m / eps, its product with lr / (1 - beta1^2), both factors rounded, and the approximate quotient
+    want = -lr / (1 - beta1 ** 2) * m32.astype(np.float64) / eps
+    got = c.params[0].double().cpu().numpy()
+    assert (np.abs(got - want) <= 8 * 2.0 ** -24 * np.abs(want)).all()
