@@ -346,7 +346,7 @@ __device__ __forceinline__ void unpack_item(const Params &p, T *out, int64_t row
     for (int u = 0; u < kAhead; ++u) {
         if (!FULL && u > 0 && base + u * kChunk >= p.cols) break;
         float v[8];
-        fp8_decode8<FMT>(q[u], fp8_scale(E[u]), v);
+        fp8_decode8<FMT>(q[u], fp8_scale_any(E[u]), v);
         saturate<T>(v);
         Words<T> w;
         from_floats(w, v);

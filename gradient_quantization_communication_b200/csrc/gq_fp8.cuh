@@ -45,8 +45,15 @@ __device__ __forceinline__ uint32_t fp8_exp(uint32_t abs_bits)
 }
 // 2^(127 - E), the factor of a block's values before rounding (E = 255: anything finite).
 __device__ __forceinline__ float fp8_inverse(uint32_t E) { return __uint_as_float((254u - min(E, 253u)) << 23); }
-// 2^(E - 127); infinity for E = 255, whose codes are NaN.
+// 2^(E - 127) of a block that packing or a step wrote: infinity for E = 255, whose codes are NaN, and 0 for E = 0, whose
+// codes are 0.
 __device__ __forceinline__ float fp8_scale(uint32_t E) { return __uint_as_float(E << 23); }
+// 2^(E - 127) of any block, whatever its codes; NaN for E = 255.  (AdamW's step takes the other one: with this one 64 tensors
+// of 1e6, bf16 with masters, take 201 us, not 186.)
+__device__ __forceinline__ float fp8_scale_any(uint32_t E)
+{
+    return __uint_as_float(E - 1u < 254u ? E << 23 : E == 0u ? 0x400000u : 0x7fffffffu);
+}
 
 // The codes of two values already scaled, a in the low byte: nearest, ties to even.
 template <int FMT>

@@ -482,7 +482,8 @@ GQ_API gq_status_t gq_layer_norm_backward(int dtype, int param_dtype, int64_t ro
  *   GQ_FP8_E4M3  4 exponent and 3 mantissa bits, largest 448, smallest 2^-9, NaN 0x7f and 0xff;
  *   GQ_FP8_E5M2  5 and 2, largest finite 57344, smallest 2^-16, infinities and NaN.
  * E is the smallest with max |x| <= 1.75 * 2^(8 or 15) * 2^(E - 127) over the block, at least 10; codes
- * are rounded to nearest, ties to even.  Every value is exact in bfloat16 and float32.  A block with a NaN
+ * are rounded to nearest, ties to even.  Every value under such an E is exact in bfloat16 and float32.  (Packed forms
+ * of other origin may have any E; what passes binary32 is infinite when unpacked.)  A block with a NaN
  * or an infinity has E = 255 and codes 0x7f.
  */
 typedef enum { GQ_FP8_E4M3 = 0, GQ_FP8_E5M2 = 1 } gq_fp8_t;
@@ -533,11 +534,12 @@ GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int
  * gq_adamw_layout bytes, 16-byte aligned: a code byte an element, padded to whole blocks of 128, then one
  * exponent byte a block, padded to a multiple of 16.  The step uses the moments as it computes them and
  * keeps them as follows:
- *   m  GQ_FP8_E4M3 codes and exponents as gq_fp8_pack's blocks.  For beta1 <= 17/18 it is rounded to nearest, exactly as
- *      there: a gradient's change by less than half a code's step over 1 - beta1 may then not be seen by m where the
- *      gradients have no noise.  For beta1 above 17/18 nearest values would keep m where it is for good (a step without a gradient takes
- *      less off it than half a code's step, which is up to 1/18), and it is rounded stochastically: away from 0 with the probability
- *      that its remainder has, sign kept;
+ *   m  GQ_FP8_E4M3 codes and exponents as gq_fp8_pack's blocks (a caller's own have E from 10 to 247, or all codes
+ *      0).  For beta1 <= 17/18 it is rounded to nearest, exactly as there: a gradient's change by less than half a
+ *      code's step over 1 - beta1 may then not be seen by m where the gradients have no noise.  For beta1 above 17/18
+ *      nearest values would keep m where it is for good (a step without a gradient takes less off it than half a
+ *      code's step, which is up to 1/18), and it is rounded stochastically: away from 0 with the probability that its
+ *      remainder has, sign kept;
  *   v  code 0: 0; code c > 0 under exponent E: (8 + c mod 8) * 2^(floor(c / 8) - 34 + E - 127).  E is the
  *      smallest with max v <= 1.875 * 2^(E - 127) over the block, in [32, 254]; E = 255: NaN (codes 0).
  *      v is rounded stochastically: up with the probability that its remainder has, from 16 random bits of
