@@ -484,7 +484,7 @@ GQ_API gq_status_t gq_layer_norm_backward(int dtype, int param_dtype, int64_t ro
  * E is the smallest with max |x| <= 1.75 * 2^(8 or 15) * 2^(E - 127) over the block, at least 10; codes
  * are rounded to nearest, ties to even.  Every value under such an E is exact in bfloat16 and float32.  (Packed forms
  * of other origin may have any E; what passes binary32 is infinite when unpacked.)  A block with a NaN
- * or an infinity has E = 255 and codes 0x7f.
+ * or an infinity has E = 255 and all its codes 0x7f, what pads a cut block among them.
  */
 typedef enum { GQ_FP8_E4M3 = 0, GQ_FP8_E5M2 = 1 } gq_fp8_t;
 GQ_API gq_status_t gq_fp8_layout(int tile, int64_t rows, int64_t cols, size_t *bytes, size_t *codes_off,

@@ -61,3 +61,28 @@ def test_product_under_every_exponent(fmt, m):
             want[:] = np.nan
         assert np.array_equal(np.isnan(got), np.isnan(want)), E
         assert np.array_equal(np.nan_to_num(got, nan=7.0), np.nan_to_num(want, nan=7.0)), E
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("rows,cols", [(5, 130), (200, 300), (129, 257)])
+def test_padding_of_a_block_without_a_value(fmt, tile, bad, rows, cols):
+    """All 128 codes of a block with E = 255 are 0x7f, its padding behind the matrix among them; other padding is 0."""
+    x = torch.randn(rows, cols, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    x[rows - 1, cols - 1] = bad
+    for src, buf_of in ((x, lambda p, t: p), (x.t(), lambda p, t: t)):
+        r, c = src.shape
+        p, t = (torch.full((G.gq_fp8_layout(*s, tile)[0],), 0xEE, dtype=torch.uint8, device="cuda") for s in ((rows, cols), (cols, rows)))
+        G.gq_fp8_pack(x, p, t, fmt=fmt, tile=tile)
+        got = buf_of(p, t).cpu().numpy()
+        pitch = O.pitches(c)[0]
+        codes = got[:r * pitch].reshape(r, pitch)
+        last = c // 128 * 128                             # the cut block
+        hit = np.zeros(r, bool)
+        hit[(r - 1) // 128 * 128 if tile else r - 1:] = True
+        assert (codes[hit, last:] == 0x7F).all() and (codes[~hit, c:] == 0).all()
+        want, exps = O.pack(src.cpu(), fmt, tile)
+        assert np.array_equal(codes, want)
+        off = O.layout(tile, r, c)[1]
+        assert np.array_equal(got[off:off + exps.size].reshape(exps.shape), exps)
