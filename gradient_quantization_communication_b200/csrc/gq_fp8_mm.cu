@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     using S = Shape<GROUP, TN>;
     extern __shared__ unsigned char raw_smem[];
     __shared__ Shared sh;
-    const uint32_t stages = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    const uint32_t stages = ring_start(smem_u32(raw_smem));
+    float *const part = reinterpret_cast<float *>(raw_smem + (stages - smem_u32(raw_smem)));  // a single CTA's, in the end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank(), leader = GROUP == 2 ? 0u : rank;  // whose barriers the MMAs go by
     const int pair_rank = GROUP == 2 ? (int)rank : 0;
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
             }
             if (GROUP == 1 && !ok) sh.failed = 1;
             if (count > 0) {
-                const Out<T, S> out(p, it, reinterpret_cast<float *>(raw_smem), x0, count, row, ok);
+                const Out<T, S> out(p, it, part, x0, count, row, ok);
                 if (kFirst == 0) {
                     tmem_begin16(cols, held[0]);
                     tmem_wait16(held[0]);
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(Shape<GROUP, TN>::kThreads, Shape<GROUP, TN>::
     else if (p.s.splits > 1) {
         Item it;
         item_of<GROUP>(p.s, blockIdx.x, 0, rank, it);
-        join_cluster<T, S>(p, it, sh, reinterpret_cast<float *>(raw_smem), rank);
+        join_cluster<T, S>(p, it, sh, part, rank);
     }
     if (warp == 1) {
         if constexpr (GROUP == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem));

@@ -29,6 +29,9 @@ struct Shape {
     static constexpr int kStageBytes = kWBytes + kXBytes;
     static constexpr int kStages = 229376 / kPerSm / kStageBytes < 8 ? 229376 / kPerSm / kStageBytes : 8;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+    // single CTAs: a part of a tile, binary32, in the stages' place once the last MMA has read them
+    static constexpr int kPartBytes = GROUP == 1 ? TN * 128 * 4 : 0;
+    static_assert(kPartBytes <= kStages * kStageBytes, "a part takes the stages' place");
     // TMEM: two accumulators, the second from column kSecond on (or at a tile's fewer tokens), then two buffers of
     // exponents (4 columns for 128 features, TN / 32 but at least 4 for the tokens)
     static constexpr int kExpCols = 4 + (TN > 128 ? 8 : 4);
@@ -39,6 +42,10 @@ struct Shape {
     // keeps until its cluster's join
     static_assert(kPerSm * kTmem <= 512 && (kPerSm == 1 || 3 * kSmemBytes > 232448), "TMEM");
 };
+// The stages' (and a part's) address in dynamic shared memory that begins at `base`: the 128-byte swizzle wants 1024 bytes, a
+// part's loads 16, and where dynamic shared memory begins behind the static is the toolchain's matter.
+GQ_TILES_FN constexpr uint32_t ring_start(uint32_t base) { return (base + 1023u) & ~1023u; }
+
 constexpr int kMostTokens = 256;
 using Pair = Shape<2, kMostTokens>;
 static_assert(Pair::kExps + 2 * Pair::kExpCols <= 512, "TMEM");
