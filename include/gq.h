@@ -511,9 +511,13 @@ GQ_API gq_status_t gq_fp8_unpack(int dtype, int format, int tile, int64_t rows, 
  *   accumulate 1 adds to y (float32 only: GQ_ERR_UNSUPPORTED otherwise), 0 overwrites it.
  *   workspace  device, at least gq_fp8_matmul_workspace bytes, 16-byte aligned; NULL if that is 0.  Its
  *              contents do not outlive the call.
- * m = 0 is a no-op; 1 <= n < 2^31, 1 <= k <= GQ_ACT_MAX_COLS.  Products are exact; sums are binary32, where
- * the tensor cores cut off instead of rounding over runs of up to 4096 columns (16384 where y has 16 bits,
- * whose own rounding is far coarser), and sums below 2^-126 may read as 0.  A row of y with a NaN block in its operands is NaN where the formula is.
+ * m = 0 is a no-op; 1 <= n < 2^31, 1 <= k <= GQ_ACT_MAX_COLS.  Products are exact; sums are binary32, and the tensor
+ * cores cut them off instead of rounding: of every 32 products and the sum so far what lies below 2^-25 of the
+ * largest one's power of two, then of their sum what lies below 2^-23.  Float32 results are summed so over runs of up
+ * to 4096 columns, which are added rounded: a run is off by at most 1.4e-4 of its largest partial sum (where one product
+ * outweighs all others; by less than 1e-6 where they are of about one size).  Where y has 16 bits runs have up to 16384
+ * columns, and four times that: beside half a step of y, 3.9e-3 in bfloat16, 4.9e-4 in float16.  Sums below 2^-126
+ * may read as 0.  A row of y with a NaN block in its operands is NaN where the formula is.
  */
 GQ_API gq_status_t gq_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k, size_t *bytes);
 GQ_API gq_status_t gq_fp8_matmul(int dtype, int64_t m, int64_t n, int64_t k, int format_a, int tile_a, const void *a,
