@@ -595,8 +595,9 @@ GQ_API gq_status_t gq_adamw_create(const gq_adamw_config_t *cfg, const gq_adamw_
 GQ_API gq_status_t gq_adamw_destroy(gq_adamw_t opt);
 
 /*
- * out[0] = sqrt of the sum of grad^2 over all tensors, out[1] = min(1, max_norm / out[0]) (1 for a norm of 0; NaN
- * if the norm is not finite), both summed in binary64 in a fixed order.  out: device, 2 floats, 4-byte aligned;
+ * out[0] = sqrt of the sum of grad^2 over all tensors, out[1] = min(1, max_norm / that) (1 for a norm of 0; NaN
+ * if a gradient is not finite), both in binary64, in a fixed order, and rounded: a norm beyond float32's largest
+ * value is infinite in out[0], while out[1] is still the quotient.  out: device, 2 floats, 4-byte aligned;
  * max_norm > 0 (infinity: only the check that the gradients are finite).
  */
 GQ_API gq_status_t gq_adamw_norm(gq_adamw_t opt, double max_norm, float *out, void *stream);

@@ -211,3 +211,14 @@ def test_small_beta1_on_the_smallest_moments(beta1, eps):
     want = -lr / (1 - beta1 ** 2) * m32.astype(np.float64) / eps
     got = c.params[0].double().cpu().numpy()
     assert (np.abs(got - want) <= 8 * 2.0 ** -24 * np.abs(want)).all()
+
+
+def test_norm_beyond_float32():
+    """The factor is taken from the norm in binary64, which passes float32's largest value here and reads as infinity."""
+    c = Case([300], torch.float32, torch.float32, False, 32)
+    c.flat["grad"].zero_()
+    c.grads[0][:2] = 3.0e38
+    out = torch.empty(2, device="cuda")
+    c.opt.norm(2.0 ** 100, out)
+    norm = np.sqrt(2.0) * f32(3.0e38)
+    assert np.isinf(float(out[0])) and abs(float(out[1]) - 2.0 ** 100 / norm) <= 2.0 ** -23 * 2.0 ** 100 / norm
