@@ -42,8 +42,8 @@ __device__ __forceinline__ void sum2(Two a, Two b, float &x, float &y)
 
 // The update's square root and quotient: rounded to nearest, or (FAST) off by up to 2 units in the last place each, and
 // subnormal second moments as 0.  Only the parameter's own change, lr times something near 1, carries that error.  FAST is
-// taken where the moments are in 8 bits and instructions bound the kernel (206 us against 172 when it was built, 64 tensors
-// of 1e6, bf16 parameters and fp32 gradients), and eps is so large that a subnormal moment's root (below 2^-63) vanishes
+// taken where the moments are in 8 bits and instructions bound the kernel (146 us with it, 202 without, 64 tensors of
+// 1e6, bf16 parameters and fp32 gradients), and eps is so large that a subnormal moment's root (below 2^-63) vanishes
 // beside it, and beta1 no smaller than update() can join with a block's scale.
 template <bool FAST>
 __device__ __forceinline__ float root(float x)
@@ -299,10 +299,10 @@ __device__ __forceinline__ void update(const Params &p, const Loaded<S, G, EIGHT
 
 // Blocks walk the table in strides of the grid.  Entries are fetched two chunks ahead, and with moments in 8 bits the
 // elements 256 x 8 ahead: the way from an entry to its elements and back, which a block would wait for twice a chunk,
-// is otherwise most of its time (374 us without either, 206 with, 64 tensors of 1e6, bf16 parameters).
+// is otherwise much of its time (244 us without either, 146 with, 64 tensors of 1e6, bf16 parameters).
 // Blocks an SM: three, but two where 8-bit moments leave room for a float32 parameter's and gradient's elements on the
-// way only so (195 us against 211; with a bf16 parameter 178 against 157), or where loads that are shifted take more (64
-// x 1000001, bf16 parameters: 228 against 269).
+// way only so (184 us against 206; with a bf16 parameter 168 against 146), or where loads that are shifted take more (64
+// x 1000001, bf16 parameters: 227 against 268).
 constexpr int blocks_of(bool eight, bool al, int updated, int grad) { return eight && (!al || updated + grad == 8) ? 2 : 3; }
 
 template <typename P, typename G, bool MASTER, bool EIGHT, int MODE, bool AL>

@@ -14,7 +14,7 @@
 //
 // Bounded for many tokens by the SMs' way to L2 and then by power: a stage of a pair's CTA is 32 KB for 512 cycles of
 // MMAs, and arrives after 650 (13.5 TB/s over all SMs); the tensor pipe is active 72 % of the time.  Measured in graphs of
-// ten calls, bf16: 8192 tokens, 4096 x 4096 99 us (2.77 PFLOP/s), 16384 tokens, 4096 x 16384 759 us (2.90, 89 % of twice
+// ten calls, bf16: 8192 tokens, 4096 x 4096 100 us (2.75 PFLOP/s), 16384 tokens, 4096 x 16384 757 us (2.90, 89 % of twice
 // the library's measured bf16 rate); in a long run of calls, under the power cap, some 2.3.  For few tokens by latency:
 // 16 tokens, 4096 x 4096 8.4 us, of which 1 us until the first copy is issued, 1.2 until it arrives, 1.1 for all stages, 1.2
 // for the sums' way out of TMEM and 2.7 for the cluster's join, where the weight's bytes would take 2.6.
