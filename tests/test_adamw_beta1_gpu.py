@@ -222,3 +222,32 @@ def test_norm_beyond_float32():
     c.opt.norm(2.0 ** 100, out)
     norm = np.sqrt(2.0) * f32(3.0e38)
     assert np.isinf(float(out[0])) and abs(float(out[1]) - 2.0 ** 100 / norm) <= 2.0 ** -23 * 2.0 ** 100 / norm
+
+
+def test_captured_step_above_the_border():
+    """A captured step draws anew at every replay: its step number is read when it runs."""
+    a, b = (Case([5000, 300, 77], torch.bfloat16, torch.float32, True, 8, seed=5) for _ in range(2))
+    scalars = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    h = dict(beta1=0.95, beta2=0.999, eps=1e-8)
+    b.opt.norm(0.5, torch.empty(2, device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.opt.step(lr=1.0, step=1, scalars=scalars, **h)
+    for step in (1, 2, 3):
+        a.opt.step(lr=1e-3 / step, step=step, **h)
+        scalars.copy_(G.gq_adamw_scalars(1e-3 / step, h["beta1"], h["beta2"], step))
+        graph.replay()
+        for x, y in zip([a.flat[k] for k in a.flat] + a.m + a.v, [b.flat[k] for k in b.flat] + b.m + b.v):
+            assert torch.equal(x, y), step
+
+
+def test_two_streams_above_the_border():
+    a, b = (Case([70000, 300, 8200], torch.float32, torch.float32, False, 8, seed=6) for _ in range(2))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for step in (1, 2, 3):
+        a.opt.step(**hyper(0.98), step=step)
+        b.opt.step(**hyper(0.98), step=step, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.flat["param"], b.flat["param"])
+    assert all(torch.equal(x, y) for x, y in zip(a.m + a.v, b.m + b.v))
