@@ -118,10 +118,10 @@ static void each_failure(const char *what, F body)
 
 int main()
 {
-    std::vector<float> mem(5 * 1024);
+    std::vector<float> mem(5 * 1200);
     const gq_adamw_config_t cfg = {GQ_FLOAT32, GQ_FLOAT32, 32, 1};
-    const gq_adamw_tensor_t t = {&mem[0], &mem[1024], nullptr, &mem[2048], &mem[3072], 1000, 0.0f, 1.0f};
-    float *const out = &mem[4096];
+    const gq_adamw_tensor_t t = {&mem[0], &mem[1200], nullptr, &mem[2400], &mem[3600], 1000, 0.0f, 1.0f};
+    float *const out = &mem[4800];
     alignas(16) static float spare[1000];
     // an optimizer made and destroyed: a failing cudaFree has freed its block here
     each_failure("gq_adamw_create", [&] {
